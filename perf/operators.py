@@ -134,6 +134,11 @@ def _pad_last(t, to):
     return t if t.shape[-1] == to else torch.cat([t, t.new_zeros(t.shape[:-1] + (to - t.shape[-1],))], -1)
 
 
+def _on(t, v):
+    """v as a tensor on t's device: a division by a Python number is a product with its rounded reciprocal there."""
+    return torch.full((), v, dtype=torch.float32, device=t.device)
+
+
 def _round_up(n, m):
     return -(-n // m) * m
 
@@ -157,7 +162,7 @@ def _to_fp8_blocks(w):
     """E4M3 codes [N, K] (uint8) and scales [N/128, K/128] of w, one scale for each 128 x 128 block."""
     N, K = w.shape
     b = w.float().view(N // 128, 128, K // 128, 128)
-    s = (b.abs().amax((1, 3)) / E4M3_MAX).clamp(min=1e-12)
+    s = (b.abs().amax((1, 3)) / _on(w, E4M3_MAX)).clamp(min=1e-12)
     q = (b / s[:, None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return q.view(N, K).view(torch.uint8), s
 
@@ -217,7 +222,7 @@ def _fp8_rounded(x, fmt="e4m3"):
     """What the FP8 codes of x stand for, groups of 128 along the last axis."""
     top, kind = (E4M3_MAX, torch.float8_e4m3fn) if fmt == "e4m3" else (E5M2_MAX, torch.float8_e5m2)
     b = x.float().unflatten(-1, (-1, 128))
-    s = (b.abs().amax(-1, keepdim=True) / top).clamp(min=1e-12)
+    s = (b.abs().amax(-1, keepdim=True) / _on(b, top)).clamp(min=1e-12)
     return ((b / s).clamp(-top, top).to(kind).float() * s).flatten(-2)
 
 
@@ -333,7 +338,7 @@ def _exact_fp8(x, fmt="e4m3"):
     v[:, :C] = x.double()
     v = v.view(-1, 128)
     top, bits, low = (448.0, 3, -6) if fmt == "e4m3" else (57344.0, 2, -14)
-    scale = torch.maximum((v.abs().max(1, keepdim=True).values / top).float(), torch.tensor(1e-12, device=x.device)).double()
+    scale = torch.maximum((v.abs().max(1, keepdim=True).values / _on(v, top).double()).float(), torch.tensor(1e-12, device=x.device)).double()
     y = (v / scale).float().double().clamp(-top, top)
     exp = torch.floor(torch.log2(y.abs().clamp(min=2.0 ** (low - 1)))).clamp(min=low)
     ulp = torch.exp2(exp - bits)
