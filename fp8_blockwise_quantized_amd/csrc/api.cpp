@@ -1,10 +1,10 @@
 // C-ABI entry points declared in include/fp8bq.h: validate, plan, launch on the caller's stream.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cstring>
 
 #include "../../include/fp8bq.h"
+#include "device.hpp"
 #include "launch.hpp"
 #include "optim.hpp"
 #include "plan.hpp"
@@ -12,43 +12,11 @@
 
 namespace fp8bq {
 
-constexpr int kMaxDevices = 64;
-// Per-device cache: 0 = unknown, 1 = gfx950, 2 = other architecture.  Benign races (all writers
-// store the same value).
-static std::atomic<int> g_dev_state[kMaxDevices];
-static std::atomic<int> g_dev_cus[kMaxDevices];
-
-// Returns kOk if the current device is a gfx950; fills *cus with its compute-unit count and *index
-// with its index (each if not null).
-static int current_device(int* cus, int* index = nullptr) {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
-    (void)hipGetLastError();
-    return kErrDevice;
-  }
-  int state = g_dev_state[dev].load(std::memory_order_relaxed);
-  if (state == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
-      (void)hipGetLastError();
-      return kErrDevice;
-    }
-    state = (std::strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : 2;
-    g_dev_cus[dev].store(prop.multiProcessorCount, std::memory_order_relaxed);
-    g_dev_state[dev].store(state, std::memory_order_relaxed);
-  }
-  if (cus) *cus = g_dev_cus[dev].load(std::memory_order_relaxed);
-  if (index) *index = dev;
-  return state == 1 ? kOk : kErrDevice;
-}
-
 static int cu_count_or_default() {
   int cus = 0;
   if (current_device(&cus) == kOk && cus > 0) return cus;
   return 256;
 }
-
-static int launched(hipError_t e) { return e == hipSuccess ? kOk : kErrLaunch; }
 
 static int run_gemm(const GemmArgs& g, void* stream) {
   const int cus = cu_count_or_default();

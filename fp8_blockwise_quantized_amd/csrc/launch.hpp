@@ -85,6 +85,21 @@ struct GemmDesc {
 
 hipError_t launch_gemm(int op, const GemmDesc& d, const GemmPlan& plan, void* ws, hipStream_t st);
 
+// Products grouped by expert (d: the stacked operands; for kOpWgrad d.K is the padded token count).
+struct GroupDesc {
+  const int64_t* offsets;
+  int experts;
+  int64_t tokens;
+};
+hipError_t launch_grouped_gemm(int op, const GemmDesc& d, const GroupDesc& g, const GemmPlan& plan, hipStream_t st);
+
+// Token-axis quantizer with groups that begin anew at each expert (qt [C, padded], st [padded/128][C]),
+// and, when q is non-null, the 1x128 row quantizer from the same read.
+hipError_t launch_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t ldx, const int64_t* offsets,
+                                int experts, int fr, uint8_t* q, int64_t ldq, float* s, int64_t lds, int fc,
+                                uint8_t* qt, int64_t ldqt, float* st_, int64_t ldst, int64_t padded, int cus,
+                                hipStream_t st);
+
 // Byte-matrix transpose: dst[c * ldd + r] = src[r * lds + c] for r < R, c < C (R, C multiples of 128).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t lds, uint8_t* dst, int64_t ldd, int64_t R, int64_t C,
                                hipStream_t st);

@@ -115,4 +115,43 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
   return p;
 }
 
+GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu_count) {
+  GemmPlan p;
+  const int64_t cus = cu_count > 0 ? cu_count : 256;
+  const int64_t used = T < E ? (T > 0 ? T : 1) : E;
+  const int64_t share = cdiv(T, used);
+  const int64_t rows = op == kOpWgrad ? N : share;
+  const int64_t cols = op == kOpFprop ? N : K;
+  const int64_t nkb = op == kOpWgrad ? cdiv(share, 128) : (op == kOpFprop ? K : N) / 128;
+  const int shapes[3] = {k256x256, k128x128, k64x64};
+  double best = 0.0;
+  for (int i = 0; i < 3; ++i) {
+    const int s = shapes[i];
+    const double units = (double)used * (double)cdiv(rows, tile_rows(s)) * (double)cdiv(cols, tile_cols(s));
+    const double slots = (double)(cus * blocks_per_cu(s));
+    const double full = (double)(int64_t)(units / slots);
+    const double frac = units / slots - full;
+    const double us = (full + (frac > 0.0 ? 0.5 * (1.0 + frac) : 0.0)) * (double)nkb * block_us(s);
+    if (i == 0 || us < best) {
+      best = us;
+      p.shape = s;
+    }
+  }
+  if (forced_shape() >= 0) p.shape = forced_shape();
+  p.tile_m = tile_rows(p.shape);
+  p.tile_n = tile_cols(p.shape);
+  p.tiles_n = cdiv(cols, p.tile_n);
+  p.tiles_m = op == kOpWgrad ? cdiv(N, p.tile_m) : T / p.tile_m + used;  // upper bound over the experts
+  const double units = (double)p.tiles_m * (double)p.tiles_n * (op == kOpWgrad ? (double)E : 1.0);
+  if (units >= 2147483647.0) {
+    p.fits = false;
+    return p;
+  }
+  p.units = (int64_t)units;
+  const int64_t slots = cus * blocks_per_cu(p.shape);
+  const int64_t g = slots >= 8 ? slots - slots % 8 : slots;
+  p.grid = p.units < g ? p.units : g;
+  return p;
+}
+
 }  // namespace fp8bq

@@ -51,4 +51,12 @@ struct GemmPlan {
 // dY[M,N] W[N,K]; wgrad: dW[N,K] = dY[M,N]^T X[M,K]).
 GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count);
 
+// Plan of a product grouped by expert: tile shape and persistent grid.  op is kOpFprop, kOpDgrad or
+// kOpWgrad; T tokens on E experts; N, K as in plan_gemm.  The tokens of each expert are known on the device
+// only, so the shape is chosen for equal shares and the grid covers the most tiles any shares can give.
+GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu_count);
+
+// Rows that hold T tokens with every expert's padded to whole 128-token blocks, whatever their shares.
+inline int64_t grouped_padded_rows(int64_t T, int64_t E) { return (T + 127 * (E < T ? E : T)) / 128 * 128; }
+
 }  // namespace fp8bq

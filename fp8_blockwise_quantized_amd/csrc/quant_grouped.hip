@@ -1,0 +1,164 @@
+// Token-axis quantizer of the products grouped by expert, with the row quantizer from the same read.
+//
+// wgrad contracts over the tokens of one expert, so its 128-token groups must begin at the expert's
+// first token.  Expert e's tokens are laid out from block P[e] on, P[e+1] = P[e] + ceil(n_e / 128): the
+// last block's missing tokens are zero codes, which add nothing.  Codes and scales are those of the
+// 128x1 quantizer on the expert's rows padded with zeros, and of the 1x128 quantizer, bit for bit.
+//
+// Bound by HBM (2 bytes read and 1 or 2 written per element).  A workgroup owns one 128-column group
+// and walks the 128-token blocks with a stride, so the table of experts is built once per workgroup and
+// not once per block.  Thread mapping and LDS layouts are those of the dense dual quantizer.
+#include "group_table.hpp"
+#include "launch.hpp"
+#include "quant_common.hpp"
+
+namespace fp8bq {
+
+template <typename TIn, int FR, int FC, bool ROWS>
+__global__ __launch_bounds__(256) void quant_grouped_kernel(const TIn* __restrict__ x, int64_t T, int64_t ldx,
+                                                            const int64_t* __restrict__ offsets, int E,
+                                                            uint8_t* __restrict__ q, int64_t ldq,
+                                                            float* __restrict__ s, int64_t lds,
+                                                            uint8_t* __restrict__ qt, int64_t ldqt,
+                                                            float* __restrict__ st, int64_t ldst, int64_t padded) {
+  __shared__ float red[16][kRedStride];
+  __shared__ __attribute__((aligned(16))) float ssc[kColPos];
+  __shared__ __attribute__((aligned(16))) float src[kColPos];
+  __shared__ __attribute__((aligned(16))) uint8_t tileT[kQtBytes];
+  __shared__ int rows[kMaxExperts + 1];
+  __shared__ uint32_t blocks[kMaxExperts + 1];
+
+  const int t = threadIdx.x;
+  const int lane = t & 63;
+  const int cc = t & 15;
+  const int rg = t >> 4;
+  const int64_t g = blockIdx.x;  // 128-column group
+  const int64_t c0 = g * kQtCols;
+  const int64_t col = c0 + 8 * cc;
+
+  if (t < 64) group_table_rows(offsets, E, T, kGroup, 1, rows, blocks, lane);
+  __syncthreads();
+  const uint32_t cap = (uint32_t)(padded / kGroup);
+  const uint32_t nblk = blocks[E] < cap ? blocks[E] : cap;
+
+  for (uint32_t rb = blockIdx.y; rb < nblk; rb += gridDim.y) {
+    const int e = group_find(blocks, E, rb, lane);
+    const int64_t r0 = rows[e] + (int64_t)(rb - blocks[e]) * kGroup;  // first token of the block
+    const int left = (int)(rows[e + 1] - r0);                        // tokens in it (128 if more)
+
+    float v[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      if (8 * rg + p < left) {
+        Load8<TIn>::run(x + (r0 + 8 * rg + p) * ldx + col, v[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+      }
+    }
+
+    if constexpr (ROWS) {
+      float m[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        m[p] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[p] = __builtin_fmaxf(m[p], __builtin_fabsf(v[p][i]));
+      }
+      const float sc_own = group_scale<FR>(row16_max_scatter<8>(m, cc));
+      const float rc_own = 1.0f / sc_own;
+      const int own = 8 * rg + (cc >> scatter_shift<8>());
+      if ((cc & 1) == 0 && own < left) s[g * lds + r0 + own] = sc_own;
+      static_for<8>([&](auto P) {
+        constexpr int p = decltype(P)::value;
+        const float sc = row16_bcast<(p << scatter_shift<8>())>(sc_own);
+        const float rc = row16_bcast<(p << scatter_shift<8>())>(rc_own);
+        if (8 * rg + p < left) store_codes8(q + (r0 + 8 * rg + p) * ldq + col, quant8<FR>(v[p], sc, rc));
+      });
+    }
+
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float m = __builtin_fabsf(v[0][i]);
+#pragma unroll
+      for (int p = 1; p < 8; ++p) m = __builtin_fmaxf(m, __builtin_fabsf(v[p][i]));
+      red[rg][col_pos(8 * cc + i)] = m;
+    }
+    __syncthreads();
+    if (t < kQtCols) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) m = __builtin_fmaxf(m, red[k][col_pos(t)]);
+      const float sc = group_scale<FC>(m);
+      ssc[col_pos(t)] = sc;
+      src[col_pos(t)] = 1.0f / sc;
+      st[rb * ldst + c0 + t] = sc;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = 8 * cc + i;
+      const float sc = ssc[col_pos(c)], rc = src[col_pos(c)];
+      float y[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) y[p] = blockwise_quotient(v[p][i], sc, rc);
+      const uint2 w = make_uint2(pack4<FC>(y[0], y[1], y[2], y[3]), pack4<FC>(y[4], y[5], y[6], y[7]));
+      *reinterpret_cast<uint2*>(tileT + qt_off(c, rg)) = w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+      const int c = (t >> 3) + 32 * pass;
+      const int ch = t & 7;
+      const uint4 codes = *reinterpret_cast<const uint4*>(tileT + qt_off(c, 2 * ch));
+      store_codes16(qt + (c0 + c) * ldqt + (int64_t)rb * kGroup + 16 * ch, codes);
+    }
+    __syncthreads();  // tileT and red are written again for the next block
+  }
+}
+
+template <typename TIn, int FR, int FC, bool ROWS>
+static hipError_t launch_t(const void* x, int64_t T, int64_t C, int64_t ldx, const int64_t* offsets, int E, uint8_t* q,
+                           int64_t ldq, float* s, int64_t lds, uint8_t* qt, int64_t ldqt, float* st_, int64_t ldst,
+                           int64_t padded, int cus, hipStream_t st) {
+  // about eight workgroups per CU (four resident), at most one per 128x128 tile
+  const int64_t ncg = C / kQtCols, nrb = padded / kGroup;
+  int64_t gy = (8 * (int64_t)cus + ncg - 1) / ncg;
+  gy = gy < nrb ? gy : nrb;
+  gy = gy < 65535 ? gy : 65535;
+  hipLaunchKernelGGL((quant_grouped_kernel<TIn, FR, FC, ROWS>), dim3((unsigned)ncg, (unsigned)gy), dim3(256), 0, st,
+                     (const TIn*)x, T, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_, ldst, padded);
+  return hipGetLastError();
+}
+
+template <typename TIn>
+static hipError_t launch_in(const void* x, int64_t T, int64_t C, int64_t ldx, const int64_t* offsets, int E, int fr,
+                            uint8_t* q, int64_t ldq, float* s, int64_t lds, int fc, uint8_t* qt, int64_t ldqt,
+                            float* st_, int64_t ldst, int64_t padded, int cus, hipStream_t st) {
+  if (q == nullptr)
+    return fc == kE4M3 ? launch_t<TIn, kE4M3, kE4M3, false>(x, T, C, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_,
+                                                             ldst, padded, cus, st)
+                       : launch_t<TIn, kE4M3, kE5M2, false>(x, T, C, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_,
+                                                             ldst, padded, cus, st);
+  if (fr == kE4M3)
+    return fc == kE4M3 ? launch_t<TIn, kE4M3, kE4M3, true>(x, T, C, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_,
+                                                            ldst, padded, cus, st)
+                       : launch_t<TIn, kE4M3, kE5M2, true>(x, T, C, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_,
+                                                            ldst, padded, cus, st);
+  return fc == kE4M3 ? launch_t<TIn, kE5M2, kE4M3, true>(x, T, C, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_, ldst,
+                                                          padded, cus, st)
+                     : launch_t<TIn, kE5M2, kE5M2, true>(x, T, C, ldx, offsets, E, q, ldq, s, lds, qt, ldqt, st_, ldst,
+                                                          padded, cus, st);
+}
+
+hipError_t launch_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t ldx, const int64_t* offsets,
+                                int experts, int fr, uint8_t* q, int64_t ldq, float* s, int64_t lds, int fc,
+                                uint8_t* qt, int64_t ldqt, float* st_, int64_t ldst, int64_t padded, int cus,
+                                hipStream_t st) {
+  return xt == 0 ? launch_in<uint16_t>(x, T, C, ldx, offsets, experts, fr, q, ldq, s, lds, fc, qt, ldqt, st_, ldst,
+                                       padded, cus, st)
+                 : launch_in<float>(x, T, C, ldx, offsets, experts, fr, q, ldq, s, lds, fc, qt, ldqt, st_, ldst,
+                                    padded, cus, st);
+}
+
+}  // namespace fp8bq

@@ -358,4 +358,110 @@ int validate_gemm(const GemmArgs& g, size_t ws_needed, bool* empty, bool* zero_f
   return kOk;
 }
 
+static bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
+
+int validate_grouped(const GroupedArgs& g, bool* empty, bool* zero_fill) {
+  *empty = false;
+  *zero_fill = false;
+  if (g.op < 0 || g.op > 2) return kErrShape;
+  if (!fmt_ok(g.fa) || !fmt_ok(g.fb)) return kErrFormat;
+  if (g.out_t != 0 && g.out_t != 1 && !(g.out_t == 2 && g.op == 2)) return kErrDtype;
+  const int64_t E = g.E, T = g.T, N = g.N, K = g.K;
+  if (E < 1 || E > kMaxGroupExperts || T < 0 || N < 0 || K < 0 || N % 128 != 0 || K % 128 != 0) return kErrShape;
+  if (g.op == 2 && T % 128 != 0) return kErrShape;
+  if (N == 0 || K == 0) {
+    // a zero width leaves nothing to write, but a zero contraction has no defined output rows
+    const bool none = g.op == 2 || T == 0 || (g.op == 0 ? N : K) == 0;
+    *empty = none;
+    return none ? kOk : kErrShape;
+  }
+  if (T == 0 && g.op != 2) {
+    *empty = true;
+    return kOk;
+  }
+  // token counts and stacked rows are 32-bit in the kernels, and scale offsets 32-bit byte offsets
+  const int64_t kRows = (int64_t)1 << 30;
+  if (T >= kRows || N >= kRows || K >= kRows || N > kRows / E || K > kRows / E) return kErrShape;
+  const int oes = g.out_t == 0 ? 2 : 4;
+  Mat qa, sa, qb, sb, out;
+  int64_t contraction;
+  if (g.op == 0) {  // X [T, K], W [E N, K] -> Y [T, N]
+    qa = Mat{g.qa, T, K, g.ldqa, 1};
+    sa = Mat{g.sa, K / 128, T, g.ldsa, 4};
+    qb = Mat{g.qb, E * N, K, g.ldqb, 1};
+    sb = Mat{g.sb, E * N / 128, K / 128, g.ldsb, 4};
+    out = Mat{g.out, T, N, g.ldout, oes};
+    contraction = K;
+  } else if (g.op == 1) {  // dY [T, N], W^T [K, E N] -> dX [T, K]
+    qa = Mat{g.qa, T, N, g.ldqa, 1};
+    sa = Mat{g.sa, N / 128, T, g.ldsa, 4};
+    qb = Mat{g.qb, K, E * N, g.ldqb, 1};
+    sb = Mat{g.sb, E * N / 128, K / 128, g.ldsb, 4};
+    out = Mat{g.out, T, K, g.ldout, oes};
+    contraction = N;
+  } else {  // dY^T [N, Tp], X^T [K, Tp] -> dW [E N, K]
+    qa = Mat{g.qa, N, T, g.ldqa, 1};
+    sa = Mat{g.sa, T / 128, N, g.ldsa, 4};
+    qb = Mat{g.qb, K, T, g.ldqb, 1};
+    sb = Mat{g.sb, T / 128, K, g.ldsb, 4};
+    out = Mat{g.out, E * N, K, g.ldout, oes};
+    contraction = T;
+  }
+  int st;
+  if (g.out == nullptr) return kErrNull;
+  if ((st = check_mat(out, true)) != kOk) return st;
+  if (contraction == 0) {
+    *zero_fill = true;
+    return kOk;
+  }
+  if (g.offsets == nullptr || g.qa == nullptr || g.sa == nullptr || g.qb == nullptr || g.sb == nullptr) return kErrNull;
+  if (!aligned8(g.offsets)) return kErrAlign;
+  if ((st = check_mat(qa, true)) != kOk) return st;
+  if ((st = check_mat(qb, true)) != kOk) return st;
+  // one tile of a code operand is reached through a 32-bit buffer range
+  const int64_t kSpan = (int64_t)1 << 32;
+  if (255 * qa.ld + contraction >= kSpan || 255 * qb.ld + contraction >= kSpan) return kErrLd;
+  if ((st = check_mat(sa, true)) != kOk) return st;
+  if ((st = check_mat(sb, g.op == 2)) != kOk) return st;
+  // fprop reaches the scale of weight block nb at byte 4 nb ldsb of a 32-bit range
+  if (g.op == 0 && sb.ld > (kSpan / 4 - 1) / sb.rows) return kErrLd;
+  const Mat off{g.offsets, 1, E + 1, E + 1, 8};
+  if (overlaps(out, qa) || overlaps(out, sa) || overlaps(out, qb) || overlaps(out, sb) || overlaps(out, off))
+    return kErrOverlap;
+  return kOk;
+}
+
+int validate_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t ldx, const void* offsets, int64_t E,
+                           int fr, const void* q, int64_t ldq, const void* s, int64_t lds, int fc, const void* qt,
+                           int64_t ldqt, const void* st, int64_t ldst, int64_t padded, int64_t padded_needed,
+                           bool* empty) {
+  *empty = false;
+  const bool rows = q != nullptr || s != nullptr;
+  if (in_esize(xt) == 0) return kErrDtype;
+  if ((rows && !fmt_ok(fr)) || !fmt_ok(fc)) return kErrFormat;
+  if (E < 1 || E > kMaxGroupExperts || T < 0 || C < 0 || C % 128 != 0) return kErrShape;
+  if (T >= ((int64_t)1 << 30) || padded % 128 != 0 || padded < padded_needed || padded >= ((int64_t)1 << 31) ||
+      C / 128 >= ((int64_t)1 << 31))
+    return kErrShape;
+  if (T == 0 || C == 0) {
+    *empty = true;
+    return kOk;
+  }
+  if (offsets == nullptr) return kErrNull;
+  if (!aligned8(offsets)) return kErrAlign;
+  const Mat mx{x, T, C, ldx, in_esize(xt)}, off{offsets, 1, E + 1, E + 1, 8};
+  const Mat mqt{qt, C, padded, ldqt, 1}, mst{st, padded / 128, C, ldst, 4};
+  const Mat mq{q, T, C, ldq, 1}, ms{s, C / 128, T, lds, 4};
+  int r;
+  if ((r = check_quant(mx, mqt, mst, true)) != kOk) return r;
+  if (overlaps(mqt, off) || overlaps(mst, off)) return kErrOverlap;
+  if (rows) {
+    if ((r = check_quant(mx, mq, ms, true)) != kOk) return r;
+    if (overlaps(mq, off) || overlaps(ms, off) || overlaps(mq, mqt) || overlaps(mq, mst) || overlaps(ms, mqt) ||
+        overlaps(ms, mst))
+      return kErrOverlap;
+  }
+  return kOk;
+}
+
 }  // namespace fp8bq

@@ -101,4 +101,24 @@ struct GemmArgs {
 // empty, so the result is all zeros.  ws_needed: bytes the plan needs.
 int validate_gemm(const GemmArgs& g, size_t ws_needed, bool* empty, bool* zero_fill);
 
+// Products grouped by expert.  op: 0 fprop, 1 dgrad, 2 wgrad; T: tokens (wgrad: padded tokens, a multiple of
+// 128); operand shapes as in include/fp8bq_grouped.h.  *empty: nothing to write.  *zero_fill (wgrad): no
+// tokens, so the result is all zeros.
+constexpr int kMaxGroupExperts = 512;
+struct GroupedArgs {
+  int op;
+  int64_t E, T, N, K;
+  const void* offsets;
+  const void* qa; int64_t ldqa; const void* sa; int64_t ldsa; int fa;
+  const void* qb; int64_t ldqb; const void* sb; int64_t ldsb; int fb;
+  const void* out; int out_t; int64_t ldout;
+};
+int validate_grouped(const GroupedArgs& g, bool* empty, bool* zero_fill);
+
+// Grouped token-axis quantizer, with the row quantizer when q or s is given (then both must be).
+int validate_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t ldx, const void* offsets, int64_t E,
+                           int fr, const void* q, int64_t ldq, const void* s, int64_t lds, int fc, const void* qt,
+                           int64_t ldqt, const void* st, int64_t ldst, int64_t padded, int64_t padded_needed,
+                           bool* empty);
+
 }  // namespace fp8bq
