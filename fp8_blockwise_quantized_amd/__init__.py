@@ -671,3 +671,10 @@ from .grouped import (MAX_EXPERTS, fp8bq_grouped_gemm_dgrad, fp8bq_grouped_gemm_
                       fp8bq_grouped_gemm_wgrad, fp8bq_grouped_padded_rows, fp8bq_quantize_act_grouped,
                       grouped_gemm_dgrad, grouped_gemm_fprop, grouped_gemm_wgrad, quantize_act_grouped_128x1,
                       quantize_act_grouped_dual)
+
+# the layer in microscaled 4-bit floating point (include/fp8bq_mx.h)
+from .mx import (fp8bq_gemm_mxfp4, fp8bq_gemm_mxfp4_workspace_size, fp8bq_grouped_gemm_mxfp4,  # noqa: E402,F401
+                 fp8bq_grouped_gemm_mxfp4_workspace_size, fp8bq_grouped_linear_mxfp4,
+                 fp8bq_grouped_linear_mxfp4_workspace_size, fp8bq_linear_mxfp4, fp8bq_linear_mxfp4_workspace_size,
+                 fp8bq_quantize_mxfp4, gemm_mxfp4, grouped_gemm_mxfp4, grouped_linear_mxfp4, linear_mxfp4,
+                 quantize_mxfp4, quantize_mxfp4_dual, quantize_mxfp4_t)

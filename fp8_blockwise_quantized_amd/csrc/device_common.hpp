@@ -17,6 +17,10 @@
 
 namespace fp8bq {
 
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
 constexpr int kGroup = 128;  // every scale block is 128 wide along its grouped axis
 
 enum Fmt : int { kE4M3 = 0, kE5M2 = 1 };

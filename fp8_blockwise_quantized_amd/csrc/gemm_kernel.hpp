@@ -32,9 +32,6 @@
 
 namespace fp8bq {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 
 // 16-byte chunk swizzle inside a 128-byte LDS row.  It depends on row % 16 only, so every 16-row
 // patch has the same per-lane read pattern (one pair of lane offsets serves all patches; the patch

@@ -100,6 +100,35 @@ hipError_t launch_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int
                                 uint8_t* qt, int64_t ldqt, float* st_, int64_t ldst, int64_t padded, int cus,
                                 hipStream_t st);
 
+// MXFP4 (4-bit codes in blocks of 32 with E8M0 scales): quantizer (row outputs q/s and transposed column
+// outputs qt/st, either pair may be null) and products C[m, n] = sum_k A[m, k] B[n, k].
+hipError_t launch_mx_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq,
+                           uint32_t* s, int64_t lds, uint8_t* qt, int64_t ldqt, uint32_t* st_, int64_t ldst,
+                           hipStream_t st);
+enum MxA : int { kMxBf16 = 0, kMxF32 = 1, kMxCodes = 2 };
+struct MxDesc {
+  const void* a;  // codes (lda bytes a row) with scale words sa, or BF16 / FP32 values (lda elements a row)
+  int64_t lda;
+  const uint32_t* sa;
+  int64_t ldsa;
+  int a_type;     // MxA
+  const uint8_t* b;
+  int64_t ldb;
+  const uint32_t* sb;
+  int64_t ldsb;
+  void* c;
+  int64_t ldc;
+  int out_t;      // 0: BF16, 1: FP32, 2: FP32 accumulated into
+  int64_t M, N, K;
+};
+// offsets null: one dense product.  Else A's rows are sorted by expert and B is stacked [experts N, K].
+struct MxGroups {
+  const int64_t* offsets;
+  int experts;
+};
+// Few rows: rows is the (expected) row count of one product, which picks the tile height.
+hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, int64_t rows, int cus, hipStream_t st);
+
 // Byte-matrix transpose: dst[c * ldd + r] = src[r * lds + c] for r < R, c < C (R, C multiples of 128).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t lds, uint8_t* dst, int64_t ldd, int64_t R, int64_t C,
                                hipStream_t st);

@@ -154,4 +154,15 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
   return p;
 }
 
+MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count) {
+  (void)N;
+  (void)K;
+  (void)cu_count;
+  MxPlan p;
+  const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
+  p.rows = cdiv(M, used);
+  p.fused = linear && p.rows <= 16;
+  return p;
+}
+
 }  // namespace fp8bq

@@ -59,4 +59,12 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
 // Rows that hold T tokens with every expert's padded to whole 128-token blocks, whatever their shares.
 inline int64_t grouped_padded_rows(int64_t T, int64_t E) { return (T + 127 * (E < T ? E : T)) / 128 * 128; }
 
+// Plan of an MXFP4 product (E == 0: dense; else M tokens grouped on E experts).  linear: A comes unquantized.
+struct MxPlan {
+  bool fused = false;  // A is quantized in the product's kernel (only with linear)
+  int64_t rows = 0;    // rows one product is expected to have
+  size_t ws = 0;       // workspace of the product itself
+};
+MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count);
+
 }  // namespace fp8bq

@@ -464,4 +464,99 @@ int validate_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t 
   return kOk;
 }
 
+int validate_mx_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, const void* q, int64_t ldq,
+                      const void* s, int64_t lds, const void* qt, int64_t ldqt, const void* st, int64_t ldst,
+                      bool* empty) {
+  *empty = false;
+  const bool rows = q != nullptr || s != nullptr, cols = qt != nullptr || st != nullptr;
+  if (in_esize(xt) == 0) return kErrDtype;
+  // row blocks need whole blocks of columns; column blocks are padded, but are stored per 8 columns
+  if (R < 0 || C < 0 || C % 8 != 0 || (rows && C % 32 != 0)) return kErrShape;
+  if (R == 0 || C == 0) {
+    *empty = true;
+    return kOk;
+  }
+  if (x == nullptr || (!rows && !cols)) return kErrNull;
+  const int64_t kMost = (int64_t)1 << 31;
+  if (R >= kMost || C >= kMost || (R / 128 + 1) * (C / 128 + 1) >= kMost) return kErrShape;  // tiles of one launch
+  const Mat mx{x, R, C, ldx, in_esize(xt)};
+  const Mat mq{q, R, C / 2, ldq, 1}, ms{s, (C + 127) / 128, R, lds, 4};
+  const Mat mqt{qt, C, (R + 31) / 32 * 16, ldqt, 1}, mst{st, (R + 127) / 128, C, ldst, 4};
+  int r;
+  if (rows) {
+    if ((r = check_quant(mx, mq, ms, false)) != kOk) return r;
+  }
+  if (cols) {
+    if ((r = check_quant(mx, mqt, mst, false)) != kOk) return r;
+  }
+  if (rows && cols && (overlaps(mq, mqt) || overlaps(mq, mst) || overlaps(ms, mqt) || overlaps(ms, mst)))
+    return kErrOverlap;
+  return kOk;
+}
+
+// The operands of an MXFP4 product as matrices: A (codes or values), its scales (codes only), B, its scales,
+// the output and the offsets (grouped only); absent ones have no rows.
+static void mx_mats(const MxArgs& g, Mat (&m)[6]) {
+  const int64_t rows_b = g.E ? g.E * g.N : g.N, kw = (g.K + 127) / 128;
+  const bool codes = g.a_type == 2;
+  m[0] = codes ? Mat{g.a, g.M, g.K / 2, g.lda, 1} : Mat{g.a, g.M, g.K, g.lda, g.a_type == 0 ? 2 : 4};
+  m[1] = Mat{g.sa, codes ? kw : 0, g.M, g.ldsa, 4};
+  m[2] = Mat{g.b, rows_b, g.K / 2, g.ldb, 1};
+  m[3] = Mat{g.sb, kw, rows_b, g.ldsb, 4};
+  m[4] = Mat{g.out, g.M, g.N, g.ldout, g.out_t == 0 ? 2 : 4};
+  m[5] = Mat{g.offsets, g.E ? 1 : 0, g.E + 1, g.E + 1, 8};
+}
+
+int validate_mx(const MxArgs& g, bool* empty, bool* zero_fill) {
+  *empty = false;
+  *zero_fill = false;
+  if (g.a_type < 0 || g.a_type > 2 || g.out_t < 0 || g.out_t > 2) return kErrDtype;
+  if (g.E < 0 || g.E > kMaxGroupExperts || g.M < 0 || g.N < 0 || g.K < 0 || g.K % 32 != 0) return kErrShape;
+  if (g.M == 0 || g.N == 0) {
+    *empty = true;
+    return kOk;
+  }
+  const int64_t kRows = (int64_t)1 << 30;
+  const int64_t copies = g.E ? g.E : 1;
+  if (g.M >= kRows || g.K >= kRows || g.N >= kRows / copies) return kErrShape;
+  // work units of one launch: tiles of at least 16 x 16, every expert with a started one of its own
+  if ((g.M / 16 + copies) * (g.N / 16 + 1) >= ((int64_t)1 << 31)) return kErrShape;
+  Mat m[6];
+  mx_mats(g, m);
+  int st;
+  if (g.out == nullptr) return kErrNull;
+  if ((st = check_mat(m[4], false)) != kOk) return st;
+  if (g.K == 0) {
+    if (g.E) return kErrShape;  // (which rows belong to an expert is not known on the host)
+    *zero_fill = true;
+    return kOk;
+  }
+  for (int i = 0; i < 6; ++i)
+    if (m[i].rows && m[i].p == nullptr) return kErrNull;
+  if (g.E && !aligned8(g.offsets)) return kErrAlign;
+  if ((st = check_mat(m[0], true)) != kOk) return st;
+  if ((st = check_mat(m[2], true)) != kOk) return st;
+  if (m[1].rows && (st = check_mat(m[1], false)) != kOk) return st;
+  if ((st = check_mat(m[3], false)) != kOk) return st;
+  // one tile of a code operand is reached through a 32-bit buffer range
+  const int64_t kSpan = (int64_t)1 << 32;
+  if ((m[1].rows && 255 * g.lda + g.K >= kSpan) || 255 * g.ldb + g.K >= kSpan) return kErrLd;
+  for (int i = 0; i < 6; ++i)
+    if (i != 4 && overlaps(m[4], m[i])) return kErrOverlap;
+  return kOk;
+}
+
+int check_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed) {
+  if (ws_needed == 0) return kOk;
+  if (ws == nullptr || ws_bytes < ws_needed) return kErrWorkspace;
+  if (!aligned16(ws)) return kErrAlign;
+  if (ws_needed >= (size_t)kMaxExtentBytes) return kErrShape;
+  const Mat w{ws, 1, (int64_t)ws_needed, (int64_t)ws_needed, 1};
+  Mat m[6];
+  mx_mats(g, m);
+  for (int i = 0; i < 6; ++i)
+    if (overlaps(w, m[i])) return kErrOverlap;
+  return kOk;
+}
+
 }  // namespace fp8bq

@@ -121,4 +121,21 @@ int validate_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t 
                            int64_t ldqt, const void* st, int64_t ldst, int64_t padded, int64_t padded_needed,
                            bool* empty);
 
+// MXFP4 (include/fp8bq_mx.h).  Scale words may have any leading dimension; packed codes are rows of K/2 bytes.
+int validate_mx_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, const void* q, int64_t ldq,
+                      const void* s, int64_t lds, const void* qt, int64_t ldqt, const void* st, int64_t ldst,
+                      bool* empty);
+// Products.  E == 0: dense, else grouped by expert (offsets; B stacked [E N, K]).  a_type: 0 BF16, 1 FP32
+// (ldqa in elements; no scales), 2 codes.  *zero_fill: K == 0.  ws_needed is checked by check_workspace.
+struct MxArgs {
+  int64_t E, M, N, K;
+  const void* offsets;
+  int a_type;
+  const void* a; int64_t lda; const void* sa; int64_t ldsa;
+  const void* b; int64_t ldb; const void* sb; int64_t ldsb;
+  const void* out; int out_t; int64_t ldout;
+};
+int validate_mx(const MxArgs& g, bool* empty, bool* zero_fill);
+int check_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed);
+
 }  // namespace fp8bq
