@@ -88,8 +88,8 @@ static int run_mx(const MxArgs& g, void* ws, size_t ws_bytes, void* stream) {
     d.a_type = kMxCodes;
   }
   const MxGroups grp{(const int64_t*)g.offsets, (int)g.E};
-  (void)plan;
-  return launched(launch_mx_skinny(d, grp, plan.rows, cus_plan, s));
+  if (plan.skinny) return launched(launch_mx_skinny(d, grp, plan.rows, cus_plan, s));
+  return launched(launch_mx_gemm(d, grp, plan, (uint8_t*)ws + space.codes + space.scales, s));
 }
 
 }  // namespace fp8bq

@@ -128,6 +128,8 @@ struct MxGroups {
 };
 // Few rows: rows is the (expected) row count of one product, which picks the tile height.
 hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, int64_t rows, int cus, hipStream_t st);
+// Many rows, A in codes; ws: p.ws bytes of partial sums.
+hipError_t launch_mx_gemm(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st);
 
 // Byte-matrix transpose: dst[c * ldd + r] = src[r * lds + c] for r < R, c < C (R, C multiples of 128).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t lds, uint8_t* dst, int64_t ldd, int64_t R, int64_t C,

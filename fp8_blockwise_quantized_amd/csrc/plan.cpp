@@ -154,14 +154,45 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
   return p;
 }
 
+// Time of one 256-long stage for one round of resident MXFP4 work units, in microseconds on MI355X.
+static double mx_stage_us(int shape) { return shape == k256x256 ? 1.3 : shape == k64x64 ? 0.7 : 0.9; }
+
 MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count) {
-  (void)N;
-  (void)K;
-  (void)cu_count;
   MxPlan p;
+  const int64_t cus = cu_count > 0 ? cu_count : 256;
   const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
   p.rows = cdiv(M, used);
   p.fused = linear && p.rows <= 16;
+  p.skinny = p.rows <= 64;
+  if (p.skinny) return p;
+  const int64_t nkb = cdiv(K, 256);
+  const int shapes[3] = {k256x256, k128x128, k64x64};
+  double best = 0.0;
+  for (int i = 0; i < 3; ++i) {
+    const int s = shapes[i];
+    const int64_t slots = cus * blocks_per_cu(s);
+    const double tiles = (double)used * (double)cdiv(p.rows, tile_rows(s)) * (double)cdiv(N, tile_cols(s));
+    for (int split = 1; split <= (E == 0 ? kMaxSplit : 1); ++split) {
+      if (split > 1 && nkb / split < 4) break;
+      const double rounds = tiles * split / (double)slots;
+      const double full = (double)(int64_t)rounds, frac = rounds - full;
+      double us = (full + (frac > 0.0 ? 0.5 * (1.0 + frac) : 0.0)) * ((double)nkb / split + 1.0) * mx_stage_us(s);
+      if (split > 1) us += 6.0 + (8.0 * split + 4.0) * (double)M * (double)N / 5.0e6;
+      if ((i == 0 && split == 1) || us < best * (split > 1 ? 0.97 : 1.0)) {
+        best = us;
+        p.shape = s;
+        p.split_k = split;
+      }
+    }
+  }
+  if (forced_shape() >= 0) p.shape = forced_shape();
+  p.tiles_n = cdiv(N, tile_cols(p.shape));
+  p.tiles_m = E == 0 ? cdiv(M, tile_rows(p.shape)) : M / tile_rows(p.shape) + used;
+  const int64_t units = p.tiles_m * p.tiles_n * p.split_k;  // (sizes are limited by the validation)
+  const int64_t slots = cus * blocks_per_cu(p.shape);
+  const int64_t g = slots >= 8 ? slots - slots % 8 : slots;
+  p.grid = units < g ? units : g;
+  p.ws = p.split_k > 1 ? (size_t)p.split_k * (size_t)M * (size_t)(cdiv(N, 4) * 4) * 4 : 0;
   return p;
 }
 

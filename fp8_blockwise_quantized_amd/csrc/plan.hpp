@@ -62,7 +62,12 @@ inline int64_t grouped_padded_rows(int64_t T, int64_t E) { return (T + 127 * (E 
 // Plan of an MXFP4 product (E == 0: dense; else M tokens grouped on E experts).  linear: A comes unquantized.
 struct MxPlan {
   bool fused = false;  // A is quantized in the product's kernel (only with linear)
+  bool skinny = true;  // few rows: the streaming kernel; else LDS tiles of the shape below
   int64_t rows = 0;    // rows one product is expected to have
+  int shape = k128x128;
+  int split_k = 1;
+  int64_t tiles_m = 0, tiles_n = 0;
+  int64_t grid = 0;
   size_t ws = 0;       // workspace of the product itself
 };
 MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count);
