@@ -270,7 +270,10 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   static_assert(SBM != kSbBlock128 || WTN <= 128, "a wave's columns must share one weight block");
   static_assert(SBM != kSbBlock128 || BN % kGroup == 0 || kGroup % BN == 0, "a narrow tile lies in one weight block");
   static_assert(NSTAGE >= 2 && NSTAGE * STAGE <= 160 * 1024, "LDS ring does not fit");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NSTAGE * STAGE];
+  // (the table of a grouped product lies in the same array: a second __shared__ object makes the compiler
+  // wait for every LDS-DMA load in flight before each LDS read)
+  constexpr bool GROUPED = GM != kGroupNone;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NSTAGE * STAGE + (GROUPED ? kGroupTableBytes : 0)];
 
   const int t = threadIdx.x;
   const int lane = t & 63;
@@ -281,10 +284,9 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   const uint32_t G = gridDim.x;
 
   // grouped: the table of unit counts and of row (or contraction block) starts per expert
-  constexpr bool GROUPED = GM != kGroupNone;
   using UnitT = std::conditional_t<GROUPED, GroupUnit, Unit>;
-  __shared__ uint32_t gunits[GROUPED ? kMaxExperts + 1 : 1];
-  __shared__ int gstarts[GROUPED ? kMaxExperts + 1 : 1];
+  uint32_t* gunits = reinterpret_cast<uint32_t*>(smem + NSTAGE * STAGE);
+  int* gstarts = reinterpret_cast<int*>(gunits + kMaxExperts + 1);
   uint32_t U = tiles_m * tiles_n * (uint32_t)nsplit;
   if constexpr (GROUPED) {
     if (wid == 0) {

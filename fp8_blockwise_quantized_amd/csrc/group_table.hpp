@@ -14,6 +14,7 @@ namespace fp8bq {
 
 constexpr int kMaxExperts = 512;
 constexpr int kExpertsPerLane = kMaxExperts / 64;
+constexpr int kGroupTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;  // unit counts and starts
 
 __device__ __forceinline__ uint32_t wave_scan_add(uint32_t v, int lane) {  // inclusive
 #pragma unroll

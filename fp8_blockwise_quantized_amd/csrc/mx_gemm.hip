@@ -9,14 +9,19 @@
 // patch reads for 8 MFMAs of 32 cycles, three quarters of the LDS bandwidth with eight waves.
 //
 // Layout.  A stage holds 256 values (128 bytes) of the tile's rows of A and B and the two scale words of each
-// row.  Tiles arrive by direct global->LDS loads into a ring of two stages; 16-byte chunks are XOR-swizzled by
-// row as in the FP8 kernel.  The MFMA's first operand is the B patch: lane l ends with row l % 32 of the A
-// patch and 16 of the B patch's 32 columns.  B patch rows are permuted so that those 16 are consecutive
-// (16 (l / 32) .. +15): the two lanes of an output row write 64 contiguous bytes of BF16.
+// row, and arrives by direct global->LDS loads into a ring of two stages; a stage's loads go out between the
+// last MFMAs of the stage whose slot it takes.  16-byte chunks are XOR-swizzled by row.  The MFMA's first operand
+// is the B patch: lane l ends with row l % 32 of the A patch and 16 of the B patch's 32 columns, B patch rows
+// being permuted so that those 16 are two runs of eight.
+// Measured alternatives (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3; this form 285 / 122 / 284):
+// loads all issued after the barrier 294 / 132 / 287; four stages of 128 values 304 / 128 / 295; 128 x 256 tiles, two
+// workgroups per CU 345 / 148 / 344.  Without the loads 8192^3 takes 228 us, without loads, barriers and
+// writes 217: the matrix pipes with the LDS reads they need are the larger part, at the clock the card's power
+// allows them.
 //
 // A lane's operand is block l / 32 of a 64-long step; it shifts the row's scale word by 8 (l / 32) once per
 // 128-long stretch, and the instruction's byte select (0 or 2) picks the step.  The words of a contraction's
-// last stretch are masked past the last block (zero bytes, 2^-127 on both sides: the product of whatever codes
+// last stretches are masked past the last block (zero bytes, 2^-127 on both sides: the product of whatever codes
 // lie there vanishes below FP32's range).
 //
 // Workgroups are persistent and the ring runs on across tiles, as in the FP8 kernel.
@@ -25,49 +30,64 @@
 
 namespace fp8bq {
 
-constexpr int kMxStage = 256;  // values per stage
-
-// B patch: MFMA row rho is tile row 16 ((rho / 4) % 2) + 4 (rho / 8) + rho % 4; rho of tile row n:
-__device__ __forceinline__ int mx_rho(int n) { return 8 * ((n >> 2) & 3) + 4 * ((n >> 4) & 1) + (n & 3); }
+// B patch: tile row n of MFMA row rho = 8 a + 4 h + b (lane half h, accumulators 4 a + b), so that a half holds
+// columns 8 h .. +7 and 16 + 8 h .. +7 of the patch; and the inverse.
 __device__ __forceinline__ int mx_row_of_rho(int rho) {
-  return 16 * ((rho >> 2) & 1) + 4 * (rho >> 3) + (rho & 3);
+  const int a = rho >> 3, h = (rho >> 2) & 1, b = rho & 3;
+  return 16 * (a >> 1) + 8 * h + 4 * (a & 1) + b;
+}
+__device__ __forceinline__ int mx_rho(int n) {
+  return 8 * (2 * ((n >> 4) & 1) + ((n >> 2) & 1)) + 4 * ((n >> 3) & 1) + (n & 3);
 }
 
-template <int BM, int BN, int NW>
+// LDS ring: NST stages of STEPS 64-long steps.
+template <int BM, int BN, int NW, int STEPS, int NST>
 struct MxTile {
-  static constexpr int kB = BM * 128;
-  static constexpr int kSA = (BM + BN) * 128;  // scale words [2][BM], then [2][BN]
-  static constexpr int kSB = kSA + 2 * BM * 4;
-  static constexpr int kStage = kSB + 2 * BN * 4;
-  static constexpr int kBlocks = 4 * 2 * kStage + 4 * 8 * kMaxExperts <= 160 * 1024 ? 4
-                                 : 2 * 2 * kStage + 2 * 8 * kMaxExperts <= 160 * 1024 ? 2 : 1;  // workgroups per CU
+  static constexpr int kRow = 32 * STEPS;  // bytes of a row in a stage
+  static constexpr int kB = BM * kRow;
+  static constexpr int kSA = (BM + BN) * kRow;  // per 128-long stretch: scale words of A's rows, then of B's
+  static constexpr int kStage = kSA + STEPS / 2 * (BM + BN) * 4;
+  static constexpr int kLds = NST * kStage + kGroupTableBytes;
+  static constexpr int kBlocks = 4 * kLds <= 160 * 1024 ? 4 : 2 * kLds <= 160 * 1024 ? 2 : 1;  // workgroups per CU
   // waves per SIMD that the launch bound keeps registers for
   static constexpr int kMinWaves = kBlocks * NW / 4;
+  static_assert(kLds <= 160 * 1024, "LDS ring does not fit");
 };
+// 16-byte chunk swizzle inside a row of 64 or 128 bytes: any 16 lanes of a fragment read (rows r .. r + 15, one
+// logical chunk) cover all 64 banks once.
+template <int STEPS>
+__device__ __forceinline__ int mx_swz(int row) {
+  return STEPS == 2 ? (row >> 2) & 3 : swz(row);
+}
 
-template <int BM, int BN, int WGM, int WGN, int OUT, bool GROUPED>
-__global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN>::kMinWaves)) void mx_gemm_kernel(
+template <int BM, int BN, int WGM, int WGN, int STEPS, int NST, int OUT, bool GROUPED>
+__global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NST>::kMinWaves)) void mx_gemm_kernel(
     MxDesc d, uint32_t tiles_m, uint32_t tiles_n, int nsplit, float* __restrict__ partial, int64_t ldp, int vec,
     GroupArgs<GROUPED ? kGroupRowsMode : kGroupNone> grp) {
   constexpr int NW = WGM * WGN;
-  using Tile = MxTile<BM, BN, NW>;
+  using Tile = MxTile<BM, BN, NW, STEPS, NST>;
   constexpr int WTM = BM / WGM, WTN = BN / WGN;
   constexpr int MI = WTM / 32, NI = WTN / 32;
-  constexpr int AL = BM / 8 / NW, BL = BN / 8 / NW;       // 1 KB code loads per wave and stage
-  constexpr int SJA = 2 * BM / 64, SJ = SJA + 2 * BN / 64;  // scale jobs of 64 words
-  constexpr int SL = SJ / NW;
+  constexpr int CH = 2 * STEPS;   // 16-byte chunks of a row
+  constexpr int RPL = 64 / CH;    // rows of a 1 KB code load
+  constexpr int AL = BM / RPL / NW, BL = BN / RPL / NW;  // code loads per wave and stage
+  constexpr int SJ = STEPS / 2 * (BM + BN) / 64;         // scale jobs of 64 words
+  constexpr int SL = SJ > NW ? SJ / NW : 1;              // (with fewer jobs than waves some are loaded twice)
   constexpr int LOADS = AL + BL + SL;
-  static_assert(SJ % NW == 0 && BM / 8 % NW == 0 && BN / 8 % NW == 0, "loads split evenly over the waves");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * Tile::kStage];
-  __shared__ uint32_t gunits[GROUPED ? kMaxExperts + 1 : 1];
-  __shared__ int gstarts[GROUPED ? kMaxExperts + 1 : 1];
+  static_assert((SJ % NW == 0 || NW % SJ == 0) && BM / RPL % NW == 0 && BN / RPL % NW == 0, "loads split evenly");
+  // (one array: a second __shared__ object makes the compiler wait for every LDS-DMA load in flight before
+  // each LDS read)
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * Tile::kStage + (GROUPED ? kGroupTableBytes : 0)];
+  uint32_t* gunits = reinterpret_cast<uint32_t*>(smem + NST * Tile::kStage);
+  int* gstarts = reinterpret_cast<int*>(gunits + kMaxExperts + 1);
 
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wid = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wid / WGN, wn = wid % WGN;
   const int nblk = (int)(d.K / kMxBlock);
-  const int nkb = (nblk + 7) / 8;
+  const int nwords = (nblk + 3) / 4;
+  const int nkb = (nblk + 2 * STEPS - 1) / (2 * STEPS);  // stages of the contraction
   const uint32_t G = gridDim.x;
   using UnitT = std::conditional_t<GROUPED, GroupUnit, Unit>;
   uint32_t U = tiles_m * tiles_n * (uint32_t)nsplit;
@@ -101,13 +121,15 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN>::kMinWave
   uint32_t aoff[AL], boff[BL], soff[SL];
   const uint32_t* sbase[SL];
   uint32_t sbytes[SL];
-  int64_t sld[SL];  // words between a job's stretches, and its stretch within the stage
+  // scale job j: stretch j / JS of the stage, the words of 64 rows, A's rows first
+  constexpr int JS = (BM + BN) / 64;
+  int64_t sld[SL];  // words between a job's stretches
   int sword[SL];
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
-    const int j = wid + NW * i;
-    sld[i] = j < SJA ? d.ldsa : d.ldsb;
-    sword[i] = j < SJA ? j / (BM / 64) : (j - SJA) / (BN / 64);
+    const int j = (wid + NW * i) % SJ;
+    sld[i] = j % JS < BM / 64 ? d.ldsa : d.ldsb;
+    sword[i] = j / JS;
   }
   auto set_sources = [&](const UnitT& u) {
     abase = (const uint8_t*)d.a + (int64_t)u.m0 * d.lda;
@@ -117,46 +139,38 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN>::kMinWave
     bbytes = sat32((nleft < BN - 1 ? nleft : BN - 1) * d.ldb + d.K / 2);
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
-      const int row = 8 * (wid + NW * i) + (lane >> 3);
+      const int row = RPL * (wid + NW * i) + lane / CH;
       const int64_t r = row < mleft ? row : mleft;
-      aoff[i] = (uint32_t)(r * d.lda) + (uint32_t)(((lane & 7) ^ swz(row)) * 16);
+      aoff[i] = (uint32_t)(r * d.lda) + (uint32_t)(((lane % CH) ^ mx_swz<STEPS>(row)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
-      const int row = 8 * (wid + NW * i) + (lane >> 3);
+      const int row = RPL * (wid + NW * i) + lane / CH;
       const int64_t r = row < nleft ? row : nleft;
-      boff[i] = (uint32_t)(r * d.ldb) + (uint32_t)(((lane & 7) ^ swz(mx_rho(row))) * 16);
+      boff[i] = (uint32_t)(r * d.ldb) + (uint32_t)(((lane % CH) ^ mx_swz<STEPS>(mx_rho(row))) * 16);
     }
-    // scale job j: word p of 64 rows; p = j / (rows / 64) within A's jobs, then B's
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
-      const int j = wid + NW * i;
-      if (j < SJA) {
-        const int64_t r = 64 * (j % (BM / 64)) + lane;
-        soff[i] = (uint32_t)((r < mleft ? r : mleft) * 4);
-        sbase[i] = d.sa + u.m0;
-        sbytes[i] = (uint32_t)((mleft < BM - 1 ? mleft : BM - 1) * 4 + 4);
-      } else {
-        const int64_t r = 64 * ((j - SJA) % (BN / 64)) + lane;
-        soff[i] = (uint32_t)((r < nleft ? r : nleft) * 4);
-        sbase[i] = d.sb + u.n0;
-        sbytes[i] = (uint32_t)((nleft < BN - 1 ? nleft : BN - 1) * 4 + 4);
-      }
+      const int j = (wid + NW * i) % SJ % JS;
+      const bool a = j < BM / 64;
+      const int64_t r = 64 * (a ? j : j - BM / 64) + lane, left = a ? mleft : nleft, most = (a ? BM : BN) - 1;
+      soff[i] = (uint32_t)((r < left ? r : left) * 4);
+      sbase[i] = a ? d.sa + u.m0 : d.sb + u.n0;
+      sbytes[i] = (uint32_t)((left < most ? left : most) * 4 + 4);
     }
   };
-  const int nwords = (nblk + 3) / 4;
   auto issue_load = [&](int i, uint8_t* stg) {
     if (i < AL) {
-      dma16(rsrc_of(abase + (int64_t)lkb * 128, abytes - (uint32_t)lkb * 128), aoff[i], stg + (wid + NW * i) * 1024);
+      dma16(rsrc_of(abase + (int64_t)lkb * Tile::kRow, abytes - (uint32_t)(lkb * Tile::kRow)), aoff[i], stg + (wid + NW * i) * 1024);
     } else if (i < AL + BL) {
-      dma16(rsrc_of(bbase + (int64_t)lkb * 128, bbytes - (uint32_t)lkb * 128), boff[i - AL],
+      dma16(rsrc_of(bbase + (int64_t)lkb * Tile::kRow, bbytes - (uint32_t)(lkb * Tile::kRow)), boff[i - AL],
             stg + Tile::kB + (wid + NW * (i - AL)) * 1024);
     } else {
       const int q = i - AL - BL;
-      const int word = 2 * lkb + sword[q];
-      const bool in = word < nwords;  // (past the last word: zeros)
+      const int word = STEPS / 2 * lkb + sword[q];
+      const bool in = STEPS == 2 || word < nwords;  // (past the last word: zeros)
       dma4(rsrc_of(sbase[q] + (in ? word : 0) * sld[q], in ? sbytes[q] : 0u), soff[q],
-           stg + Tile::kSA + 256 * (wid + NW * q));
+           stg + Tile::kSA + 256 * ((wid + NW * q) % SJ));
     }
   };
   auto advance = [&]() {
@@ -184,29 +198,37 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN>::kMinWave
   int ckb = C.kb0;
   const int r32 = lane & 31, h = lane >> 5;
   const int arow = wm * WTM + r32, brow = wn * WTN + mx_row_of_rho(r32);
-  const int asw = swz(r32), bsw = swz(r32);  // (swz reads row % 16; patch rows start at multiples of 32)
+  const int sw = mx_swz<STEPS>(r32);  // (patches start at multiples of 32 rows)
   auto aread = [&](const uint8_t* stg, int i, int step) {
-    return *reinterpret_cast<const v4i*>(stg + (arow + 32 * i) * 128 + (((2 * step + h) ^ asw) << 4));
+    return *reinterpret_cast<const v4i*>(stg + (arow + 32 * i) * Tile::kRow + (((2 * step + h) ^ sw) << 4));
   };
   auto bread = [&](const uint8_t* stg, int j, int step) {
-    return *reinterpret_cast<const v4i*>(stg + Tile::kB + (brow + 32 * j) * 128 + (((2 * step + h) ^ bsw) << 4));
+    return *reinterpret_cast<const v4i*>(stg + Tile::kB + (brow + 32 * j) * Tile::kRow + (((2 * step + h) ^ sw) << 4));
   };
-  auto sread = [&](const uint8_t* stg, int p, uint32_t (&sa)[MI], uint32_t (&sb)[NI]) {
-    const uint32_t* wa = reinterpret_cast<const uint32_t*>(stg + Tile::kSA) + p * BM + arow;
-    const uint32_t* wb = reinterpret_cast<const uint32_t*>(stg + Tile::kSB) + p * BN + brow;
+  v4i fa[2][MI], fb[2][NI];  // operands of the current and the next step
+  uint32_t sa[MI], sb[NI];   // scale words as read, and with the lane's bytes in place
+  uint32_t ua[MI], ub[NI];
+  auto read_step = [&](const uint8_t* stg, int step, int to) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = wa[32 * i];
+    for (int i = 0; i < MI; ++i) fa[to][i] = aread(stg, i, step);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) sb[j] = wb[32 * j];
+    for (int j = 0; j < NI; ++j) fb[to][j] = bread(stg, j, step);
+  };
+  auto read_scales = [&](const uint8_t* stg, int p) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(stg + Tile::kSA) + p * (BM + BN);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i] = w[arow + 32 * i];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) sb[j] = w[BM + brow + 32 * j];
   };
   // keep the bytes of existing blocks and bring the lane's two to bytes 0 and 2
-  auto smask = [&](int kb, int p, uint32_t (&sa)[MI], uint32_t (&sb)[NI]) {
-    const int left = nblk - 8 * kb - 4 * p;
+  auto place_scales = [&](int kb, int p) {
+    const int left = nblk - 2 * STEPS * kb - 4 * p;
     const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = (sa[i] & mask) >> (8 * h);
+    for (int i = 0; i < MI; ++i) ua[i] = (sa[i] & mask) >> (8 * h);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) sb[j] = (sb[j] & mask) >> (8 * h);
+    for (int j = 0; j < NI; ++j) ub[j] = (sb[j] & mask) >> (8 * h);
   };
 
   v16f acc[MI][NI];
@@ -218,56 +240,47 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN>::kMinWave
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   set_sources(L);
-  load_stage(smem);
-  load_stage(smem + Tile::kStage);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LOADS) : "memory");
-  v4i fa[2][MI], fb[2][NI];
-  uint32_t sa[2][MI], sb[2][NI];
 #pragma unroll
-  for (int i = 0; i < MI; ++i) fa[0][i] = aread(smem, i, 0);
-#pragma unroll
-  for (int j = 0; j < NI; ++j) fb[0][j] = bread(smem, j, 0);
-  sread(smem, 0, sa[0], sb[0]);
+  for (int s = 0; s < NST; ++s) load_stage(smem + s * Tile::kStage);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NST - 1) * LOADS) : "memory");
+  read_step(smem, 0, 0);
+  read_scales(smem, 0);
 
   int rd = 0;
   while (true) {
     uint8_t* stage = smem + rd * Tile::kStage;
-    uint8_t* nstage = smem + (rd ^ 1) * Tile::kStage;
+    const int nx = rd + 1 == NST ? 0 : rd + 1;
+    const uint8_t* nstage = smem + nx * Tile::kStage;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int cur = s & 1, nxt = cur ^ 1, p = s >> 1;
-      if (s == 0 || s == 2) smask(ckb, p, sa[p], sb[p]);
-      if (s < 3) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) fa[nxt][i] = aread(stage, i, s + 1);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) fb[nxt][j] = bread(stage, j, s + 1);
-        if (s == 1) sread(stage, 1, sa[1], sb[1]);
+    for (int s = 0; s < STEPS; ++s) {
+      if (s % 2 == 0) place_scales(ckb, s / 2);
+      if (s < STEPS - 1) {
+        read_step(stage, s + 1, (s + 1) & 1);
+        if (s % 2 == 1) read_scales(stage, (s + 1) / 2);
       } else {
-        // everything this wave needs of the stage is in registers; the next stage has landed
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) issue_load(i, stage);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) fa[nxt][i] = aread(nstage, i, 0);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) fb[nxt][j] = bread(nstage, j, 0);
-        sread(nstage, 0, sa[0], sb[0]);
+        // everything this wave needs of the stage is in registers and the next stage has landed; after the
+        // barrier that holds for all waves, and the slot takes the stage NST ahead
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NST - 2) * LOADS) : "memory");
+        read_step(nstage, 0, 0);
+        read_scales(nstage, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int u = 0; u < MI * NI; ++u) {
+        const int i = u / NI, j = u % NI;
+        if (s % 2)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(fb[1][j]), mx_operand(fa[1][i]),
+                                                                      acc[i][j], 4, 4, 2, (int)ub[j], 2, (int)ua[i]);
+        else
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(fb[0][j]), mx_operand(fa[0][i]),
+                                                                      acc[i][j], 4, 4, 0, (int)ub[j], 0, (int)ua[i]);
+        if (s == STEPS - 1) {
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          if (s & 1)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(fb[cur][j]), mx_operand(fa[cur][i]),
-                                                                        acc[i][j], 4, 4, 2, (int)sb[p][j], 2,
-                                                                        (int)sa[p][i]);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(fb[cur][j]), mx_operand(fa[cur][i]),
-                                                                        acc[i][j], 4, 4, 0, (int)sb[p][j], 0,
-                                                                        (int)sa[p][i]);
+          for (int l = u * LOADS / (MI * NI); l < (u + 1) * LOADS / (MI * NI); ++l) issue_load(l, stage);
+          __builtin_amdgcn_sched_barrier(0);
         }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     // keep the MFMAs in the step sequence (not sunk past the cursor update's branches)
@@ -276,56 +289,80 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN>::kMinWave
 #pragma unroll
       for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
     advance();
-    rd ^= 1;
+    rd = nx;
     if (++ckb < C.kb1) continue;
 
-    // unit finished: write the tile or its partial sum.  Lane l: row l % 32 of each A patch, columns
-    // 16 (l / 32) .. +15 of each B patch.
+    // unit finished: write the tile or its partial sum.  Lane l: row l % 32 of each A patch; accumulators
+    // 8 r .. 8 r + 7 (r = 0, 1) are columns 16 r + 8 (l / 32) .. +7 of each B patch.
     {
       const int64_t mlim = m_end(C), nlim = n_end(C);
-      const int64_t m = (int64_t)C.m0 + arow;
+      const int64_t m = (int64_t)C.m0 + arow, n0 = (int64_t)C.n0 + wn * WTN + 8 * h;
       int64_t ccol = 0;
       if constexpr (GROUPED) ccol = C.ccol;
+      const bool full = vec && (int64_t)C.m0 + BM <= mlim && (int64_t)C.n0 + BN <= nlim;
+      if (nsplit > 1 || OUT != 0) {
+        const int64_t ldo = nsplit > 1 ? ldp : d.ldc;
+        float* o = (nsplit > 1 ? partial + (int64_t)C.split * d.M * ldp : reinterpret_cast<float*>(d.c)) + m * ldo + n0 + ccol;
+        const bool add = OUT == 2 && nsplit == 1;
+        if (full) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int64_t row = m + 32 * i;
-        if (row >= mlim) continue;
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          const int64_t n = (int64_t)C.n0 + wn * WTN + 32 * j + 16 * h;
-          const v16f& v = acc[i][j];
-          const int64_t left = nlim - n;
-          if (left <= 0) continue;
-          if (nsplit > 1 || OUT != 0) {
-            float* o = nsplit > 1 ? partial + ((int64_t)C.split * d.M + row) * ldp + n
-                                  : reinterpret_cast<float*>(d.c) + row * d.ldc + n + ccol;
-            if (left >= 16 && (nsplit > 1 || vec)) {
+            for (int j = 0; j < NI; ++j)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                v4f w = {v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
-                v4f* o4 = reinterpret_cast<v4f*>(o) + r;
-                if (OUT == 2 && nsplit == 1) w = *o4 + w;
+                v4f w = {acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+                v4f* o4 = reinterpret_cast<v4f*>(o + 32 * i * ldo + 32 * j + 16 * (r >> 1) + 4 * (r & 1));
+                if (add) w = *o4 + w;
                 *o4 = w;
               }
-            } else {
+        } else {
 #pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (r < left) o[r] = (OUT == 2 && nsplit == 1) ? o[r] + v[r] : v[r];
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const int64_t c = 32 * j + 16 * (r >> 3) + (r & 7);
+                float* p = o + 32 * i * ldo + c;
+                if (m + 32 * i < mlim && n0 + c < nlim) *p = add ? *p + acc[i][j][r] : acc[i][j][r];
+              }
+        }
+      } else {
+        uint16_t* o = reinterpret_cast<uint16_t*>(d.c) + m * d.ldc + n0 + ccol;
+        if (full) {
+          // a lane's two 16-byte chunks of a patch row: lanes l and l + 16 swap one, so that a store instruction
+          // writes 64 contiguous bytes of 16 rows (four lanes each) and not 32 of 32 rows
+          uint16_t* s0 = reinterpret_cast<uint16_t*>(d.c) +
+                         ((int64_t)C.m0 + wm * WTM + (lane & 15)) * d.ldc + n0 + ccol + (lane & 16);
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+              const v16f& v = acc[i][j];
+              uint32_t x[4], y[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const auto p = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[2 * r], v[2 * r + 1]),
+                                                                pack_bf16x2(v[8 + 2 * r], v[9 + 2 * r]), false, false);
+                x[r] = p[0];
+                y[r] = p[1];
+              }
+              uint16_t* s = s0 + 32 * i * d.ldc + 32 * j;
+              *reinterpret_cast<uint4*>(s) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(s + 16 * d.ldc) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-          } else {
-            uint16_t* o = reinterpret_cast<uint16_t*>(d.c) + row * d.ldc + n + ccol;
-            uint32_t w[8];
+        } else {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) w[r] = pack_bf16x2(v[2 * r], v[2 * r + 1]);
-            if (left >= 16 && vec) {
-              *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (r < left) o[r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
-            }
-          }
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const int64_t c = 32 * j + 16 * (r >> 3) + (r & 7);
+                if (m + 32 * i < mlim && n0 + c < nlim)
+                  o[32 * i * d.ldc + c] = (uint16_t)pack_bf16x2(acc[i][j][r], 0.0f);
+              }
         }
       }
 #pragma unroll
@@ -374,16 +411,16 @@ __global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict_
   }
 }
 
-template <int BM, int BN, int WGM, int WGN, int OUT>
+template <int BM, int BN, int WGM, int WGN, int STEPS, int NST, int OUT>
 static hipError_t launch_tile(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, int vec,
                               hipStream_t st) {
   const int64_t ldp = (d.N + 3) / 4 * 4;
   if (grp.offsets)
-    hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, OUT, true>), dim3((unsigned)p.grid), dim3(WGM * WGN * 64), 0,
+    hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, STEPS, NST, OUT, true>), dim3((unsigned)p.grid), dim3(WGM * WGN * 64), 0,
                        st, d, (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, 1, (float*)nullptr, ldp, vec,
                        GroupArgs<kGroupRowsMode>{grp.offsets, grp.experts, d.M});
   else
-    hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, OUT, false>), dim3((unsigned)p.grid), dim3(WGM * WGN * 64), 0,
+    hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, STEPS, NST, OUT, false>), dim3((unsigned)p.grid), dim3(WGM * WGN * 64), 0,
                        st, d, (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, p.split_k, (float*)ws, ldp, vec,
                        GroupArgs<kGroupNone>{});
   return hipGetLastError();
@@ -391,12 +428,12 @@ static hipError_t launch_tile(const MxDesc& d, const MxGroups& grp, const MxPlan
 
 template <int OUT>
 static hipError_t launch_out(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st) {
-  const int vec = (d.ldc * (OUT == 0 ? 2 : 4)) % 16 == 0;
+  const int vec = p.split_k > 1 || (d.ldc * (OUT == 0 ? 2 : 4)) % 16 == 0;
   hipError_t e;
   switch (p.shape) {
-    case k256x256: e = launch_tile<256, 256, 2, 4, OUT>(d, grp, p, ws, vec, st); break;
-    case k64x64: e = launch_tile<64, 64, 2, 2, OUT>(d, grp, p, ws, vec, st); break;
-    default: e = launch_tile<128, 128, 2, 2, OUT>(d, grp, p, ws, vec, st); break;
+    case k256x256: e = launch_tile<256, 256, 2, 4, 4, 2, OUT>(d, grp, p, ws, vec, st); break;
+    case k64x64: e = launch_tile<64, 64, 2, 2, 4, 2, OUT>(d, grp, p, ws, vec, st); break;
+    default: e = launch_tile<128, 128, 2, 2, 4, 2, OUT>(d, grp, p, ws, vec, st); break;
   }
   if (e != hipSuccess || p.split_k <= 1) return e;
   const int64_t ldp = (d.N + 3) / 4 * 4;
