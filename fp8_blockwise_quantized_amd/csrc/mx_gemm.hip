@@ -322,10 +322,19 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const int64_t c = 32 * j + 16 * (r >> 3) + (r & 7);
+              for (int r = 0; r < 4; ++r) {
+                const int64_t c = 32 * j + 16 * (r >> 1) + 4 * (r & 1);
                 float* p = o + 32 * i * ldo + c;
-                if (m + 32 * i < mlim && n0 + c < nlim) *p = add ? *p + acc[i][j][r] : acc[i][j][r];
+                if (m + 32 * i >= mlim || n0 + c >= nlim) continue;
+                if (vec && n0 + c + 4 <= nlim) {
+                  v4f w = {acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+                  if (add) w = *reinterpret_cast<v4f*>(p) + w;
+                  *reinterpret_cast<v4f*>(p) = w;
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    if (n0 + c + k < nlim) p[k] = add ? p[k] + acc[i][j][4 * r + k] : acc[i][j][4 * r + k];
+                }
               }
         }
       } else {
@@ -358,10 +367,20 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const int64_t c = 32 * j + 16 * (r >> 3) + (r & 7);
-                if (m + 32 * i < mlim && n0 + c < nlim)
-                  o[32 * i * d.ldc + c] = (uint16_t)pack_bf16x2(acc[i][j][r], 0.0f);
+              for (int r = 0; r < 2; ++r) {
+                const int64_t c = 32 * j + 16 * r;
+                uint16_t* p = o + 32 * i * d.ldc + c;
+                if (m + 32 * i >= mlim || n0 + c >= nlim) continue;
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(acc[i][j][8 * r + 2 * k], acc[i][j][8 * r + 2 * k + 1]);
+                if (vec && n0 + c + 8 <= nlim) {
+                  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    if (n0 + c + k < nlim) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+                }
               }
         }
       }

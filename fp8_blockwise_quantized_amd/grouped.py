@@ -23,8 +23,9 @@ Rows of y and dx that belong to no expert are left as they are (undefined in a t
 
 import torch
 
-from . import (_F32, _HI, _U8, E4M3, OUT_F32_ACCUM, _c_i64, _c_int, _c_vp, _entry, _expect_all, _in_type, _ld,
-               _out_type, _pad4, _ptr, _RESTYPES, _SIGS, _stream, lib)
+from . import (E4M3, IN_BF16, IN_F32, OUT_BF16, OUT_F32, OUT_F32_ACCUM, _c_i64, _c_int, _c_vp, _entry, _pad4, _RESTYPES,
+               _SIGS, lib)
+from ._marshal import F32, HI, U8, experts, matrix, stacked, stream
 
 MAX_EXPERTS = 512
 
@@ -40,79 +41,77 @@ _SIGS.update({
 })
 _RESTYPES["fp8bq_grouped_padded_rows"] = _c_i64
 
-_I64 = (torch.int64,)
-
 
 def fp8bq_grouped_padded_rows(T, E):
     return int(lib().fp8bq_grouped_padded_rows(int(T), int(E)))
 
 
-def _experts(offsets):
-    """The number of experts E of an offsets tensor of E + 1 entries."""
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be a 1-D tensor of E + 1 entries")
-    if not offsets.is_contiguous():
-        raise ValueError("offsets must be contiguous")
-    return offsets.numel() - 1
-
-
-def _stacked(rows, E, what):
-    if rows % E:
-        raise ValueError(f"{what}: {rows} stacked rows do not split over {E} experts")
-    return rows // E
+def _out(t, accumulate=False):
+    return OUT_F32_ACCUM if accumulate else OUT_BF16 if t.dtype == torch.bfloat16 else OUT_F32
 
 
 @_entry
 def fp8bq_quantize_act_grouped(x, offsets, fmt_rows, q, s, fmt_cols, qt, st):
     T, C = x.shape
-    E = _experts(offsets)
+    dev = x.device
+    op, E = experts(offsets, dev)
     padded = qt.shape[1]
-    _expect_all([(x, "x", (T, C), _HI), (offsets, "offsets", (E + 1,), _I64), (q, "q", (T, C), _U8),
-                 (s, "s", (C // 128, T), _F32), (qt, "qt", (C, padded), _U8),
-                 (st, "st", (padded // 128, C), _F32)])
-    return (_ptr(x), _in_type(x), T, C, _ld(x), _ptr(offsets), E, fmt_rows, _ptr(q), _ld(q) if q is not None else 0,
-            _ptr(s), _ld(s) if s is not None else 0, fmt_cols, _ptr(qt), _ld(qt), _ptr(st), _ld(st), padded, _stream(x))
+    xp, ldx = matrix(x, "x", (T, C), HI, dev)
+    qp, ldq = matrix(q, "q", (T, C), U8, dev)
+    sp, lds = matrix(s, "s", (C // 128, T), F32, dev)
+    qtp, ldqt = matrix(qt, "qt", (C, padded), U8, dev)
+    stp, ldst = matrix(st, "st", (padded // 128, C), F32, dev)
+    return (xp, IN_BF16 if x.dtype == torch.bfloat16 else IN_F32, T, C, ldx, op, E, fmt_rows, qp, ldq, sp, lds, fmt_cols,
+            qtp, ldqt, stp, ldst, padded, stream(dev))
 
 
 @_entry
 def fp8bq_grouped_gemm_fprop(qx, sx, fx, offsets, qw, sw, fw, y):
     T, K = qx.shape
-    E = _experts(offsets)
-    N = _stacked(qw.shape[0], E, "qw")
-    _expect_all([(qx, "qx", (T, K), _U8), (sx, "sx", (K // 128, T), _F32), (offsets, "offsets", (E + 1,), _I64),
-                 (qw, "qw", (E * N, K), _U8), (sw, "sw", (E * N // 128, K // 128), _F32), (y, "y", (T, N), _HI)])
-    return (E, T, N, K, _ptr(offsets), _ptr(qx), _ld(qx), _ptr(sx), _ld(sx), fx, _ptr(qw), _ld(qw), _ptr(sw), _ld(sw),
-            fw, _ptr(y), _out_type(y), _ld(y), _stream(y))
+    dev = qx.device
+    op, E = experts(offsets, dev)
+    N = stacked(qw.shape[0], E, "qw")
+    qxp, ldqx = matrix(qx, "qx", (T, K), U8, dev)
+    sxp, ldsx = matrix(sx, "sx", (K // 128, T), F32, dev)
+    qwp, ldqw = matrix(qw, "qw", (E * N, K), U8, dev)
+    swp, ldsw = matrix(sw, "sw", (E * N // 128, K // 128), F32, dev)
+    yp, ldy = matrix(y, "y", (T, N), HI, dev)
+    return E, T, N, K, op, qxp, ldqx, sxp, ldsx, fx, qwp, ldqw, swp, ldsw, fw, yp, _out(y), ldy, stream(dev)
 
 
 @_entry
 def fp8bq_grouped_gemm_dgrad(qdy, sdy, fdy, offsets, qwt, sw, fw, dx):
     T, N = qdy.shape
-    E = _experts(offsets)
+    dev = qdy.device
+    op, E = experts(offsets, dev)
     K = qwt.shape[0]
-    _expect_all([(qdy, "qdy", (T, N), _U8), (sdy, "sdy", (N // 128, T), _F32), (offsets, "offsets", (E + 1,), _I64),
-                 (qwt, "qwt", (K, E * N), _U8), (sw, "sw", (E * N // 128, K // 128), _F32), (dx, "dx", (T, K), _HI)])
-    return (E, T, N, K, _ptr(offsets), _ptr(qdy), _ld(qdy), _ptr(sdy), _ld(sdy), fdy, _ptr(qwt), _ld(qwt), _ptr(sw),
-            _ld(sw), fw, _ptr(dx), _out_type(dx), _ld(dx), _stream(dx))
+    qdyp, ldqdy = matrix(qdy, "qdy", (T, N), U8, dev)
+    sdyp, ldsdy = matrix(sdy, "sdy", (N // 128, T), F32, dev)
+    qwtp, ldqwt = matrix(qwt, "qwt", (K, E * N), U8, dev)
+    swp, ldsw = matrix(sw, "sw", (E * N // 128, K // 128), F32, dev)
+    dxp, lddx = matrix(dx, "dx", (T, K), HI, dev)
+    return E, T, N, K, op, qdyp, ldqdy, sdyp, ldsdy, fdy, qwtp, ldqwt, swp, ldsw, fw, dxp, _out(dx), lddx, stream(dev)
 
 
 @_entry
 def fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=False):
     N, padded = qdyt.shape
-    E = _experts(offsets)
+    dev = qdyt.device
+    op, E = experts(offsets, dev)
     K = qxt.shape[0]
-    _expect_all([(qdyt, "qdyt", (N, padded), _U8), (sdyt, "sdyt", (padded // 128, N), _F32),
-                 (qxt, "qxt", (K, padded), _U8), (sxt, "sxt", (padded // 128, K), _F32),
-                 (offsets, "offsets", (E + 1,), _I64), (dw, "dw", (E * N, K), _F32 if accumulate else _HI)])
-    return (E, padded, N, K, _ptr(offsets), _ptr(qdyt), _ld(qdyt), _ptr(sdyt), _ld(sdyt), fdy, _ptr(qxt), _ld(qxt),
-            _ptr(sxt), _ld(sxt), fx, _ptr(dw), OUT_F32_ACCUM if accumulate else _out_type(dw), _ld(dw), _stream(dw))
+    qdytp, ldqdyt = matrix(qdyt, "qdyt", (N, padded), U8, dev)
+    sdytp, ldsdyt = matrix(sdyt, "sdyt", (padded // 128, N), F32, dev)
+    qxtp, ldqxt = matrix(qxt, "qxt", (K, padded), U8, dev)
+    sxtp, ldsxt = matrix(sxt, "sxt", (padded // 128, K), F32, dev)
+    dwp, lddw = matrix(dw, "dw", (E * N, K), F32 if accumulate else HI, dev)
+    return (E, padded, N, K, op, qdytp, ldqdyt, sdytp, ldsdyt, fdy, qxtp, ldqxt, sxtp, ldsxt, fx, dwp,
+            _out(dw, accumulate), lddw, stream(dev))
 
 
 def _cols_outputs(x, offsets):
     T, C = x.shape
-    padded = fp8bq_grouped_padded_rows(T, _experts(offsets))
-    qt = torch.empty((C, padded), dtype=torch.uint8, device=x.device)
-    return qt, torch.empty((padded // 128, C), dtype=torch.float32, device=x.device)
+    padded = fp8bq_grouped_padded_rows(T, offsets.shape[0] - 1)
+    return x.new_empty((C, padded), dtype=torch.uint8), x.new_empty((padded // 128, C), dtype=torch.float32)
 
 
 def quantize_act_grouped_128x1(x, offsets, fmt=E4M3):
@@ -125,22 +124,24 @@ def quantize_act_grouped_dual(x, offsets, fmt_rows=E4M3, fmt_cols=E4M3):
     """(q, s) of quantize_act_1x128(x, fmt_rows) and (qt, st) of quantize_act_grouped_128x1(x, offsets,
     fmt_cols) from one pass over x."""
     T, C = x.shape
-    q = torch.empty((T, C), dtype=torch.uint8, device=x.device)
-    s = torch.empty((C // 128, _pad4(T)), dtype=torch.float32, device=x.device)[:, :T]
+    q = x.new_empty((T, C), dtype=torch.uint8)
+    s = x.new_empty((C // 128, _pad4(T)), dtype=torch.float32)
+    if s.shape[1] != T:
+        s = s[:, :T]
     qt, st = _cols_outputs(x, offsets)
     fp8bq_quantize_act_grouped(x, offsets, fmt_rows, q, s, fmt_cols, qt, st)
     return q, s, qt, st
 
 
 def grouped_gemm_fprop(qx, sx, offsets, qw, sw, fx=E4M3, fw=E4M3, out_dtype=torch.bfloat16, out=None):
-    N = _stacked(qw.shape[0], _experts(offsets), "qw")
-    y = out if out is not None else torch.empty((qx.shape[0], N), dtype=out_dtype, device=qx.device)
+    N = stacked(qw.shape[0], offsets.shape[0] - 1, "qw")
+    y = out if out is not None else qx.new_empty((qx.shape[0], N), dtype=out_dtype)
     fp8bq_grouped_gemm_fprop(qx, sx, fx, offsets, qw, sw, fw, y)
     return y
 
 
 def grouped_gemm_dgrad(qdy, sdy, offsets, qwt, sw, fdy=E4M3, fw=E4M3, out_dtype=torch.bfloat16, out=None):
-    dx = out if out is not None else torch.empty((qdy.shape[0], qwt.shape[0]), dtype=out_dtype, device=qdy.device)
+    dx = out if out is not None else qdy.new_empty((qdy.shape[0], qwt.shape[0]), dtype=out_dtype)
     fp8bq_grouped_gemm_dgrad(qdy, sdy, fdy, offsets, qwt, sw, fw, dx)
     return dx
 
@@ -150,7 +151,7 @@ def grouped_gemm_wgrad(qdyt, sdyt, qxt, sxt, offsets, fdy=E4M3, fx=E4M3, out_dty
     """accumulate=True adds the result to `out` (an FP32 main-grad buffer) instead of overwriting it."""
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate=True needs an FP32 `out` tensor holding the running sum")
-    dw = out if out is not None else torch.empty((_experts(offsets) * qdyt.shape[0], qxt.shape[0]), dtype=out_dtype,
-                                                 device=qdyt.device)
+    dw = out if out is not None else qdyt.new_empty(((offsets.shape[0] - 1) * qdyt.shape[0], qxt.shape[0]),
+                                                    dtype=out_dtype)
     fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=accumulate)
     return dw

@@ -26,9 +26,8 @@ dW = gemm_mxfp4(columns of dY, columns of X), with the quantizers' gradient take
 
 import torch
 
-from . import (_HI, _U8, OUT_F32_ACCUM, _c_i64, _c_int, _c_sz, _c_vp, _entry, _expect_all, _F32, _in_type, _ld,
-               _out_type, _ptr, _RESTYPES, _SIGS, _stream, _ws_args, lib)
-from .grouped import _I64, _experts, _stacked
+from . import OUT_BF16, OUT_F32, OUT_F32_ACCUM, IN_BF16, IN_F32, _RESTYPES, _SIGS, _c_i64, _c_int, _c_sz, _c_vp, _entry, lib
+from ._marshal import F32, HI, U8, experts, matrix, scale_words, space, stacked, stream
 
 _OUT_WS = [_c_vp, _c_int, _c_i64, _c_vp, _c_sz, _c_vp]
 _CODES = [_c_vp, _c_i64, _c_vp, _c_i64]
@@ -65,112 +64,119 @@ def fp8bq_grouped_linear_mxfp4_workspace_size(E, T, N, K):
     return lib().fp8bq_grouped_linear_mxfp4_workspace_size(E, T, N, K)
 
 
-def _lds(s):
-    """Leading dimension, in words, of scales [words, R, 4]."""
-    if s.numel() == 0:
-        return max(s.size(1), 1)
-    if s.stride(2) != 1 or (s.size(1) > 1 and s.stride(1) != 4) or (s.size(0) > 1 and s.stride(0) % 4):
-        raise ValueError("scales must be [words, rows, 4] with rows of four bytes next to each other")
-    return s.stride(0) // 4 if s.size(0) > 1 else s.size(1)
-
-
-def _ldo(t):
-    """Leading dimension of an output (any, even where one row leaves it undefined)."""
-    return max(_ld(t), t.size(1), 1)
-
-
 def _words(n):
     return (n + 127) // 128
+
+
+def _in(t):
+    return IN_BF16 if t.dtype == torch.bfloat16 else IN_F32
+
+
+def _out(t, accumulate=False):
+    return OUT_F32_ACCUM if accumulate else OUT_BF16 if t.dtype == torch.bfloat16 else OUT_F32
 
 
 @_entry
 def fp8bq_quantize_mxfp4(x, q, s, qt, st):
     R, C = x.shape
-    _expect_all([(x, "x", (R, C), _HI), (q, "q", (R, C // 2), _U8), (s, "s", (_words(C), R, 4), _U8),
-                 (qt, "qt", (C, (R + 31) // 32 * 16), _U8), (st, "st", (_words(R), C, 4), _U8)])
-    return (_ptr(x), _in_type(x), R, C, _ld(x), _ptr(q), _ld(q) if q is not None else 0, _ptr(s),
-            _lds(s) if s is not None else 0, _ptr(qt), _ld(qt) if qt is not None else 0, _ptr(st),
-            _lds(st) if st is not None else 0, _stream(x))
+    dev = x.device
+    xp, ldx = matrix(x, "x", (R, C), HI, dev)
+    qp, ldq = matrix(q, "q", (R, C // 2), U8, dev)
+    sp, lds = scale_words(s, "s", (_words(C), R, 4), dev)
+    qtp, ldqt = matrix(qt, "qt", (C, (R + 31) // 32 * 16), U8, dev)
+    stp, ldst = scale_words(st, "st", (_words(R), C, 4), dev)
+    return xp, _in(x), R, C, ldx, qp, ldq, sp, lds, qtp, ldqt, stp, ldst, stream(dev)
 
 
 @_entry
 def fp8bq_gemm_mxfp4(qa, sa, qb, sb, c, ws=None, accumulate=False):
-    M, K = qa.shape[0], 2 * qa.shape[1]
+    M, K2 = qa.shape
     N = qb.shape[0]
-    _expect_all([(qa, "qa", (M, K // 2), _U8), (sa, "sa", (_words(K), M, 4), _U8), (qb, "qb", (N, K // 2), _U8),
-                 (sb, "sb", (_words(K), N, 4), _U8), (c, "c", (M, N), _F32 if accumulate else _HI)], ws)
-    wsp, wsb = _ws_args(ws)
-    return (M, N, K, _ptr(qa), _ld(qa), _ptr(sa), _lds(sa), _ptr(qb), _ld(qb), _ptr(sb), _lds(sb), _ptr(c),
-            OUT_F32_ACCUM if accumulate else _out_type(c), _ldo(c), wsp, wsb, _stream(c))
+    dev = qa.device
+    W = _words(2 * K2)
+    qap, ldqa = matrix(qa, "qa", (M, K2), U8, dev)
+    sap, ldsa = scale_words(sa, "sa", (W, M, 4), dev)
+    qbp, ldqb = matrix(qb, "qb", (N, K2), U8, dev)
+    sbp, ldsb = scale_words(sb, "sb", (W, N, 4), dev)
+    cp, ldc = matrix(c, "c", (M, N), F32 if accumulate else HI, dev)
+    wsp, wsb = space(ws, dev)
+    return M, N, 2 * K2, qap, ldqa, sap, ldsa, qbp, ldqb, sbp, ldsb, cp, _out(c, accumulate), ldc, wsp, wsb, stream(dev)
 
 
 @_entry
 def fp8bq_linear_mxfp4(x, qw, sw, y, ws=None):
     M, K = x.shape
     N = qw.shape[0]
-    _expect_all([(x, "x", (M, K), _HI), (qw, "qw", (N, K // 2), _U8), (sw, "sw", (_words(K), N, 4), _U8),
-                 (y, "y", (M, N), _HI)], ws)
-    wsp, wsb = _ws_args(ws)
-    return (M, N, K, _ptr(x), _in_type(x), _ld(x), _ptr(qw), _ld(qw), _ptr(sw), _lds(sw), _ptr(y), _out_type(y),
-            _ldo(y), wsp, wsb, _stream(y))
+    dev = x.device
+    xp, ldx = matrix(x, "x", (M, K), HI, dev)
+    qwp, ldqw = matrix(qw, "qw", (N, K // 2), U8, dev)
+    swp, ldsw = scale_words(sw, "sw", (_words(K), N, 4), dev)
+    yp, ldy = matrix(y, "y", (M, N), HI, dev)
+    wsp, wsb = space(ws, dev)
+    return M, N, K, xp, _in(x), ldx, qwp, ldqw, swp, ldsw, yp, _out(y), ldy, wsp, wsb, stream(dev)
 
 
 @_entry
 def fp8bq_grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, y, ws=None):
-    T, K = qa.shape[0], 2 * qa.shape[1]
-    E = _experts(offsets)
-    N = _stacked(qw.shape[0], E, "qw")
-    _expect_all([(qa, "qa", (T, K // 2), _U8), (sa, "sa", (_words(K), T, 4), _U8), (offsets, "offsets", (E + 1,), _I64),
-                 (qw, "qw", (E * N, K // 2), _U8), (sw, "sw", (_words(K), E * N, 4), _U8), (y, "y", (T, N), _HI)], ws)
-    wsp, wsb = _ws_args(ws)
-    return (E, T, N, K, _ptr(offsets), _ptr(qa), _ld(qa), _ptr(sa), _lds(sa), _ptr(qw), _ld(qw), _ptr(sw), _lds(sw),
-            _ptr(y), _out_type(y), _ldo(y), wsp, wsb, _stream(y))
+    T, K2 = qa.shape
+    dev = qa.device
+    op, E = experts(offsets, dev)
+    N = stacked(qw.shape[0], E, "qw")
+    W = _words(2 * K2)
+    qap, ldqa = matrix(qa, "qa", (T, K2), U8, dev)
+    sap, ldsa = scale_words(sa, "sa", (W, T, 4), dev)
+    qwp, ldqw = matrix(qw, "qw", (E * N, K2), U8, dev)
+    swp, ldsw = scale_words(sw, "sw", (W, E * N, 4), dev)
+    yp, ldy = matrix(y, "y", (T, N), HI, dev)
+    wsp, wsb = space(ws, dev)
+    return E, T, N, 2 * K2, op, qap, ldqa, sap, ldsa, qwp, ldqw, swp, ldsw, yp, _out(y), ldy, wsp, wsb, stream(dev)
 
 
 @_entry
 def fp8bq_grouped_linear_mxfp4(x, offsets, qw, sw, y, ws=None):
     T, K = x.shape
-    E = _experts(offsets)
-    N = _stacked(qw.shape[0], E, "qw")
-    _expect_all([(x, "x", (T, K), _HI), (offsets, "offsets", (E + 1,), _I64), (qw, "qw", (E * N, K // 2), _U8),
-                 (sw, "sw", (_words(K), E * N, 4), _U8), (y, "y", (T, N), _HI)], ws)
-    wsp, wsb = _ws_args(ws)
-    return (E, T, N, K, _ptr(offsets), _ptr(x), _in_type(x), _ld(x), _ptr(qw), _ld(qw), _ptr(sw), _lds(sw), _ptr(y),
-            _out_type(y), _ldo(y), wsp, wsb, _stream(y))
+    dev = x.device
+    op, E = experts(offsets, dev)
+    N = stacked(qw.shape[0], E, "qw")
+    xp, ldx = matrix(x, "x", (T, K), HI, dev)
+    qwp, ldqw = matrix(qw, "qw", (E * N, K // 2), U8, dev)
+    swp, ldsw = scale_words(sw, "sw", (_words(K), E * N, 4), dev)
+    yp, ldy = matrix(y, "y", (T, N), HI, dev)
+    wsp, wsb = space(ws, dev)
+    return E, T, N, K, op, xp, _in(x), ldx, qwp, ldqw, swp, ldsw, yp, _out(y), ldy, wsp, wsb, stream(dev)
 
 
-def _codes(R, K, device):
-    return (torch.empty((R, K // 2), dtype=torch.uint8, device=device),
-            torch.empty((_words(K), R, 4), dtype=torch.uint8, device=device))
+def _codes(R, K, like):
+    return like.new_empty((R, K // 2), dtype=torch.uint8), like.new_empty((_words(K), R, 4), dtype=torch.uint8)
 
 
 def quantize_mxfp4(x):
-    q, s = _codes(*x.shape, x.device)
+    q, s = _codes(*x.shape, x)
     fp8bq_quantize_mxfp4(x, q, s, None, None)
     return q, s
 
 
 def quantize_mxfp4_t(x):
     R, C = x.shape
-    qt, st = _codes(C, (R + 31) // 32 * 32, x.device)
+    qt, st = _codes(C, (R + 31) // 32 * 32, x)
     fp8bq_quantize_mxfp4(x, None, None, qt, st)
     return qt, st
 
 
 def quantize_mxfp4_dual(x):
     R, C = x.shape
-    q, s = _codes(R, C, x.device)
-    qt, st = _codes(C, (R + 31) // 32 * 32, x.device)
+    q, s = _codes(R, C, x)
+    qt, st = _codes(C, (R + 31) // 32 * 32, x)
     fp8bq_quantize_mxfp4(x, q, s, qt, st)
     return q, s, qt, st
 
 
-def _space(n, device):
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+def _space(n, like):
+    return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
 def _output(out, M, N, dtype, like):
-    return out if out is not None else torch.empty((M, N), dtype=dtype, device=like.device)
+    return out if out is not None else like.new_empty((M, N), dtype=dtype)
 
 
 def gemm_mxfp4(qa, sa, qb, sb, out_dtype=torch.bfloat16, out=None, ws=None, accumulate=False):
@@ -181,7 +187,7 @@ def gemm_mxfp4(qa, sa, qb, sb, out_dtype=torch.bfloat16, out=None, ws=None, accu
     N = qb.shape[0]
     c = _output(out, M, N, out_dtype, qa)
     if ws is None:
-        ws = _space(fp8bq_gemm_mxfp4_workspace_size(M, N, 2 * K2), qa.device)
+        ws = _space(fp8bq_gemm_mxfp4_workspace_size(M, N, 2 * K2), qa)
     fp8bq_gemm_mxfp4(qa, sa, qb, sb, c, ws, accumulate=accumulate)
     return c
 
@@ -191,28 +197,28 @@ def linear_mxfp4(x, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     N = qw.shape[0]
     y = _output(out, M, N, out_dtype, x)
     if ws is None:
-        ws = _space(fp8bq_linear_mxfp4_workspace_size(M, N, K), x.device)
+        ws = _space(fp8bq_linear_mxfp4_workspace_size(M, N, K), x)
     fp8bq_linear_mxfp4(x, qw, sw, y, ws)
     return y
 
 
 def grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     T, K2 = qa.shape
-    E = _experts(offsets)
-    N = _stacked(qw.shape[0], E, "qw")
+    E = offsets.shape[0] - 1
+    N = stacked(qw.shape[0], E, "qw")
     y = _output(out, T, N, out_dtype, qa)
     if ws is None:
-        ws = _space(fp8bq_grouped_gemm_mxfp4_workspace_size(E, T, N, 2 * K2), qa.device)
+        ws = _space(fp8bq_grouped_gemm_mxfp4_workspace_size(E, T, N, 2 * K2), qa)
     fp8bq_grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, y, ws)
     return y
 
 
 def grouped_linear_mxfp4(x, offsets, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     T, K = x.shape
-    E = _experts(offsets)
-    N = _stacked(qw.shape[0], E, "qw")
+    E = offsets.shape[0] - 1
+    N = stacked(qw.shape[0], E, "qw")
     y = _output(out, T, N, out_dtype, x)
     if ws is None:
-        ws = _space(fp8bq_grouped_linear_mxfp4_workspace_size(E, T, N, K), x.device)
+        ws = _space(fp8bq_grouped_linear_mxfp4_workspace_size(E, T, N, K), x)
     fp8bq_grouped_linear_mxfp4(x, offsets, qw, sw, y, ws)
     return y
