@@ -49,8 +49,7 @@ static int run_mx(const MxArgs& g, void* ws, size_t ws_bytes, void* stream) {
   int st = validate_mx(g, &empty, &zero);
   if (st != kOk || empty) return st;
   const bool linear = g.a_type != kMxCodes;
-  const int cus_plan = cus_or_default();
-  const MxPlan plan = plan_mx(linear, g.E, g.M, g.N, g.K, cus_plan);
+  const MxPlan plan = plan_mx(linear, g.E, g.M, g.N, g.K, cus_or_default());
   const MxSpace space = zero ? MxSpace{0, 0, 0} : mx_space(plan, linear, g.M, g.K);
   if ((st = check_workspace(g, ws, ws_bytes, space.total())) != kOk) return st;
   if ((st = current_device(nullptr)) != kOk) return st;
@@ -88,7 +87,7 @@ static int run_mx(const MxArgs& g, void* ws, size_t ws_bytes, void* stream) {
     d.a_type = kMxCodes;
   }
   const MxGroups grp{(const int64_t*)g.offsets, (int)g.E};
-  if (plan.skinny) return launched(launch_mx_skinny(d, grp, plan.rows, cus_plan, s));
+  if (plan.skinny) return launched(launch_mx_skinny(d, grp, plan, s));
   return launched(launch_mx_gemm(d, grp, plan, (uint8_t*)ws + space.codes + space.scales, s));
 }
 

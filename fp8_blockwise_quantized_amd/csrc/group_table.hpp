@@ -16,20 +16,29 @@ constexpr int kMaxExperts = 512;
 constexpr int kExpertsPerLane = kMaxExperts / 64;
 constexpr int kGroupTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;  // unit counts and starts
 
-__device__ __forceinline__ uint32_t wave_scan_add(uint32_t v, int lane) {  // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// Inclusive wave scans by DPP: four shifts within the rows of 16 lanes, then each row's last lane into the
+// next row and lane 31 into the upper half.  Lanes without a source take 0, the identity of both operations.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t scan_source(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan_add(uint32_t v) {
+  v += scan_source<0x111, 0xF>(v);
+  v += scan_source<0x112, 0xF>(v);
+  v += scan_source<0x114, 0xF>(v);
+  v += scan_source<0x118, 0xF>(v);
+  v += scan_source<0x142, 0xA>(v);
+  v += scan_source<0x143, 0xC>(v);
   return v;
 }
-__device__ __forceinline__ int wave_scan_max(int v, int lane) {  // inclusive, v >= 0
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v = o > v ? o : v;
-  }
+__device__ __forceinline__ int wave_scan_max(int v) {  // v >= 0
+  const auto up = [&](uint32_t o) { v = (int)o > v ? (int)o : v; };
+  up(scan_source<0x111, 0xF>(v));
+  up(scan_source<0x112, 0xF>(v));
+  up(scan_source<0x114, 0xF>(v));
+  up(scan_source<0x118, 0xF>(v));
+  up(scan_source<0x142, 0xA>(v));
+  up(scan_source<0x143, 0xC>(v));
   return v;
 }
 
@@ -45,7 +54,7 @@ __device__ __forceinline__ void group_offsets(const int64_t* offsets, int E, int
   }
 #pragma unroll
   for (int i = 1; i <= kExpertsPerLane; ++i) o[i] = o[i] > o[i - 1] ? o[i] : o[i - 1];
-  const int upto = wave_scan_max(o[kExpertsPerLane], lane);
+  const int upto = wave_scan_max(o[kExpertsPerLane]);
   int before = __shfl_up(upto, 1);
   before = lane == 0 ? 0 : before;
 #pragma unroll
@@ -57,7 +66,7 @@ __device__ __forceinline__ void group_sums(const uint32_t (&c)[kExpertsPerLane],
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < kExpertsPerLane; ++i) mine += c[i];
-  uint32_t at = wave_scan_add(mine, lane) - mine;
+  uint32_t at = wave_scan_add(mine) - mine;
 #pragma unroll
   for (int i = 0; i < kExpertsPerLane; ++i) {
     const int j = kExpertsPerLane * lane + i;
@@ -102,7 +111,7 @@ __device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < kExpertsPerLane; ++i) mine += c[i];
-  uint32_t at = wave_scan_add(mine, lane) - mine;
+  uint32_t at = wave_scan_add(mine) - mine;
   const uint32_t cap = (uint32_t)(padded / 128);
 #pragma unroll
   for (int i = 0; i < kExpertsPerLane; ++i) {

@@ -126,8 +126,8 @@ struct MxGroups {
   const int64_t* offsets;
   int experts;
 };
-// Few rows: rows is the (expected) row count of one product, which picks the tile height.
-hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, int64_t rows, int cus, hipStream_t st);
+// Few rows: p.nj column tiles of 16 a wave, p.split_k waves splitting the contraction.
+hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st);
 // Many rows, A in codes; ws: p.ws bytes of partial sums.
 hipError_t launch_mx_gemm(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st);
 

@@ -1,14 +1,16 @@
 // MXFP4 product for few rows of A (tokens): C[m, n] = sum_k A[m, k] B[n, k], B (the weights) streamed once.
 //
-// Bound by the weights' bytes (0.53 per weight) and, at the smallest sizes, by the latency of one pass.  A
-// workgroup owns 16 columns n (rows of B) and up to 16 MC rows of A; its eight waves split the contraction in
-// pieces of 256 (a 128-byte line of every B row), so all of a workgroup's loads are in flight at once, and
-// join their FP32 sums in LDS in wave order.  v_mfma_scale_f32_16x16x128_f8f6f4 takes B as its first operand:
-// lane l holds block l / 16 of row l % 16 of both operands (16 bytes of codes, one scale byte), straight from
-// memory, and ends with C row l % 16 and columns 4 (l / 16) .. +3.
+// Bound by the weights' bytes (0.53 per weight) and, at the smallest sizes, by the latency of one pass.
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes B as its first operand: lane l holds block l / 16 of row l % 16 of both
+// operands (16 bytes of codes, one scale byte), straight from memory, and ends with C row l % 16 and columns
+// 4 (l / 16) .. +3.  A wave owns 16 NJ columns and up to 64 rows and reads 256 values of its B rows (128-byte
+// lines) at a time.  KS waves of a workgroup split the contraction of the same columns and join their FP32
+// sums in LDS, in wave order: with few columns (one token through one layer) all eight, so that every load
+// of a workgroup is in flight at once; with many (64 experts) none, so that there is nothing to join.
 //
-// FUSED: A comes as BF16 or FP32 and each lane quantizes the block it needs itself: the 32 values of its MFMA
-// operand are exactly one block, so the maximum needs no other lane and no separate launch is paid.
+// FUSED (A in BF16 or FP32): the 32 values of a lane's operand are exactly one block, so each lane quantizes the
+// block it needs itself, without another lane and without a launch of its own, while the weights are on
+// their way.  Every column tile repeats that work, so it is taken for few rows only (plan_mx).
 #include "group_table.hpp"
 #include "launch.hpp"
 #include "mx_common.hpp"
@@ -18,18 +20,74 @@ namespace fp8bq {
 
 constexpr int kSkinnyWaves = 8;
 
-// The lane's block of A: codes and scale byte (zeros where the row or the block does not exist).
+// The lane's block of A on its way to an operand: load() issues the reads, get() gives codes and scale byte
+// (zeros where the row or the block does not exist).
 template <typename TA>
-struct MxBlockOf {  // TA = uint16_t (BF16) or float: quantized here
-  static __device__ __forceinline__ void run(const MxDesc& d, int64_t m, int64_t blk, bool valid, v4i& codes,
-                                             int& scale) {
-    codes = (v4i){0, 0, 0, 0};
-    scale = 0;
-    if (!valid) return;
-    const TA* p = reinterpret_cast<const TA*>(d.a) + m * d.lda + blk * kMxBlock;
-    float v[4][8];
+struct MxBlockOf;
+template <>
+struct MxBlockOf<uint8_t> {  // quantized before
+  v4i c;
+  uint32_t w;
+  __device__ __forceinline__ void load(const MxDesc& d, int64_t m, int64_t blk, bool valid) {
+    c = (v4i){0, 0, 0, 0};
+    w = 0;
+    if (valid) {
+      c = *reinterpret_cast<const v4i*>(reinterpret_cast<const uint8_t*>(d.a) + m * d.lda + blk * 16);
+      w = d.sa[(blk >> 2) * d.ldsa + m] >> (8 * (blk & 3));
+    }
+  }
+  __device__ __forceinline__ void get(v4i& codes, int& scale) const {
+    codes = c;
+    scale = (int)w;
+  }
+};
+template <>
+struct MxBlockOf<uint16_t> {  // BF16
+  u32x4 w[4];
+  __device__ __forceinline__ void load(const MxDesc& d, int64_t m, int64_t blk, bool valid) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Load8<TA>::run(p + 8 * i, v[i]);
+    for (int i = 0; i < 4; ++i) w[i] = (u32x4){0, 0, 0, 0};
+    if (valid) {
+      const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(d.a) + m * d.lda + blk * kMxBlock);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ void get(v4i& codes, int& scale) {
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m2 = pk_umax16(m2, w[i][j] & 0x7FFF7FFFu);
+    const uint32_t m = umax(m2 & 0xFFFFu, m2 >> 16) << 16;
+    const uint32_t b = mx_scale_byte(m);
+    if (b == 0u && m != 0u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i][j] = mx_lift_bf16(w[i][j]);
+    }
+    const float sc = mx_scale_of(b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) codes[i] = (int)mx_pack8_bf16(w[i][0], w[i][1], w[i][2], w[i][3], sc);
+    scale = (int)b;
+  }
+};
+template <>
+struct MxBlockOf<float> {
+  float v[4][8];
+  __device__ __forceinline__ void load(const MxDesc& d, int64_t m, int64_t blk, bool valid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (valid) {
+      const float* p = reinterpret_cast<const float*>(d.a) + m * d.lda + blk * kMxBlock;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) Load8<float>::run(p + 8 * i, v[i]);
+    }
+  }
+  __device__ __forceinline__ void get(v4i& codes, int& scale) {
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -44,17 +102,6 @@ struct MxBlockOf {  // TA = uint16_t (BF16) or float: quantized here
       codes[i] = (int)mx_pack8(v[i]);
     }
     scale = (int)b;
-  }
-};
-template <>
-struct MxBlockOf<uint8_t> {  // quantized before
-  static __device__ __forceinline__ void run(const MxDesc& d, int64_t m, int64_t blk, bool valid, v4i& codes,
-                                             int& scale) {
-    codes = (v4i){0, 0, 0, 0};
-    scale = 0;
-    if (!valid) return;
-    codes = *reinterpret_cast<const v4i*>(reinterpret_cast<const uint8_t*>(d.a) + m * d.lda + blk * 16);
-    scale = (int)(d.sa[(blk >> 2) * d.ldsa + m] >> (8 * (blk & 3)));
   }
 };
 
@@ -80,15 +127,19 @@ __device__ __forceinline__ void mx_store4(void* c, int64_t ldc, int64_t m, int64
   }
 }
 
-template <typename TA, int MC, int OUT, bool GROUPED>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void mx_skinny_kernel(MxDesc d, MxGroups grp) {
-  __shared__ float part[kSkinnyWaves][MC][4][64];
+// MC: row sub-tiles of 16 a wave holds (1, or 4 for codes of more than a few rows); ks: waves that split the
+// contraction (a power of two up to 8).
+template <typename TA, int MC, int NJ, int OUT, bool GROUPED>
+__global__ __launch_bounds__(kSkinnyWaves * 64, 4) void mx_skinny_kernel(MxDesc d, MxGroups grp, int ks) {
+  __shared__ float part[kSkinnyWaves][NJ][4][64];
   __shared__ int starts[GROUPED ? kMaxExperts + 1 : 1];
   __shared__ uint32_t units[GROUPED ? kMaxExperts + 1 : 1];
   const int t = threadIdx.x, lane = t & 63;
   const int wid = __builtin_amdgcn_readfirstlane(t >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const uint32_t tiles_n = (uint32_t)((d.N + 15) / 16);
+  const int phase = wid & (ks - 1), first = wid - phase;  // the waves of one set of columns: first .. first + ks - 1
+  const int cols = kSkinnyWaves / ks * NJ * 16;           // of the workgroup
+  const uint32_t tiles_n = (uint32_t)((d.N + cols - 1) / cols);
   const int64_t nblk = d.K / kMxBlock;
 
   uint32_t total;
@@ -101,7 +152,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx_skinny_kernel(MxDesc d, 
   }
 
   for (uint32_t u = blockIdx.x; u < total; u += gridDim.x) {
-    int64_t m0, mend, nbase = 0;
+    int64_t m0 = 0, mend = d.M, nbase = 0;
     uint32_t w = u;
     if constexpr (GROUPED) {
       const int e = group_find(units, grp.experts, u, lane);
@@ -109,96 +160,122 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx_skinny_kernel(MxDesc d, 
       m0 = starts[e];
       mend = starts[e + 1];
       nbase = (int64_t)e * d.N;
-    } else {
-      m0 = 0;
-      mend = d.M;
     }
     m0 += (int64_t)(w / tiles_n) * (16 * MC);
-    const int64_t nt = (int64_t)(w % tiles_n) * 16;  // first column within the expert's N
-    const int64_t nrow = nt + r16 < d.N ? nt + r16 : d.N - 1;
-    const uint8_t* brow = d.b + (nbase + nrow) * d.ldb;
-    const uint32_t* bscale = d.sb + nbase + nrow;
+    const int mc = MC == 1 ? 1 : __builtin_amdgcn_readfirstlane((int)(mend - m0 >= 16 * MC ? MC : (mend - m0 + 15) / 16));
+    const int64_t nt = (int64_t)(w % tiles_n) * cols + wid / ks * (NJ * 16);  // the wave's first column
+    const uint8_t* brow[NJ];
+    const uint32_t* bscale[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t n = nt + 16 * j + r16;
+      const int64_t row = nbase + (n < d.N ? n : d.N - 1);
+      brow[j] = d.b + row * d.ldb;
+      bscale[j] = d.sb + row;
+    }
 
-    v4f acc[MC];
+    v4f acc[MC][NJ];
 #pragma unroll
-    for (int i = 0; i < MC; ++i) acc[i] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t k8 = (int64_t)wid * 8; k8 < nblk; k8 += kSkinnyWaves * 8) {  // 8 blocks: two MFMA steps
-      v4i bc[2];
-      int bs[2];
+    for (int i = 0; i < MC; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t blk = k8 + 4 * h + g;
-        const bool valid = blk < nblk;
-        const int64_t at = valid ? blk : nblk - 1;
-        bc[h] = *reinterpret_cast<const v4i*>(brow + at * 16);
-        bs[h] = valid ? (int)(bscale[(at >> 2) * d.ldsb] >> (8 * (at & 3))) : 0;
-      }
+      for (int j = 0; j < NJ; ++j) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    if (nt < d.N) {
+      for (int64_t k8 = (int64_t)phase * 8; k8 < nblk; k8 += ks * 8) {  // 8 blocks: two MFMA steps
+        // A's reads first: memory answers in order, and quantizing can then begin before B is there
+        MxBlockOf<TA> a[2][MC];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t blk = k8 + 4 * h + g;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < MC; ++i) {
-          const int64_t m = m0 + 16 * i + r16;
-          v4i ac;
-          int as;
-          MxBlockOf<TA>::run(d, m, blk, m < mend && blk < nblk, ac, as);
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(bc[h]), mx_operand(ac), acc[i], 4, 4, 0,
-                                                                    bs[h], 0, as);
+          for (int i = 0; i < MC; ++i)
+            if (i < mc) {
+              const int64_t blk = k8 + 4 * h + g, m = m0 + 16 * i + r16;
+              a[h][i].load(d, m, blk, m < mend && blk < nblk);
+            }
+        v4i bc[2][NJ];
+        int bs[2][NJ];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t blk = k8 + 4 * h + g;
+          const int64_t at = blk < nblk ? blk : nblk - 1;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            bc[h][j] = *reinterpret_cast<const v4i*>(brow[j] + at * 16);
+            bs[h][j] = (int)bscale[j][(at >> 2) * d.ldsb];
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t blk = k8 + 4 * h + g;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) bs[h][j] = blk < nblk ? bs[h][j] >> (8 * (blk & 3)) : 0;
+#pragma unroll
+          for (int i = 0; i < MC; ++i)
+            if (i < mc) {
+              v4i ac;
+              int as;
+              a[h][i].get(ac, as);
+#pragma unroll
+              for (int j = 0; j < NJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(bc[h][j]), mx_operand(ac),
+                                                                             acc[i][j], 4, 4, 0, bs[h][j], 0, as);
+            }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < MC; ++i)
+    for (int i = 0; i < MC; ++i) {
+      if (i >= mc) continue;
+      const int64_t m = m0 + 16 * i + r16;
+      if (ks == 1) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wid][i][r][lane] = acc[i][r];
-    __syncthreads();
-    if (wid < MC) {
-      v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < NJ; ++j)
+          if (m < mend) mx_store4<OUT>(d.c, d.ldc, m, nt + 16 * j + 4 * g, d.N, acc[i][j]);
+      } else {
 #pragma unroll
-      for (int k = 0; k < kSkinnyWaves; ++k)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] += part[k][wid][r][lane];
-      const int64_t m = m0 + 16 * wid + r16;
-      if (m < mend) mx_store4<OUT>(d.c, d.ldc, m, nt + 4 * g, d.N, sum);
+          for (int r = 0; r < 4; ++r) part[wid][j][r][lane] = acc[i][j][r];
+        __syncthreads();
+        for (int j = phase; j < NJ; j += ks) {
+          v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int k = 0; k < ks; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[r] += part[first + k][j][r][lane];
+          if (m < mend) mx_store4<OUT>(d.c, d.ldc, m, nt + 16 * j + 4 * g, d.N, sum);
+        }
+        __syncthreads();
+      }
     }
-    __syncthreads();
   }
 }
 
-template <typename TA, int MC, int OUT>
-static hipError_t launch_mc(const MxDesc& d, const MxGroups& grp, int cus, hipStream_t st) {
-  const int64_t tiles_n = (d.N + 15) / 16;
-  if (grp.offsets) {
-    const int64_t most = (d.M / (16 * MC) + (grp.experts < d.M ? grp.experts : d.M)) * tiles_n;
-    const int64_t g = most < 16 * (int64_t)cus ? most : 16 * (int64_t)cus;
-    hipLaunchKernelGGL((mx_skinny_kernel<TA, MC, OUT, true>), dim3((unsigned)g), dim3(kSkinnyWaves * 64), 0, st, d,
-                       grp);
-  } else {
-    const int64_t all = (d.M + 16 * MC - 1) / (16 * MC) * tiles_n;
-    const int64_t g = all < 65536 ? all : 65536;
-    hipLaunchKernelGGL((mx_skinny_kernel<TA, MC, OUT, false>), dim3((unsigned)g), dim3(kSkinnyWaves * 64), 0, st, d,
-                       grp);
-  }
+template <typename TA, int MC, int NJ, int OUT>
+static hipError_t launch_nj(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
+  if (grp.offsets)
+    hipLaunchKernelGGL((mx_skinny_kernel<TA, MC, NJ, OUT, true>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st,
+                       d, grp, p.split_k);
+  else
+    hipLaunchKernelGGL((mx_skinny_kernel<TA, MC, NJ, OUT, false>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0,
+                       st, d, grp, p.split_k);
   return hipGetLastError();
 }
 
-template <typename TA, int OUT>
-static hipError_t launch_a(const MxDesc& d, const MxGroups& grp, int64_t rows, int cus, hipStream_t st) {
-  if (rows <= 16) return launch_mc<TA, 1, OUT>(d, grp, cus, st);
-  if (rows <= 32) return launch_mc<TA, 2, OUT>(d, grp, cus, st);
-  return launch_mc<TA, 4, OUT>(d, grp, cus, st);
+template <typename TA, int MC, int OUT>
+static hipError_t launch_mc(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
+  return p.nj == 1 ? launch_nj<TA, MC, 1, OUT>(d, grp, p, st) : launch_nj<TA, MC, 2, OUT>(d, grp, p, st);
 }
 
-template <typename TA>
-static hipError_t launch_out(const MxDesc& d, const MxGroups& grp, int64_t rows, int cus, hipStream_t st) {
-  if (d.out_t == 0) return launch_a<TA, 0>(d, grp, rows, cus, st);
-  if (d.out_t == 1) return launch_a<TA, 1>(d, grp, rows, cus, st);
-  return launch_a<TA, 2>(d, grp, rows, cus, st);
+template <typename TA, int MC>
+static hipError_t launch_out(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
+  if (d.out_t == 0) return launch_mc<TA, MC, 0>(d, grp, p, st);
+  if (d.out_t == 1) return launch_mc<TA, MC, 1>(d, grp, p, st);
+  return launch_mc<TA, MC, 2>(d, grp, p, st);
 }
 
-hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, int64_t rows, int cus, hipStream_t st) {
-  if (d.a_type == kMxCodes) return launch_out<uint8_t>(d, grp, rows, cus, st);
-  return d.a_type == kMxBf16 ? launch_out<uint16_t>(d, grp, rows, cus, st) : launch_out<float>(d, grp, rows, cus, st);
+hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
+  if (d.a_type == kMxCodes)
+    return p.mc == 1 ? launch_out<uint8_t, 1>(d, grp, p, st) : launch_out<uint8_t, 4>(d, grp, p, st);
+  return d.a_type == kMxBf16 ? launch_out<uint16_t, 1>(d, grp, p, st) : launch_out<float, 1>(d, grp, p, st);
 }
 
 }  // namespace fp8bq
