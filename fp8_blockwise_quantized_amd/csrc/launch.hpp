@@ -126,7 +126,7 @@ struct MxGroups {
   const int64_t* offsets;
   int experts;
 };
-// Few rows: p.nj column tiles of 16 a wave, p.split_k waves splitting the contraction.
+// Few rows and columns: p.split_k waves split the contraction.
 hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st);
 // Many rows, A in codes; ws: p.ws bytes of partial sums.
 hipError_t launch_mx_gemm(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st);

@@ -1,16 +1,19 @@
-// MXFP4 product for few rows of A (tokens): C[m, n] = sum_k A[m, k] B[n, k], B (the weights) streamed once.
+// MXFP4 product for up to 16 rows of A (tokens) a product: C[m, n] = sum_k A[m, k] B[n, k].
 //
-// Bound by the weights' bytes (0.53 per weight) and, at the smallest sizes, by the latency of one pass.
+// For few column tiles, where one pass's latency counts (one token through 11264 x 2048: 5.6 us with the
+// quantization, 4.7 us from codes, most of it launch, first loads and the joining of sums; 12 MB of weights
+// at the copy's rate would take 2 us).  From about 1500 column tiles on the LDS-tiled kernel streams the
+// weights faster, whatever the rows (45056 x 2048, one row: 10.1 us there, 11.5 us here).
+//
 // v_mfma_scale_f32_16x16x128_f8f6f4 takes B as its first operand: lane l holds block l / 16 of row l % 16 of both
 // operands (16 bytes of codes, one scale byte), straight from memory, and ends with C row l % 16 and columns
-// 4 (l / 16) .. +3.  A wave owns 16 NJ columns and up to 64 rows and reads 256 values of its B rows (128-byte
-// lines) at a time.  KS waves of a workgroup split the contraction of the same columns and join their FP32
-// sums in LDS, in wave order: with few columns (one token through one layer) all eight, so that every load
-// of a workgroup is in flight at once; with many (64 experts) none, so that there is nothing to join.
+// 4 (l / 16) .. +3.  A wave owns 16 columns and reads 256 values of its B rows (128-byte lines) at a time; the KS
+// waves that share them split the contraction, so that every load of a workgroup is in flight at once, and
+// join their FP32 sums in LDS in wave order.
 //
 // FUSED (A in BF16 or FP32): the 32 values of a lane's operand are exactly one block, so each lane quantizes the
 // block it needs itself, without another lane and without a launch of its own, while the weights are on
-// their way.  Every column tile repeats that work, so it is taken for few rows only (plan_mx).
+// their way.  Every column tile repeats that work, so it is taken for few tiles and rows only (plan_mx).
 #include "group_table.hpp"
 #include "launch.hpp"
 #include "mx_common.hpp"
@@ -127,28 +130,27 @@ __device__ __forceinline__ void mx_store4(void* c, int64_t ldc, int64_t m, int64
   }
 }
 
-// MC: row sub-tiles of 16 a wave holds (1, or 4 for codes of more than a few rows); ks: waves that split the
-// contraction (a power of two up to 8).
-template <typename TA, int MC, int NJ, int OUT, bool GROUPED>
+// ks: waves that split the contraction (a power of two up to 8).
+template <typename TA, int OUT, bool GROUPED>
 __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void mx_skinny_kernel(MxDesc d, MxGroups grp, int ks) {
-  __shared__ float part[kSkinnyWaves][NJ][4][64];
+  __shared__ float part[kSkinnyWaves][4][64];
   __shared__ int starts[GROUPED ? kMaxExperts + 1 : 1];
   __shared__ uint32_t units[GROUPED ? kMaxExperts + 1 : 1];
   const int t = threadIdx.x, lane = t & 63;
   const int wid = __builtin_amdgcn_readfirstlane(t >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int phase = wid & (ks - 1), first = wid - phase;  // the waves of one set of columns: first .. first + ks - 1
-  const int cols = kSkinnyWaves / ks * NJ * 16;           // of the workgroup
+  const int phase = wid & (ks - 1);
+  const int cols = kSkinnyWaves / ks * 16;  // of the workgroup
   const uint32_t tiles_n = (uint32_t)((d.N + cols - 1) / cols);
   const int64_t nblk = d.K / kMxBlock;
 
   uint32_t total;
   if constexpr (GROUPED) {
-    if (wid == 0) group_table_rows(grp.offsets, grp.experts, d.M, 16 * MC, tiles_n, starts, units, lane);
+    if (wid == 0) group_table_rows(grp.offsets, grp.experts, d.M, 16, tiles_n, starts, units, lane);
     __syncthreads();
     total = units[grp.experts];
   } else {
-    total = tiles_n * (uint32_t)((d.M + 16 * MC - 1) / (16 * MC));
+    total = tiles_n * (uint32_t)((d.M + 15) / 16);
   }
 
   for (uint32_t u = blockIdx.x; u < total; u += gridDim.x) {
@@ -161,121 +163,78 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void mx_skinny_kernel(MxDesc 
       mend = starts[e + 1];
       nbase = (int64_t)e * d.N;
     }
-    m0 += (int64_t)(w / tiles_n) * (16 * MC);
-    const int mc = MC == 1 ? 1 : __builtin_amdgcn_readfirstlane((int)(mend - m0 >= 16 * MC ? MC : (mend - m0 + 15) / 16));
-    const int64_t nt = (int64_t)(w % tiles_n) * cols + wid / ks * (NJ * 16);  // the wave's first column
-    const uint8_t* brow[NJ];
-    const uint32_t* bscale[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int64_t n = nt + 16 * j + r16;
-      const int64_t row = nbase + (n < d.N ? n : d.N - 1);
-      brow[j] = d.b + row * d.ldb;
-      bscale[j] = d.sb + row;
-    }
+    const int64_t m = m0 + (int64_t)(w / tiles_n) * 16 + r16;
+    const int64_t nt = (int64_t)(w % tiles_n) * cols + wid / ks * 16;  // the wave's first column
+    const int64_t row = nbase + (nt + r16 < d.N ? nt + r16 : d.N - 1);
+    const uint8_t* brow = d.b + row * d.ldb;
+    const uint32_t* bscale = d.sb + row;
 
-    v4f acc[MC][NJ];
-#pragma unroll
-    for (int i = 0; i < MC; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
     if (nt < d.N) {
       for (int64_t k8 = (int64_t)phase * 8; k8 < nblk; k8 += ks * 8) {  // 8 blocks: two MFMA steps
         // A's reads first: memory answers in order, and quantizing can then begin before B is there
-        MxBlockOf<TA> a[2][MC];
+        MxBlockOf<TA> a[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < MC; ++i)
-            if (i < mc) {
-              const int64_t blk = k8 + 4 * h + g, m = m0 + 16 * i + r16;
-              a[h][i].load(d, m, blk, m < mend && blk < nblk);
-            }
-        v4i bc[2][NJ];
-        int bs[2][NJ];
+        for (int h = 0; h < 2; ++h) {
+          const int64_t blk = k8 + 4 * h + g;
+          a[h].load(d, m, blk, m < mend && blk < nblk);
+        }
+        v4i bc[2];
+        int bs[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t blk = k8 + 4 * h + g;
           const int64_t at = blk < nblk ? blk : nblk - 1;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            bc[h][j] = *reinterpret_cast<const v4i*>(brow[j] + at * 16);
-            bs[h][j] = (int)bscale[j][(at >> 2) * d.ldsb];
-          }
+          bc[h] = *reinterpret_cast<const v4i*>(brow + at * 16);
+          bs[h] = (int)bscale[(at >> 2) * d.ldsb];
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t blk = k8 + 4 * h + g;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) bs[h][j] = blk < nblk ? bs[h][j] >> (8 * (blk & 3)) : 0;
-#pragma unroll
-          for (int i = 0; i < MC; ++i)
-            if (i < mc) {
-              v4i ac;
-              int as;
-              a[h][i].get(ac, as);
-#pragma unroll
-              for (int j = 0; j < NJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(bc[h][j]), mx_operand(ac),
-                                                                             acc[i][j], 4, 4, 0, bs[h][j], 0, as);
-            }
+          v4i ac;
+          int as;
+          a[h].get(ac, as);
+          acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(bc[h]), mx_operand(ac), acc, 4, 4, 0,
+                                                                 blk < nblk ? bs[h] >> (8 * (blk & 3)) : 0, 0, as);
         }
       }
     }
+    if (ks > 1) {
 #pragma unroll
-    for (int i = 0; i < MC; ++i) {
-      if (i >= mc) continue;
-      const int64_t m = m0 + 16 * i + r16;
-      if (ks == 1) {
+      for (int r = 0; r < 4; ++r) part[wid][r][lane] = acc[r];
+      __syncthreads();
+      if (phase == 0) {
+        for (int k = 1; k < ks; ++k)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          if (m < mend) mx_store4<OUT>(d.c, d.ldc, m, nt + 16 * j + 4 * g, d.N, acc[i][j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) part[wid][j][r][lane] = acc[i][j][r];
-        __syncthreads();
-        for (int j = phase; j < NJ; j += ks) {
-          v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int k = 0; k < ks; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] += part[first + k][j][r][lane];
-          if (m < mend) mx_store4<OUT>(d.c, d.ldc, m, nt + 16 * j + 4 * g, d.N, sum);
-        }
-        __syncthreads();
+          for (int r = 0; r < 4; ++r) acc[r] += part[wid + k][r][lane];
       }
+      __syncthreads();
     }
+    if (phase == 0 && m < mend && nt < d.N) mx_store4<OUT>(d.c, d.ldc, m, nt + 4 * g, d.N, acc);
   }
 }
 
-template <typename TA, int MC, int NJ, int OUT>
-static hipError_t launch_nj(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
+template <typename TA, int OUT>
+static hipError_t launch_groups(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
   if (grp.offsets)
-    hipLaunchKernelGGL((mx_skinny_kernel<TA, MC, NJ, OUT, true>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st,
-                       d, grp, p.split_k);
+    hipLaunchKernelGGL((mx_skinny_kernel<TA, OUT, true>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st, d, grp,
+                       p.split_k);
   else
-    hipLaunchKernelGGL((mx_skinny_kernel<TA, MC, NJ, OUT, false>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0,
-                       st, d, grp, p.split_k);
+    hipLaunchKernelGGL((mx_skinny_kernel<TA, OUT, false>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st, d,
+                       grp, p.split_k);
   return hipGetLastError();
 }
 
-template <typename TA, int MC, int OUT>
-static hipError_t launch_mc(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
-  return p.nj == 1 ? launch_nj<TA, MC, 1, OUT>(d, grp, p, st) : launch_nj<TA, MC, 2, OUT>(d, grp, p, st);
-}
-
-template <typename TA, int MC>
+template <typename TA>
 static hipError_t launch_out(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
-  if (d.out_t == 0) return launch_mc<TA, MC, 0>(d, grp, p, st);
-  if (d.out_t == 1) return launch_mc<TA, MC, 1>(d, grp, p, st);
-  return launch_mc<TA, MC, 2>(d, grp, p, st);
+  if (d.out_t == 0) return launch_groups<TA, 0>(d, grp, p, st);
+  if (d.out_t == 1) return launch_groups<TA, 1>(d, grp, p, st);
+  return launch_groups<TA, 2>(d, grp, p, st);
 }
 
 hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
-  if (d.a_type == kMxCodes)
-    return p.mc == 1 ? launch_out<uint8_t, 1>(d, grp, p, st) : launch_out<uint8_t, 4>(d, grp, p, st);
-  return d.a_type == kMxBf16 ? launch_out<uint16_t, 1>(d, grp, p, st) : launch_out<float, 1>(d, grp, p, st);
+  if (d.a_type == kMxCodes) return launch_out<uint8_t>(d, grp, p, st);
+  return d.a_type == kMxBf16 ? launch_out<uint16_t>(d, grp, p, st) : launch_out<float>(d, grp, p, st);
 }
 
 }  // namespace fp8bq

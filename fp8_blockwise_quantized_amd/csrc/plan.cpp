@@ -158,29 +158,25 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
 // MI355X (8192 x 8192 x 8192 with each tile: 275, 340 and 500 us).
 static double mx_stage_us(int shape) { return shape == k256x256 ? 2.1 : shape == k64x64 ? 0.98 : 1.33; }
 
-// Column tiles times 128-long steps up to which every tile quantizes the rows it needs itself instead of a
-// quantizer launch before the product.
-constexpr int64_t kFusedSteps = 20000;
-
 MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count) {
   MxPlan p;
   const int64_t cus = cu_count > 0 ? cu_count : 256;
   const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
   p.rows = cdiv(M, used);
-  p.skinny = p.rows <= 64;
+  // Few rows on few column tiles: the kernel without LDS staging.  From codes (us, one row and K = 2048; the
+  // tiled kernel second): N = 4096 3.6 / 6.5, 11264 4.7 / 6.5, 22528 6.4 / 7.1, 45056 11.5 / 10.1.
+  const int64_t tiles = used * cdiv(N, 16);
+  p.skinny = M <= 16 && tiles <= 1536;
   if (p.skinny) {
-    const int64_t tiles = used * cdiv(N, 16);  // column tiles, each with its rows' blocks of A
-    p.fused = linear && p.rows <= 16 && tiles * cdiv(K, 128) <= kFusedSteps;
-    // enough waves for the card (16 to 32 a CU) come from the columns or from splitting the contraction
-    const int64_t waves = 32 * cus;
+    // Every tile quantizes its rows itself while that costs less than a quantizer launch (us, fused and not):
+    // 16 rows, 11264 x 2048 9.4 / 10.5, 16384 x 2048 11.6 / 10.5; 8 rows, 16384 x 2048 9.1 / 9.9, 22528 x 2048
+    // 12.2 / 11.5; 16 rows, 2048 x 11264 15.7 / 12.8; 8 rows, 2048 x 11264 11.4 / 12.4.
+    const int64_t steps = tiles * cdiv(K, 128);
+    p.fused = linear && steps <= 300000 / (p.rows + 8) && p.rows * K <= 131072;
     p.split_k = 8;
-    while (p.split_k > 1 && (tiles * p.split_k > waves + waves / 4 || p.split_k > cdiv(K, 256))) p.split_k /= 2;
-    p.nj = p.split_k == 1 && tiles >= waves ? 2 : 1;
-    // (shares of the experts differ: with more than four rows on average some have more than 16)
-    p.mc = p.fused || p.rows <= (E == 0 ? 16 : 4) ? 1 : 4;
-    const int64_t row_tiles = 16 * p.mc;
-    const int64_t groups = E == 0 ? cdiv(M, row_tiles) : M / row_tiles + used;
-    const int64_t units = groups * cdiv(N, 8 / p.split_k * p.nj * 16);
+    while (p.split_k > cdiv(K, 256)) p.split_k /= 2;
+    const int64_t groups = E == 0 ? 1 : used;
+    const int64_t units = groups * cdiv(N, 8 / p.split_k * 16);
     p.grid = units < 16 * cus ? units : 16 * cus;
     return p;
   }

@@ -66,8 +66,6 @@ struct MxPlan {
   int64_t rows = 0;    // rows one product is expected to have
   int shape = k128x128;
   int split_k = 1;     // skinny: waves of a workgroup that split the contraction; else as in GemmPlan
-  int nj = 1;          // skinny: column tiles of 16 a wave
-  int mc = 1;          // skinny: row tiles of 16 a wave
   int64_t tiles_m = 0, tiles_n = 0;
   int64_t grid = 0;
   size_t ws = 0;       // workspace of the product itself
