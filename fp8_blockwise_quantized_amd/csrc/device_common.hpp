@@ -94,6 +94,12 @@ __device__ __forceinline__ uint32_t pack4(float v0, float v1, float v2, float v3
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Larger of two pairs of 16-bit integers (magnitudes of packed BF16 pairs compare as such).
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_umax16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
 // Lane exchanges within DPP rows (16 lanes).  Every pattern used here reads a valid lane for every
 // lane, so bound_ctrl (zero for an invalid source) never applies; with old = 0 it lets the compiler
 // fold the move into the consuming max as one v_max_u32_dpp.

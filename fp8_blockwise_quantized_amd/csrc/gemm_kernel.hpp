@@ -640,6 +640,23 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
                                                                    pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
             }
           }
+        } else if constexpr (!CHK && NI % 2 == 0) {
+          // Two patches' four columns each (8 bytes): lanes l and l + 16 swap, so that a lane has eight
+          // consecutive columns of one patch and an output row's four lanes write 64 contiguous bytes.
+          const int g = lane >> 4;
+          uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + crow * d.ldc + ccol - 4 * g + 16 * (g & 1) + 8 * (g >> 1);
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            uint16_t* ci = c0 + 16 * i * d.ldc;
+#pragma unroll
+            for (int j = 0; j < NI; j += 2) {
+              const v4f& a = acc[i][j];
+              const v4f& b = acc[i][j + 1];
+              const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[0], a[1]), pack_bf16x2(b[0], b[1]), false, false);
+              const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[2], a[3]), pack_bf16x2(b[2], b[3]), false, false);
+              *reinterpret_cast<uint4*>(ci + 16 * j) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+            }
+          }
         } else {
           uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + crow * d.ldc + ccol;
 #pragma unroll

@@ -50,10 +50,6 @@ __device__ __forceinline__ v8i mx_operand(v4i c) { return (v8i){c.x, c.y, c.z, c
 // One block of 32 BF16 values (packed pairs, in order) -> codes and scale byte.  The converter divides by the
 // scale itself and takes pairs; a subnormal scale (byte 0, amax below 2^-124) it would flush, so such a block
 // takes the product with 2^127 instead.
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pk_umax16(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
-}
 __device__ __forceinline__ uint32_t mx_pack8_bf16(uint32_t a, uint32_t b, uint32_t c, uint32_t d, float scale) {
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, a), scale, 0);

@@ -127,7 +127,10 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
   double best = 0.0;
   for (int i = 0; i < 3; ++i) {
     const int s = shapes[i];
-    const double units = (double)used * (double)cdiv(rows, tile_rows(s)) * (double)cdiv(cols, tile_cols(s));
+    // ragged shares end half a tile short on average
+    double tiles_m = op == kOpWgrad ? (double)cdiv(rows, tile_rows(s)) : (double)share / tile_rows(s) + 0.5;
+    tiles_m = tiles_m < 1.0 ? 1.0 : tiles_m;
+    const double units = (double)used * tiles_m * (double)cdiv(cols, tile_cols(s));
     const double slots = (double)(cus * blocks_per_cu(s));
     const double full = (double)(int64_t)(units / slots);
     const double frac = units / slots - full;

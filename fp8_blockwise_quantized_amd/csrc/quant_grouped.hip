@@ -14,6 +14,62 @@
 
 namespace fp8bq {
 
+// A thread's 8 rows by 8 columns.  BF16 stays packed in half the registers: its magnitudes compare as 16-bit
+// integers, two at a time, and a value is unpacked (one shift or mask) where it is divided.
+template <typename TIn>
+struct Patch;
+template <>
+struct Patch<float> {
+  float v[8][8];
+  __device__ __forceinline__ void load(int p, const float* x) { Load8<float>::run(x, v[p]); }
+  __device__ __forceinline__ void clear(int p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+  }
+  __device__ __forceinline__ void renew() {}
+  __device__ __forceinline__ float at(int p, int i) const { return v[p][i]; }
+  __device__ __forceinline__ float row_max(int p) const {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[p][i]));
+    return m;
+  }
+  __device__ __forceinline__ void column_max(int c, float& even, float& odd) const {
+    even = odd = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      even = __builtin_fmaxf(even, __builtin_fabsf(v[p][2 * c]));
+      odd = __builtin_fmaxf(odd, __builtin_fabsf(v[p][2 * c + 1]));
+    }
+  }
+};
+template <>
+struct Patch<uint16_t> {
+  u32x4 w[8];
+  __device__ __forceinline__ void load(int p, const uint16_t* x) { w[p] = *reinterpret_cast<const u32x4*>(x); }
+  __device__ __forceinline__ void clear(int p) { w[p] = (u32x4){0, 0, 0, 0}; }
+  // Between the row and the column layout: the compiler would otherwise keep all 64 unpacked values from the
+  // one for the other (170 registers, two waves per SIMD).
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) asm volatile("" : "+v"(w[p]));
+  }
+  __device__ __forceinline__ float at(int p, int i) const { return i & 1 ? bf16hi(w[p][i >> 1]) : bf16lo(w[p][i >> 1]); }
+  __device__ __forceinline__ float row_max(int p) const {
+    uint32_t m = w[p][0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = pk_umax16(m, w[p][i] & 0x7FFF7FFFu);
+    return bf16lo(umax(m & 0xFFFFu, m >> 16));
+  }
+  __device__ __forceinline__ void column_max(int c, float& even, float& odd) const {
+    uint32_t m = w[0][c] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int p = 1; p < 8; ++p) m = pk_umax16(m, w[p][c] & 0x7FFF7FFFu);
+    even = bf16lo(m);
+    odd = bf16hi(m);
+  }
+};
+
 template <typename TIn, int FR, int FC, bool ROWS>
 __global__ __launch_bounds__(256) void quant_grouped_kernel(const TIn* __restrict__ x, int64_t T, int64_t ldx,
                                                             const int64_t* __restrict__ offsets, int E,
@@ -46,25 +102,19 @@ __global__ __launch_bounds__(256) void quant_grouped_kernel(const TIn* __restric
     const int64_t r0 = rows[e] + (int64_t)(rb - blocks[e]) * kGroup;  // first token of the block
     const int left = (int)(rows[e + 1] - r0);                        // tokens in it (128 if more)
 
-    float v[8][8];
+    Patch<TIn> v;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      if (8 * rg + p < left) {
-        Load8<TIn>::run(x + (r0 + 8 * rg + p) * ldx + col, v[p]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-      }
+      if (8 * rg + p < left)
+        v.load(p, x + (r0 + 8 * rg + p) * ldx + col);
+      else
+        v.clear(p);
     }
 
     if constexpr (ROWS) {
       float m[8];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        m[p] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[p] = __builtin_fmaxf(m[p], __builtin_fabsf(v[p][i]));
-      }
+      for (int p = 0; p < 8; ++p) m[p] = v.row_max(p);
       const float sc_own = group_scale<FR>(row16_max_scatter<8>(m, cc));
       const float rc_own = 1.0f / sc_own;
       const int own = 8 * rg + (cc >> scatter_shift<8>());
@@ -73,17 +123,17 @@ __global__ __launch_bounds__(256) void quant_grouped_kernel(const TIn* __restric
         constexpr int p = decltype(P)::value;
         const float sc = row16_bcast<(p << scatter_shift<8>())>(sc_own);
         const float rc = row16_bcast<(p << scatter_shift<8>())>(rc_own);
-        if (8 * rg + p < left) store_codes8(q + (r0 + 8 * rg + p) * ldq + col, quant8<FR>(v[p], sc, rc));
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = v.at(p, i);
+        if (8 * rg + p < left) store_codes8(q + (r0 + 8 * rg + p) * ldq + col, quant8<FR>(y, sc, rc));
       });
+      v.renew();
     }
 
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float m = __builtin_fabsf(v[0][i]);
-#pragma unroll
-      for (int p = 1; p < 8; ++p) m = __builtin_fmaxf(m, __builtin_fabsf(v[p][i]));
-      red[rg][col_pos(8 * cc + i)] = m;
-    }
+    for (int i = 0; i < 4; ++i)
+      v.column_max(i, red[rg][col_pos(8 * cc + 2 * i)], red[rg][col_pos(8 * cc + 2 * i + 1)]);
     __syncthreads();
     if (t < kQtCols) {
       float m = 0.0f;
@@ -101,7 +151,7 @@ __global__ __launch_bounds__(256) void quant_grouped_kernel(const TIn* __restric
       const float sc = ssc[col_pos(c)], rc = src[col_pos(c)];
       float y[8];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) y[p] = blockwise_quotient(v[p][i], sc, rc);
+      for (int p = 0; p < 8; ++p) y[p] = blockwise_quotient(v.at(p, i), sc, rc);
       const uint2 w = make_uint2(pack4<FC>(y[0], y[1], y[2], y[3]), pack4<FC>(y[4], y[5], y[6], y[7]));
       *reinterpret_cast<uint2*>(tileT + qt_off(c, rg)) = w;
     }
