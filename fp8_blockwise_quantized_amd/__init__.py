@@ -174,11 +174,15 @@ def _stream(t):
 
 
 def _ld(t):
-    if t.dim() == 2 and t.numel() == 0:
-        return t.size(1)  # an empty matrix has no meaningful strides; the call does nothing with it
-    if t.dim() != 2 or t.stride(1) != 1:
+    if t.dim() != 2:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+    rows, cols = t.shape
+    if rows == 0 or cols == 0:
+        return cols  # an empty matrix has no meaningful strides; the call does nothing with it
+    ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError("expected a 2-D tensor with unit column stride")
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _in_type(t):

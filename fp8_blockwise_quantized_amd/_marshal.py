@@ -1,8 +1,9 @@
 """Checks and pointers of tensor arguments, one pass per tensor (a decode step's call is paid mostly on the host).
 
 Like the package's other entry points these refuse, before any launch, what the C ABI cannot see: a wrong element
-type, shape, stride or device.  The device of the call is the first tensor's; stream() refuses one that is no
-CUDA (HIP) device and comes last, so that a wrong type or shape is named first.
+type, shape, stride or device.  The device of the call is
+the first tensor's, passed around as its index (tensor.get_device(): an integer, -1 for the CPU); stream() refuses
+one that is no CUDA (HIP) device and comes last, so that a wrong type or shape is named first.
 """
 
 import torch
@@ -17,11 +18,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def stream(device):
     """The current stream of the call's device, as an integer."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors must be on a CUDA (HIP) device, not {device}")
-    if _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA (HIP) device")
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _refuse(t, name, shape, dtypes, device):
@@ -31,14 +30,14 @@ def _refuse(t, name, shape, dtypes, device):
         raise TypeError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
+    raise ValueError(f"{name} is on {t.device}, the call's first tensor elsewhere")
 
 
 def matrix(t, name, shape, dtypes, device):
     """(address, leading dimension) of a matrix of the given shape with unit column stride; (0, 0) for None."""
     if t is None:
         return 0, 0
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.get_device() != device:
         _refuse(t, name, shape, dtypes, device)
     rows, cols = shape
     if rows == 0 or cols == 0:
@@ -53,7 +52,7 @@ def scale_words(t, name, shape, device):
     """(address, leading dimension in words) of scales [words, rows, 4]; (0, 0) for None."""
     if t is None:
         return 0, 0
-    if not isinstance(t, torch.Tensor) or t.dtype not in U8 or t.shape != shape or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype not in U8 or t.shape != shape or t.get_device() != device:
         _refuse(t, name, shape, U8, device)
     words, rows, _ = shape
     if words == 0 or rows == 0:
@@ -70,7 +69,7 @@ def experts(offsets, device):
         raise TypeError("offsets must be a torch tensor")
     if offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous 1-D tensor of E + 1 entries")
-    if offsets.dtype not in I64 or offsets.device != device:
+    if offsets.dtype not in I64 or offsets.get_device() != device:
         _refuse(offsets, "offsets", offsets.shape, I64, device)
     return offsets.data_ptr(), offsets.shape[0] - 1
 
@@ -83,8 +82,8 @@ def space(ws, device):
         raise TypeError("ws must be a torch tensor or None")
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
-    if ws.device != device:
-        raise ValueError(f"ws is on {ws.device}, the call's tensors on {device}")
+    if ws.get_device() != device:
+        raise ValueError(f"ws is on {ws.device}, the call's tensors elsewhere")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 

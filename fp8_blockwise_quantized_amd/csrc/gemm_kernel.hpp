@@ -165,6 +165,8 @@ struct GroupArgs {
 template <>
 struct GroupArgs<kGroupNone> {};
 
+enum GroupPart : int { kPartAll = 0, kPartTall = 1, kPartRest = 2 };
+
 struct GroupUnit : Unit {
   int mend, nend;    // ends of the unit's A rows and B rows
   int bkb;           // contraction blocks by which B's columns are ahead of A's
@@ -173,8 +175,9 @@ struct GroupUnit : Unit {
 };
 
 // The unit u of a grouped product (units of all experts in expert order, remapped over the XCDs as in
-// tile_of; within an expert the row-grouped tile order).
-template <int GM, int BM, int BN>
+// tile_of; within an expert the row-grouped tile order).  PART: kPartTall or kPartRest take an expert's row tiles of
+// tall_tiles() or the one short tile after them.
+template <int GM, int BM, int BN, int PART = kPartAll>
 __device__ __forceinline__ GroupUnit group_unit_of(uint32_t u, const uint32_t* units, const int* starts, int E,
                                                    int M, int N, int nkb, int lane) {
   const uint32_t U = units[E];
@@ -185,7 +188,10 @@ __device__ __forceinline__ GroupUnit group_unit_of(uint32_t u, const uint32_t* u
   const uint32_t w = Lx - units[e];
   const int s0 = starts[e], s1 = starts[e + 1];
   const uint32_t tiles_n = (uint32_t)((N + BN - 1) / BN);
-  const uint32_t tiles_m = GM == kGroupContract ? (uint32_t)((M + BM - 1) / BM) : (uint32_t)((s1 - s0 + BM - 1) / BM);
+  const uint32_t tiles_m = GM == kGroupContract ? (uint32_t)((M + BM - 1) / BM)
+                           : PART == kPartAll   ? (uint32_t)((s1 - s0 + BM - 1) / BM)
+                           : PART == kPartTall  ? (uint32_t)tall_tiles(s1 - s0)
+                                                : 1u;
   const uint32_t group = (uint32_t)kGroupRows * tiles_n;
   const uint32_t gid = w / group;
   const uint32_t first = gid * kGroupRows;
@@ -202,7 +208,7 @@ __device__ __forceinline__ GroupUnit group_unit_of(uint32_t u, const uint32_t* u
     r.kb1 = __builtin_amdgcn_readfirstlane(s1);
     r.crow = (int64_t)__builtin_amdgcn_readfirstlane(e) * M;
   } else {
-    r.m0 = __builtin_amdgcn_readfirstlane(s0) + tm * BM;
+    r.m0 = __builtin_amdgcn_readfirstlane(s0 + (PART == kPartRest ? kTall * tall_tiles(s1 - s0) : 0)) + tm * BM;
     r.mend = __builtin_amdgcn_readfirstlane(s1);
     r.kb0 = 0;
     r.kb1 = nkb;
@@ -242,10 +248,20 @@ struct StageMinBlocks {
   static constexpr int value = NW != 4 ? 1 : 4 * NSTAGE * kStage <= 160 * 1024 ? 4 : 2 * NSTAGE * kStage <= 160 * 1024 ? 2 : 1;
 };
 
-template <int OP, int BM, int BN, int WGM, int WGN, int NSTAGE, int SBM, int FA, int FB, int OUTF32, int GM = kGroupNone>
-__global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, NSTAGE>::value)) void gemm_tn_kernel(
-    GemmDesc d, uint32_t tiles_m, uint32_t tiles_n, int nsplit, float* __restrict__ partial, GroupArgs<GM> grp) {
+template <int BM, int BN, int NSTAGE, int SBM>
+constexpr int ring_bytes() {
+  constexpr int NSB = SBM == kSbColumn ? BN : ((BN + kGroup - 1) / kGroup);
+  return NSTAGE * ((BM + BN) * 128 + BM * 4 + (NSB > 64 ? NSB : 64) * 4 + 256);
+}
+
+// The work units first, first + G, ... below U of one tile shape.  smem: the ring, ring_bytes() long; gunits and
+// gstarts: the table of a grouped product.
+template <int OP, int BM, int BN, int WGM, int WGN, int NSTAGE, int SBM, int FA, int FB, int OUTF32, int GM, int PART>
+__device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_m, uint32_t tiles_n, int nsplit,
+                                              float* __restrict__ partial, const GroupArgs<GM>& grp, uint8_t* smem,
+                                              const uint32_t* gunits, const int* gstarts, uint32_t U, uint32_t first) {
   constexpr int NW = WGM * WGN;
+  constexpr bool GROUPED = GM != kGroupNone;
   constexpr int WTM = BM / WGM;
   constexpr int WTN = BN / WGN;
   constexpr int MI = WTM / 16;
@@ -270,10 +286,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   static_assert(SBM != kSbBlock128 || WTN <= 128, "a wave's columns must share one weight block");
   static_assert(SBM != kSbBlock128 || BN % kGroup == 0 || kGroup % BN == 0, "a narrow tile lies in one weight block");
   static_assert(NSTAGE >= 2 && NSTAGE * STAGE <= 160 * 1024, "LDS ring does not fit");
-  // (the table of a grouped product lies in the same array: a second __shared__ object makes the compiler
-  // wait for every LDS-DMA load in flight before each LDS read)
-  constexpr bool GROUPED = GM != kGroupNone;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NSTAGE * STAGE + (GROUPED ? kGroupTableBytes : 0)];
+  static_assert(ring_bytes<BM, BN, NSTAGE, SBM>() == NSTAGE * STAGE, "ring size");
 
   const int t = threadIdx.x;
   const int lane = t & 63;
@@ -283,37 +296,10 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   const int nkb = (int)(d.K / kGroup);
   const uint32_t G = gridDim.x;
 
-  // grouped: the table of unit counts and of row (or contraction block) starts per expert
   using UnitT = std::conditional_t<GROUPED, GroupUnit, Unit>;
-  uint32_t* gunits = reinterpret_cast<uint32_t*>(smem + NSTAGE * STAGE);
-  int* gstarts = reinterpret_cast<int*>(gunits + kMaxExperts + 1);
-  uint32_t U = tiles_m * tiles_n * (uint32_t)nsplit;
-  if constexpr (GROUPED) {
-    if (wid == 0) {
-      if constexpr (GM == kGroupContract)
-        group_table_blocks(grp.offsets, grp.experts, grp.tokens, tiles_m * tiles_n, gstarts, gunits, lane);
-      else
-        group_table_rows(grp.offsets, grp.experts, grp.tokens, BM, tiles_n, gstarts, gunits, lane);
-    }
-    __syncthreads();
-    U = __builtin_amdgcn_readfirstlane(gunits[grp.experts]);
-    if constexpr (GM == kGroupContract && OUTF32 != 2) {
-      // an expert without tokens has a zero gradient: its slice of C, spread over the workgroups
-      for (int e = 0; e < grp.experts; ++e) {
-        if (gstarts[e + 1] != gstarts[e]) continue;
-        const int64_t chunks = N / (OUTF32 ? 4 : 8);
-        for (int64_t i = (int64_t)blockIdx.x * (NW * 64) + t; i < M * chunks; i += (int64_t)G * (NW * 64)) {
-          const int64_t r = i / chunks, c = i - r * chunks;
-          uint8_t* p = (uint8_t*)d.c + ((int64_t)e * M + r) * d.ldc * (OUTF32 ? 4 : 2) + c * 16;
-          *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-        }
-      }
-    }
-    if (blockIdx.x >= U) return;
-  }
   auto unit_at = [&](uint32_t u) {
     if constexpr (GROUPED)
-      return group_unit_of<GM, BM, BN>(u, gunits, gstarts, grp.experts, (int)M, (int)N, nkb, lane);
+      return group_unit_of<GM, BM, BN, PART>(u, gunits, gstarts, grp.experts, (int)M, (int)N, nkb, lane);
     else
       return unit_of<BM, BN>(u, tiles_m, tiles_n, nsplit, nkb);
   };
@@ -324,9 +310,10 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
     if constexpr (GROUPED) return u.nend; else return N;
   };
 
+  if (first >= U) return;
   // load-side cursor: unit lu, block lkb, and this lane's sources for that unit as 32-bit offsets
   // from workgroup-uniform bases (rows past the end are clamped; their results are never stored)
-  uint32_t lu = blockIdx.x;
+  uint32_t lu = first;
   UnitT L = unit_at(lu);
   int lkb = L.kb0;
   bool lmore = true;
@@ -448,7 +435,6 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-  if (lu >= U) return;  // (the grid never exceeds the unit count)
   set_sources(L);
   // compute-side cursor
   uint32_t cu = lu;
@@ -688,6 +674,74 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   }
   // no direct-to-LDS load may still be writing when the workgroup's LDS is handed to the next one
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// One tile shape for all units.
+template <int OP, int BM, int BN, int WGM, int WGN, int NSTAGE, int SBM, int FA, int FB, int OUTF32, int GM = kGroupNone>
+__global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, NSTAGE>::value)) void gemm_tn_kernel(
+    GemmDesc d, uint32_t tiles_m, uint32_t tiles_n, int nsplit, float* __restrict__ partial, GroupArgs<GM> grp) {
+  constexpr int NW = WGM * WGN;
+  constexpr bool GROUPED = GM != kGroupNone;
+  constexpr int RING = ring_bytes<BM, BN, NSTAGE, SBM>();
+  // (the table of a grouped product lies in the same array: a second __shared__ object makes the compiler
+  // wait for every LDS-DMA load in flight before each LDS read)
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + (GROUPED ? kGroupTableBytes : 0)];
+  uint32_t* gunits = reinterpret_cast<uint32_t*>(smem + RING);
+  int* gstarts = reinterpret_cast<int*>(gunits + kMaxExperts + 1);
+  uint32_t U = tiles_m * tiles_n * (uint32_t)nsplit;
+  if constexpr (GROUPED) {
+    const int lane = threadIdx.x & 63;
+    if (threadIdx.x < 64) {
+      if constexpr (GM == kGroupContract)
+        group_table_blocks(grp.offsets, grp.experts, grp.tokens, tiles_m * tiles_n, gstarts, gunits, lane);
+      else
+        group_table_rows(grp.offsets, grp.experts, grp.tokens, BM, tiles_n, gstarts, gunits, lane);
+    }
+    __syncthreads();
+    U = __builtin_amdgcn_readfirstlane(gunits[grp.experts]);
+    if constexpr (GM == kGroupContract && OUTF32 != 2) {
+      // an expert without tokens has a zero gradient: its slice of C, spread over the workgroups
+      for (int e = 0; e < grp.experts; ++e) {
+        if (gstarts[e + 1] != gstarts[e]) continue;
+        const int64_t chunks = d.N / (OUTF32 ? 4 : 8);
+        for (int64_t i = (int64_t)blockIdx.x * (NW * 64) + threadIdx.x; i < d.M * chunks;
+             i += (int64_t)gridDim.x * (NW * 64)) {
+          const int64_t r = i / chunks, c = i - r * chunks;
+          uint8_t* p = (uint8_t*)d.c + ((int64_t)e * d.M + r) * d.ldc * (OUTF32 ? 4 : 2) + c * 16;
+          *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+  }
+  gemm_tn_units<OP, BM, BN, WGM, WGN, NSTAGE, SBM, FA, FB, OUTF32, GM, kPartAll>(d, tiles_m, tiles_n, nsplit, partial,
+                                                                                 grp, smem, gunits, gstarts, U,
+                                                                                 blockIdx.x);
+}
+
+// Grouped rows with 256 x 256 tiles and, for an expert's last rows where at most 128 are left, one 128 x 256 tile:
+// a 256-row tile there would multiply more rows that do not exist than rows that do (a quarter of all rows with
+// 512 tokens an expert).  A workgroup takes its tall units, then its short ones, counted on over both lists, so
+// that the short units fill the tall list's last round.
+template <int OP, int SBM, int FA, int FB, int OUTF32, int GM>
+__global__ __launch_bounds__(512, 2) void gemm_tn_grouped_kernel(GemmDesc d, uint32_t tiles_n, GroupArgs<GM> grp) {
+  constexpr int RING = ring_bytes<256, 256, 2, SBM>();
+  static_assert(ring_bytes<128, 256, 2, SBM>() <= RING, "one array serves both tiles");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + kGroupTableBytes + kGroupTableBytes / 2];
+  uint32_t* tall = reinterpret_cast<uint32_t*>(smem + RING);
+  uint32_t* rest = tall + kMaxExperts + 1;
+  int* starts = reinterpret_cast<int*>(rest + kMaxExperts + 1);
+  if (threadIdx.x < 64)
+    group_table_two(grp.offsets, grp.experts, grp.tokens, tiles_n, starts, tall, rest, threadIdx.x & 63);
+  __syncthreads();
+  const uint32_t U1 = __builtin_amdgcn_readfirstlane(tall[grp.experts]);
+  const uint32_t U2 = __builtin_amdgcn_readfirstlane(rest[grp.experts]);
+  const uint32_t G = gridDim.x;
+  gemm_tn_units<OP, 256, 256, 2, 4, 2, SBM, FA, FB, OUTF32, GM, kPartTall>(d, 0, tiles_n, 1, nullptr, grp, smem, tall,
+                                                                           starts, U1, blockIdx.x);
+  __syncthreads();  // (the ring is filled again)
+  const uint32_t past = blockIdx.x < U1 ? (U1 - 1 - blockIdx.x) / G * G + G + blockIdx.x : blockIdx.x;
+  gemm_tn_units<OP, 128, 256, 2, 4, 2, SBM, FA, FB, OUTF32, GM, kPartRest>(d, 0, tiles_n, 1, nullptr, grp, smem, rest,
+                                                                           starts, U2, past - U1);
 }
 
 }  // namespace fp8bq

@@ -93,6 +93,30 @@ __device__ __forceinline__ void group_table_rows(const int64_t* offsets, int E, 
   group_sums(c, E, lane, units);
 }
 
+// Row tiles of an expert's n tokens when its last tile may be short: tall tiles of 256 rows, and one of 128 where
+// 1 to 128 rows are left after them.
+constexpr int kTall = 256, kShort = 128;
+__device__ __forceinline__ int tall_tiles(int n) { return n / kTall + (n % kTall > kShort ? 1 : 0); }
+__device__ __forceinline__ int short_tiles(int n) { return n % kTall > 0 && n % kTall <= kShort ? 1 : 0; }
+
+// As group_table_rows for both lists.
+__device__ __forceinline__ void group_table_two(const int64_t* offsets, int E, int64_t T, uint32_t tiles_n,
+                                                int* starts, uint32_t* tall, uint32_t* rest, int lane) {
+  int o[kExpertsPerLane + 1];
+  group_offsets(offsets, E, T, lane, o);
+  uint32_t a[kExpertsPerLane], b[kExpertsPerLane];
+#pragma unroll
+  for (int i = 0; i < kExpertsPerLane; ++i) {
+    const int j = kExpertsPerLane * lane + i;
+    if (j <= E) starts[j] = o[i];
+    a[i] = (uint32_t)tall_tiles(o[i + 1] - o[i]) * tiles_n;
+    b[i] = (uint32_t)short_tiles(o[i + 1] - o[i]) * tiles_n;
+  }
+  if (lane == 63 && E == kMaxExperts) starts[E] = o[kExpertsPerLane];
+  group_sums(a, E, lane, tall);
+  group_sums(b, E, lane, rest);
+}
+
 // The lane's counts of 128-token blocks, for tokens padded to whole blocks per expert.
 __device__ __forceinline__ void group_block_counts(const int (&o)[kExpertsPerLane + 1],
                                                    uint32_t (&c)[kExpertsPerLane]) {

@@ -15,7 +15,14 @@ static hipError_t launch_tile(const GemmDesc& d, const GroupDesc& g, const GemmP
 template <int OP, int SBM, int FA, int FB, int OUTF32, int GM>
 static hipError_t launch_shape(const GemmDesc& d, const GroupDesc& g, const GemmPlan& p, hipStream_t st) {
   switch (p.shape) {
-    case k256x256: return launch_tile<OP, 256, 256, 2, 4, SBM, FA, FB, OUTF32, GM>(d, g, p, st);
+    case k256x256:
+      if constexpr (GM == kGroupContract) {
+        return launch_tile<OP, 256, 256, 2, 4, SBM, FA, FB, OUTF32, GM>(d, g, p, st);
+      } else {
+        hipLaunchKernelGGL((gemm_tn_grouped_kernel<OP, SBM, FA, FB, OUTF32, GM>), dim3((unsigned)p.grid), dim3(512), 0,
+                           st, d, (uint32_t)p.tiles_n, GroupArgs<GM>{g.offsets, g.experts, g.tokens});
+        return hipGetLastError();
+      }
     case k64x64: return launch_tile<OP, 64, 64, 4, 1, SBM, FA, FB, OUTF32, GM>(d, g, p, st);
     default: return launch_tile<OP, 128, 128, 2, 2, SBM, FA, FB, OUTF32, GM>(d, g, p, st);
   }

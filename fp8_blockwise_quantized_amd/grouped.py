@@ -53,7 +53,7 @@ def _out(t, accumulate=False):
 @_entry
 def fp8bq_quantize_act_grouped(x, offsets, fmt_rows, q, s, fmt_cols, qt, st):
     T, C = x.shape
-    dev = x.device
+    dev = x.get_device()
     op, E = experts(offsets, dev)
     padded = qt.shape[1]
     xp, ldx = matrix(x, "x", (T, C), HI, dev)
@@ -68,7 +68,7 @@ def fp8bq_quantize_act_grouped(x, offsets, fmt_rows, q, s, fmt_cols, qt, st):
 @_entry
 def fp8bq_grouped_gemm_fprop(qx, sx, fx, offsets, qw, sw, fw, y):
     T, K = qx.shape
-    dev = qx.device
+    dev = qx.get_device()
     op, E = experts(offsets, dev)
     N = stacked(qw.shape[0], E, "qw")
     qxp, ldqx = matrix(qx, "qx", (T, K), U8, dev)
@@ -82,7 +82,7 @@ def fp8bq_grouped_gemm_fprop(qx, sx, fx, offsets, qw, sw, fw, y):
 @_entry
 def fp8bq_grouped_gemm_dgrad(qdy, sdy, fdy, offsets, qwt, sw, fw, dx):
     T, N = qdy.shape
-    dev = qdy.device
+    dev = qdy.get_device()
     op, E = experts(offsets, dev)
     K = qwt.shape[0]
     qdyp, ldqdy = matrix(qdy, "qdy", (T, N), U8, dev)
@@ -96,7 +96,7 @@ def fp8bq_grouped_gemm_dgrad(qdy, sdy, fdy, offsets, qwt, sw, fw, dx):
 @_entry
 def fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=False):
     N, padded = qdyt.shape
-    dev = qdyt.device
+    dev = qdyt.get_device()
     op, E = experts(offsets, dev)
     K = qxt.shape[0]
     qdytp, ldqdyt = matrix(qdyt, "qdyt", (N, padded), U8, dev)

@@ -24,6 +24,8 @@ Training: fprop is linear_mxfp4 (or gemm_mxfp4 on row codes); dX = gemm_mxfp4(ro
 dW = gemm_mxfp4(columns of dY, columns of X), with the quantizers' gradient taken straight through.
 """
 
+import functools
+
 import torch
 
 from . import OUT_BF16, OUT_F32, OUT_F32_ACCUM, IN_BF16, IN_F32, _RESTYPES, _SIGS, _c_i64, _c_int, _c_sz, _c_vp, _entry, lib
@@ -79,7 +81,7 @@ def _out(t, accumulate=False):
 @_entry
 def fp8bq_quantize_mxfp4(x, q, s, qt, st):
     R, C = x.shape
-    dev = x.device
+    dev = x.get_device()
     xp, ldx = matrix(x, "x", (R, C), HI, dev)
     qp, ldq = matrix(q, "q", (R, C // 2), U8, dev)
     sp, lds = scale_words(s, "s", (_words(C), R, 4), dev)
@@ -92,7 +94,7 @@ def fp8bq_quantize_mxfp4(x, q, s, qt, st):
 def fp8bq_gemm_mxfp4(qa, sa, qb, sb, c, ws=None, accumulate=False):
     M, K2 = qa.shape
     N = qb.shape[0]
-    dev = qa.device
+    dev = qa.get_device()
     W = _words(2 * K2)
     qap, ldqa = matrix(qa, "qa", (M, K2), U8, dev)
     sap, ldsa = scale_words(sa, "sa", (W, M, 4), dev)
@@ -107,7 +109,7 @@ def fp8bq_gemm_mxfp4(qa, sa, qb, sb, c, ws=None, accumulate=False):
 def fp8bq_linear_mxfp4(x, qw, sw, y, ws=None):
     M, K = x.shape
     N = qw.shape[0]
-    dev = x.device
+    dev = x.get_device()
     xp, ldx = matrix(x, "x", (M, K), HI, dev)
     qwp, ldqw = matrix(qw, "qw", (N, K // 2), U8, dev)
     swp, ldsw = scale_words(sw, "sw", (_words(K), N, 4), dev)
@@ -119,7 +121,7 @@ def fp8bq_linear_mxfp4(x, qw, sw, y, ws=None):
 @_entry
 def fp8bq_grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, y, ws=None):
     T, K2 = qa.shape
-    dev = qa.device
+    dev = qa.get_device()
     op, E = experts(offsets, dev)
     N = stacked(qw.shape[0], E, "qw")
     W = _words(2 * K2)
@@ -135,7 +137,7 @@ def fp8bq_grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, y, ws=None):
 @_entry
 def fp8bq_grouped_linear_mxfp4(x, offsets, qw, sw, y, ws=None):
     T, K = x.shape
-    dev = x.device
+    dev = x.get_device()
     op, E = experts(offsets, dev)
     N = stacked(qw.shape[0], E, "qw")
     xp, ldx = matrix(x, "x", (T, K), HI, dev)
@@ -171,7 +173,14 @@ def quantize_mxfp4_dual(x):
     return q, s, qt, st
 
 
-def _space(n, like):
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(op, device, *sizes):
+    """Workspace of an operation at these sizes: a function of the sizes and the device alone."""
+    return getattr(lib(), op)(*sizes)
+
+
+def _space(op, like, *sizes):
+    n = _ws_bytes(op, like.get_device(), *sizes)
     return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
@@ -187,7 +196,7 @@ def gemm_mxfp4(qa, sa, qb, sb, out_dtype=torch.bfloat16, out=None, ws=None, accu
     N = qb.shape[0]
     c = _output(out, M, N, out_dtype, qa)
     if ws is None:
-        ws = _space(fp8bq_gemm_mxfp4_workspace_size(M, N, 2 * K2), qa)
+        ws = _space("fp8bq_gemm_mxfp4_workspace_size", qa, M, N, 2 * K2)
     fp8bq_gemm_mxfp4(qa, sa, qb, sb, c, ws, accumulate=accumulate)
     return c
 
@@ -197,7 +206,7 @@ def linear_mxfp4(x, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     N = qw.shape[0]
     y = _output(out, M, N, out_dtype, x)
     if ws is None:
-        ws = _space(fp8bq_linear_mxfp4_workspace_size(M, N, K), x)
+        ws = _space("fp8bq_linear_mxfp4_workspace_size", x, M, N, K)
     fp8bq_linear_mxfp4(x, qw, sw, y, ws)
     return y
 
@@ -208,7 +217,7 @@ def grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, out_dtype=torch.bfloat16, out=No
     N = stacked(qw.shape[0], E, "qw")
     y = _output(out, T, N, out_dtype, qa)
     if ws is None:
-        ws = _space(fp8bq_grouped_gemm_mxfp4_workspace_size(E, T, N, 2 * K2), qa)
+        ws = _space("fp8bq_grouped_gemm_mxfp4_workspace_size", qa, E, T, N, 2 * K2)
     fp8bq_grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, y, ws)
     return y
 
@@ -219,6 +228,6 @@ def grouped_linear_mxfp4(x, offsets, qw, sw, out_dtype=torch.bfloat16, out=None,
     N = stacked(qw.shape[0], E, "qw")
     y = _output(out, T, N, out_dtype, x)
     if ws is None:
-        ws = _space(fp8bq_grouped_linear_mxfp4_workspace_size(E, T, N, K), x)
+        ws = _space("fp8bq_grouped_linear_mxfp4_workspace_size", x, E, T, N, K)
     fp8bq_grouped_linear_mxfp4(x, offsets, qw, sw, y, ws)
     return y
