@@ -40,7 +40,7 @@ static MxSpace mx_space(const MxPlan& p, bool linear, int64_t M, int64_t K) {
   return s;
 }
 static size_t mx_ws_size(bool linear, int64_t E, int64_t M, int64_t N, int64_t K) {
-  if (!mx_sizes_ok(E, M, N, K)) return 0;
+  if (K == 0 || !mx_sizes_ok(E, M, N, K)) return 0;
   return mx_space(plan_mx(linear, E, M, N, K, cus_or_default()), linear, M, K).total();
 }
 
@@ -49,7 +49,7 @@ static int run_mx(const MxArgs& g, void* ws, size_t ws_bytes, void* stream) {
   int st = validate_mx(g, &empty, &zero);
   if (st != kOk || empty) return st;
   const bool linear = g.a_type != kMxCodes;
-  const MxPlan plan = plan_mx(linear, g.E, g.M, g.N, g.K, cus_or_default());
+  const MxPlan plan = zero ? MxPlan{} : plan_mx(linear, g.E, g.M, g.N, g.K, cus_or_default());
   const MxSpace space = zero ? MxSpace{0, 0, 0} : mx_space(plan, linear, g.M, g.K);
   if ((st = check_workspace(g, ws, ws_bytes, space.total())) != kOk) return st;
   if ((st = current_device(nullptr)) != kOk) return st;

@@ -174,20 +174,29 @@ struct GroupUnit : Unit {
   int64_t ccol;
 };
 
-// The unit u of a grouped product (units of all experts in expert order, remapped over the XCDs as in
-// tile_of; within an expert the row-grouped tile order).  PART: kPartTall or kPartRest take an expert's row tiles of
+// The unit u of a grouped product.  Rows: units of all experts in expert order, remapped over the XCDs as in
+// tile_of; within an expert the row-grouped tile order.  Contraction: the long experts first (group_table_blocks), and
+// an expert's tiles dealt out over the XCDs (with 8 tile rows, a tile row each), so that no XCD has the long ones.  PART: kPartTall or kPartRest take an expert's row tiles of
 // tall_tiles() or the one short tile after them.
 template <int GM, int BM, int BN, int PART = kPartAll>
 __device__ __forceinline__ GroupUnit group_unit_of(uint32_t u, const uint32_t* units, const int* starts, int E,
                                                    int M, int N, int nkb, int lane) {
-  const uint32_t U = units[E];
-  const uint32_t q8 = U / kXcds, r8 = U % kXcds;
-  const uint32_t x = u % kXcds;
-  const uint32_t Lx = x * q8 + (x < r8 ? x : r8) + u / kXcds;
-  const int e = group_find(units, E, Lx, lane);
-  const uint32_t w = Lx - units[e];
-  const int s0 = starts[e], s1 = starts[e + 1];
   const uint32_t tiles_n = (uint32_t)((N + BN - 1) / BN);
+  int e;
+  uint32_t w;
+  if constexpr (GM == kGroupContract) {
+    const uint32_t tiles = tiles_n * (uint32_t)((M + BM - 1) / BM);
+    e = (int)units[u / tiles];
+    w = u % tiles;
+  } else {
+    const uint32_t U = units[E];
+    const uint32_t q8 = U / kXcds, r8 = U % kXcds;
+    const uint32_t x = u % kXcds;
+    const uint32_t Lx = x * q8 + (x < r8 ? x : r8) + u / kXcds;
+    e = group_find(units, E, Lx, lane);
+    w = Lx - units[e];
+  }
+  const int s0 = starts[e], s1 = starts[e + 1];
   const uint32_t tiles_m = GM == kGroupContract ? (uint32_t)((M + BM - 1) / BM)
                            : PART == kPartAll   ? (uint32_t)((s1 - s0 + BM - 1) / BM)
                            : PART == kPartTall  ? (uint32_t)tall_tiles(s1 - s0)
@@ -693,12 +702,15 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
     const int lane = threadIdx.x & 63;
     if (threadIdx.x < 64) {
       if constexpr (GM == kGroupContract)
-        group_table_blocks(grp.offsets, grp.experts, grp.tokens, tiles_m * tiles_n, gstarts, gunits, lane);
+        group_table_blocks(grp.offsets, grp.experts, grp.tokens, gstarts, gunits, lane);
       else
         group_table_rows(grp.offsets, grp.experts, grp.tokens, BM, tiles_n, gstarts, gunits, lane);
     }
     __syncthreads();
-    U = __builtin_amdgcn_readfirstlane(gunits[grp.experts]);
+    if constexpr (GM == kGroupContract)
+      U *= __builtin_amdgcn_readfirstlane(gunits[kMaxExperts]);
+    else
+      U = __builtin_amdgcn_readfirstlane(gunits[grp.experts]);
     if constexpr (GM == kGroupContract && OUTF32 != 2) {
       // an expert without tokens has a zero gradient: its slice of C, spread over the workgroups
       for (int e = 0; e < grp.experts; ++e) {

@@ -177,7 +177,7 @@ MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_c
     const int64_t steps = tiles * cdiv(K, 128);
     p.fused = linear && steps <= 300000 / (p.rows + 8) && p.rows * K <= 131072;
     p.split_k = 8;
-    while (p.split_k > cdiv(K, 256)) p.split_k /= 2;
+    while (p.split_k > 1 && p.split_k > cdiv(K, 256)) p.split_k /= 2;
     const int64_t groups = E == 0 ? 1 : used;
     const int64_t units = groups * cdiv(N, 8 / p.split_k * 16);
     p.grid = units < 16 * cus ? units : 16 * cus;

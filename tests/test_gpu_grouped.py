@@ -248,6 +248,56 @@ def test_offsets_out_of_order_stay_inside_the_matrices(offsets):
         assert torch.all(big[held] == 7)
 
 
+def test_gradients_match_differences():
+    """On values FP8 holds exactly (-1, 0, 1 and a 7 in every group: scale 1/64), y_e = x_e w_e^T is bilinear: the change
+    of sum(y dy) when one entry of x or w moves by h is h times its gradient, exactly (integers below 2^24)."""
+    say("grouped differences")
+    counts, N, K = [40, 0, 130, 1], 128, 256
+    E, T = len(counts), sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    rng = np.random.default_rng(3)
+
+    def exact(r, c):
+        v = rng.integers(-1, 2, (r, c)).astype(np.float32)
+        for i in range(r):  # a 7 in every 128 of a row, and (first row of a block of tokens, below) of a column
+            v[i, (5 * i) % 128::128] = 7.0
+        return v
+
+    x, dy, w = exact(T, K), exact(T, N), exact(E * N, K)
+    for e, n in enumerate(counts):
+        for b in range(0, n, 128):
+            x[off[e] + b], dy[off[e] + b] = 7.0, 7.0
+    offd = dev(off)
+
+    def run(x_, w_):
+        qw, sw, qwt = fq.quantize_weight_dual(dev(w_), fq.E4M3)
+        qx, sx = fq.quantize_act_1x128(dev(x_), fq.E4M3)
+        y = fq.grouped_gemm_fprop(qx, sx, offd, qw, sw, out_dtype=torch.float32)
+        return float((y.double() * dev(dy).double()).sum()), sw, qwt
+
+    base, sw, qwt = run(x, w)
+    qdy, sdy, qdyt, sdyt = fq.quantize_act_grouped_dual(dev(dy), offd)
+    qxt, sxt = fq.quantize_act_grouped_128x1(dev(x), offd)
+    dx = fq.grouped_gemm_dgrad(qdy, sdy, offd, qwt, sw, out_dtype=torch.float32).cpu().numpy()
+    dw = fq.grouped_gemm_wgrad(qdyt, sdyt, qxt, sxt, offd, out_dtype=torch.float32).cpu().numpy()
+    for e in range(E):
+        rows, we = slice(off[e], off[e + 1]), w[e * N:(e + 1) * N]
+        assert np.array_equal(dx[rows], dy[rows] @ we)
+        assert np.array_equal(dw[e * N:(e + 1) * N], dy[rows].T @ x[rows])
+    for i, j in ((3, 7), (100, 200), (169, 1)):
+        x2 = x.copy()
+        h = -1.0 if x2[i, j] > 0 else 1.0
+        assert x2[i, j] != 7.0
+        x2[i, j] += h
+        assert run(x2, w)[0] - base == h * dx[i, j]
+    for n, k in ((5, 9), (2 * N + 64, 130), (3 * N + 127, 255)):
+        w2 = w.copy()
+        h = -1.0 if w2[n, k] > 0 else 1.0
+        assert w2[n, k] != 7.0
+        w2[n, k] += h
+        assert run(x, w2)[0] - base == h * dw[n, k]
+
+
 def test_no_tokens():
     say("grouped no tokens")
     E, N, K = 3, 128, 256

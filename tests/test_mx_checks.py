@@ -108,6 +108,7 @@ def test_workspace_sizes():
     assert fq.fp8bq_linear_mxfp4_workspace_size(4096, 2048, 2048) >= 4096 * 1024 + 4096 * 64
     assert fq.fp8bq_linear_mxfp4_workspace_size(-1, 2048, 2048) == 0
     assert fq.fp8bq_linear_mxfp4_workspace_size(64, 64, 33) == 0
+    assert fq.fp8bq_linear_mxfp4_workspace_size(4, 64, 0) == 0 and fq.fp8bq_gemm_mxfp4_workspace_size(4, 64, 0) == 0
     assert fq.fp8bq_grouped_linear_mxfp4_workspace_size(0, 64, 64, 64) == 0
     assert fq.fp8bq_grouped_linear_mxfp4_workspace_size(64, 6, 2816, 2048) == 0
 
