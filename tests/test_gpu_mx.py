@@ -169,6 +169,48 @@ def test_linear_quantizes_its_input(M, N, K, dtype):
     assert float((two - y).abs().max()) <= 1e-4 * scale
 
 
+@pytest.mark.parametrize("M", [3, 90])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_takes_strided_rows(M, dtype):
+    say("mx linear strided", M, dtype)
+    N, K = 72, 256
+    big = dev(synth.random_bf16((2 * M, K + 64), 15).to(dtype))
+    qw, sw, _ = operand(2 * N, K, 16, 0.02)
+    off = dev(np.array([0, M // 2, M], np.int64))
+    for x in (big[:M, :K], big[::2, 32:K + 32]):
+        want = fq.linear_mxfp4(x.contiguous(), qw, sw)
+        assert torch.equal(fq.linear_mxfp4(x, qw, sw), want)
+        assert torch.equal(fq.grouped_linear_mxfp4(x, off, qw, sw),
+                           fq.grouped_linear_mxfp4(x.contiguous(), off, qw, sw))
+
+
+def test_two_streams_do_not_share_state():
+    """The same calls on two streams at once, each on its own tensors, give what they give one after the other."""
+    say("mx two streams")
+    N, K = 264, 544
+    qw, sw, _ = operand(4 * N, K, 17, 0.02)
+    xs = [dev(synth.random_bf16((200, K), 18 + i)) for i in range(2)]
+    offs = [dev(np.array(o, np.int64)) for o in ([0, 3, 3, 100, 200], [0, 150, 151, 199, 200])]
+
+    def step(i):
+        q, s, qt, st = fq.quantize_mxfp4_dual(xs[i])
+        return (fq.linear_mxfp4(xs[i], qw, sw), fq.gemm_mxfp4(qt, st, qt, st, out_dtype=torch.float32),
+                fq.grouped_linear_mxfp4(xs[i], offs[i], qw, sw))
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(step(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
 def test_scales_over_the_whole_range():
     """Blocks from 2^-127 up: the scales multiply exactly."""
     say("mx scales")
