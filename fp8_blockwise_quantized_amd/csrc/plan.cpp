@@ -127,8 +127,9 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
   double best = 0.0;
   for (int i = 0; i < 3; ++i) {
     const int s = shapes[i];
-    // ragged shares end half a tile short on average
-    double tiles_m = op == kOpWgrad ? (double)cdiv(rows, tile_rows(s)) : (double)share / tile_rows(s) + 0.5;
+    // ragged shares end half a tile short on average (a quarter with 256 rows, whose last tile may be a short one)
+    double tiles_m = op == kOpWgrad ? (double)cdiv(rows, tile_rows(s))
+                                    : (double)share / tile_rows(s) + (s == k256x256 ? 0.25 : 0.5);
     tiles_m = tiles_m < 1.0 ? 1.0 : tiles_m;
     const double units = (double)used * tiles_m * (double)cdiv(cols, tile_cols(s));
     const double slots = (double)(cus * blocks_per_cu(s));

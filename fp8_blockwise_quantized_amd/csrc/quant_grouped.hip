@@ -5,7 +5,9 @@
 // last block's missing tokens are zero codes, which add nothing.  Codes and scales are those of the
 // 128x1 quantizer on the expert's rows padded with zeros, and of the 1x128 quantizer, bit for bit.
 //
-// Bound by HBM (2 bytes read and 1 or 2 written per element).  A workgroup owns one 128-column group
+// Bound by HBM (2 bytes read and 1 or 2 written per element): 32768 x 2048 tokens on 32 experts take 55 us both
+// ways (4.9 TB/s of 6.05 that a copy of 1 GiB reaches; the experts' padding adds 6%), 32768 x 1408 down the columns
+// alone 25 us from the Infinity Cache and 32 us from HBM.  A workgroup owns one 128-column group
 // and walks the 128-token blocks with a stride, so the table of experts is built once per workgroup and
 // not once per block.  Thread mapping and LDS layouts are those of the dense dual quantizer.
 #include "group_table.hpp"
