@@ -677,7 +677,8 @@ def hyperball_step_batch(weights, grads, lr=1e-4, weight_decay=0.1, eps=1e-8, ra
 
 # the layer grouped by expert (include/fp8bq_grouped.h)
 from .grouped import (MAX_EXPERTS, fp8bq_grouped_gemm_dgrad, fp8bq_grouped_gemm_fprop,  # noqa: E402,F401
-                      fp8bq_grouped_gemm_wgrad, fp8bq_grouped_padded_rows, fp8bq_quantize_act_grouped,
+                      fp8bq_grouped_gemm_wgrad, fp8bq_grouped_gemm_wgrad_workspace_size,
+                      fp8bq_grouped_padded_rows, fp8bq_quantize_act_grouped,
                       grouped_gemm_dgrad, grouped_gemm_fprop, grouped_gemm_wgrad, quantize_act_grouped_128x1,
                       quantize_act_grouped_dual)
 

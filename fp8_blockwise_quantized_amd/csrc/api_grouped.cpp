@@ -9,7 +9,7 @@
 
 namespace fp8bq {
 
-static int run_grouped(const GroupedArgs& g, void* stream) {
+static int run_grouped(const GroupedArgs& g, void* ws, size_t ws_bytes, void* stream) {
   bool empty = false, zero = false;
   int st = validate_grouped(g, &empty, &zero);
   if (st != kOk || empty) return st;
@@ -21,8 +21,9 @@ static int run_grouped(const GroupedArgs& g, void* stream) {
     const int oes = g.out_t == 0 ? 2 : 4;
     return launched(launch_zero_fill(const_cast<void*>(g.out), g.E * g.N, g.K * oes, g.ldout * oes, s));
   }
-  const GemmPlan plan = plan_grouped(g.op, g.E, g.T, g.N, g.K, cus);
+  const GemmPlan plan = plan_grouped(g.op, g.E, g.T, g.N, g.K, cus, ws != nullptr);
   if (!plan.fits) return kErrShape;
+  if ((st = check_grouped_workspace(g, ws, ws_bytes, plan.ws_gemm)) != kOk) return st;
   GemmDesc d;
   d.a = (const uint8_t*)g.qa;
   d.lda = g.ldqa;
@@ -43,7 +44,8 @@ static int run_grouped(const GroupedArgs& g, void* stream) {
   d.sb_mode = g.op == kOpWgrad ? kSbColumn : kSbBlock128;
   d.sb_kstride = g.op == kOpFprop ? 1 : g.ldsb;  // fprop: sw[nb * ldsw + kb]; dgrad: sw[nb * ldsw + k / 128]
   d.sb_nstride = g.op == kOpFprop ? g.ldsb : g.op == kOpDgrad ? 1 : 0;
-  return launched(launch_grouped_gemm(g.op, d, GroupDesc{(const int64_t*)g.offsets, (int)g.E, g.T}, plan, s));
+  return launched(launch_grouped_gemm(g.op, d, GroupDesc{(const int64_t*)g.offsets, (int)g.E, g.T, plan.ws_gemm ? ws : nullptr}, plan,
+                                      s));
 }
 
 }  // namespace fp8bq
@@ -79,7 +81,7 @@ int fp8bq_grouped_gemm_fprop(int64_t E, int64_t T, int64_t N, int64_t K, const i
                              int64_t ldy, void* stream) {
   return run_grouped(GroupedArgs{kOpFprop, E, T, N, K, offsets, qx, ldqx, sx, ldsx, (int)fx, qw, ldqw, sw, ldsw,
                                  (int)fw, y, (int)yt, ldy},
-                     stream);
+                     nullptr, 0, stream);
 }
 
 int fp8bq_grouped_gemm_dgrad(int64_t E, int64_t T, int64_t N, int64_t K, const int64_t* offsets, const uint8_t* qdy,
@@ -88,16 +90,26 @@ int fp8bq_grouped_gemm_dgrad(int64_t E, int64_t T, int64_t N, int64_t K, const i
                              int64_t lddx, void* stream) {
   return run_grouped(GroupedArgs{kOpDgrad, E, T, N, K, offsets, qdy, ldqdy, sdy, ldsdy, (int)fdy, qwt, ldqwt, sw, ldsw,
                                  (int)fw, dx, (int)dxt, lddx},
-                     stream);
+                     nullptr, 0, stream);
 }
 
 int fp8bq_grouped_gemm_wgrad(int64_t E, int64_t padded, int64_t N, int64_t K, const int64_t* offsets,
                              const uint8_t* qdyt, int64_t ldqdyt, const float* sdyt, int64_t ldsdyt, fp8bq_fp8 fdy,
                              const uint8_t* qxt, int64_t ldqxt, const float* sxt, int64_t ldsxt, fp8bq_fp8 fx,
-                             void* dw, fp8bq_out dwt, int64_t lddw, void* stream) {
+                             void* dw, fp8bq_out dwt, int64_t lddw, void* ws, size_t ws_bytes, void* stream) {
   return run_grouped(GroupedArgs{kOpWgrad, E, padded, N, K, offsets, qdyt, ldqdyt, sdyt, ldsdyt, (int)fdy, qxt, ldqxt,
                                  sxt, ldsxt, (int)fx, dw, (int)dwt, lddw},
-                     stream);
+                     ws, ws_bytes, stream);
+}
+
+size_t fp8bq_grouped_gemm_wgrad_workspace_size(int64_t E, int64_t padded, int64_t N, int64_t K) {
+  const GroupedArgs g{kOpWgrad, E, padded, N, K};
+  bool empty = false, zero = false;
+  if (validate_grouped(g, &empty, &zero) != kErrNull || padded == 0) return 0;  // (sizes alone: no output pointer)
+  int cus = 0;
+  if (current_device(&cus) != kOk) cus = 0;
+  const GemmPlan p = plan_grouped(kOpWgrad, E, padded, N, K, cus);
+  return p.fits ? p.ws_gemm : 0;
 }
 
 }  // extern "C"

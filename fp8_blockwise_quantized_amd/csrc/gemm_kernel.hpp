@@ -164,6 +164,14 @@ struct GroupArgs {
 };
 template <>
 struct GroupArgs<kGroupNone> {};
+template <>
+struct GroupArgs<kGroupContract> {
+  const int64_t* offsets;
+  int experts;
+  int64_t tokens;  // padded tokens
+  GroupSplit split;
+  uint32_t* split_list;
+};
 
 enum GroupPart : int { kPartAll = 0, kPartTall = 1, kPartRest = 2 };
 
@@ -172,21 +180,25 @@ struct GroupUnit : Unit {
   int bkb;           // contraction blocks by which B's columns are ahead of A's
   int64_t crow;      // output row and column of A row m and B row n: m + crow, n + ccol
   int64_t ccol;
+  bool whole;        // else the unit's sum is partial, set `split` of the workspace
 };
 
 // The unit u of a grouped product.  Rows: units of all experts in expert order, remapped over the XCDs as in
-// tile_of; within an expert the row-grouped tile order.  Contraction: the long experts first (group_table_blocks), and
-// an expert's tiles dealt out over the XCDs (with 8 tile rows, a tile row each), so that no XCD has the long ones.  PART: kPartTall or kPartRest take an expert's row tiles of
-// tall_tiles() or the one short tile after them.
+// tile_of; within an expert the row-grouped tile order.  Contraction: the long experts first, in chunks where they are
+// split (group_table_blocks), and a chunk's tiles dealt out over the XCDs (with 8 tile rows, a tile row each), so
+// that no XCD has the long ones.  PART: kPartTall or kPartRest take an expert's row tiles of tall_tiles() or the
+// one short tile after them.
 template <int GM, int BM, int BN, int PART = kPartAll>
 __device__ __forceinline__ GroupUnit group_unit_of(uint32_t u, const uint32_t* units, const int* starts, int E,
                                                    int M, int N, int nkb, int lane) {
   const uint32_t tiles_n = (uint32_t)((N + BN - 1) / BN);
   int e;
   uint32_t w;
+  GroupEntry entry{0, 1, 0, 0};
   if constexpr (GM == kGroupContract) {
     const uint32_t tiles = tiles_n * (uint32_t)((M + BM - 1) / BM);
-    e = (int)units[u / tiles];
+    entry = entry_of((uint32_t)__builtin_amdgcn_readfirstlane((int)units[u / tiles]));
+    e = entry.expert;
     w = u % tiles;
   } else {
     const uint32_t U = units[E];
@@ -209,12 +221,18 @@ __device__ __forceinline__ GroupUnit group_unit_of(uint32_t u, const uint32_t* u
   const int tm = __builtin_amdgcn_readfirstlane((int)(first + rem % gsz));
   const int tn = __builtin_amdgcn_readfirstlane((int)(rem / gsz));
   GroupUnit r;
-  r.split = 0;
+  r.split = entry.set + entry.chunk;
+  r.whole = entry.chunks == 1;
   if constexpr (GM == kGroupContract) {
     r.m0 = tm * BM;
     r.mend = M;
     r.kb0 = __builtin_amdgcn_readfirstlane(s0);
     r.kb1 = __builtin_amdgcn_readfirstlane(s1);
+    if (entry.chunks > 1) {
+      const int b = r.kb0, n = r.kb1 - b;
+      r.kb0 = b + n * entry.chunk / entry.chunks;
+      r.kb1 = b + n * (entry.chunk + 1) / entry.chunks;
+    }
     r.crow = (int64_t)__builtin_amdgcn_readfirstlane(e) * M;
   } else {
     r.m0 = __builtin_amdgcn_readfirstlane(s0 + (PART == kPartRest ? kTall * tall_tiles(s1 - s0) : 0)) + tm * BM;
@@ -603,11 +621,16 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
         crow += C.crow;
         ccol += C.ccol;
       }
+      bool part = nsplit > 1;  // a partial sum of the contraction
+      if constexpr (GM == kGroupContract) {
+        part = !C.whole;
+        if (part) crow = mrow;
+      }
       auto write = [&](auto checked) {
         constexpr bool CHK = decltype(checked)::value;
-        if (nsplit > 1 || OUTF32) {
-          const int64_t ldc = nsplit > 1 ? N : d.ldc;
-          float* c0 = (nsplit > 1 ? partial + (int64_t)C.split * M * N : reinterpret_cast<float*>(d.c)) + crow * ldc + ccol;
+        if (part || OUTF32) {
+          const int64_t ldc = part ? N : d.ldc;
+          float* c0 = (part ? partial + (int64_t)C.split * M * N : reinterpret_cast<float*>(d.c)) + crow * ldc + ccol;
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             float* ci = c0 + 16 * i * ldc;
@@ -615,7 +638,7 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
             for (int j = 0; j < NI; ++j) {
               if (CHK && !(mrow + 16 * i < mlim && ncol + jcol(j) < nlim)) continue;
               v4f* cij = reinterpret_cast<v4f*>(ci + jcol(j));
-              if (OUTF32 == 2 && nsplit == 1)
+              if (OUTF32 == 2 && !part)
                 *cij = *cij + acc[i][j];
               else
                 *cij = acc[i][j];
@@ -694,21 +717,23 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   constexpr int RING = ring_bytes<BM, BN, NSTAGE, SBM>();
   // (the table of a grouped product lies in the same array: a second __shared__ object makes the compiler
   // wait for every LDS-DMA load in flight before each LDS read)
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + (GROUPED ? kGroupTableBytes : 0)];
+  constexpr int TABLE = GM == kGroupContract ? kContractTableBytes : GROUPED ? kGroupTableBytes : 0;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + TABLE];
   uint32_t* gunits = reinterpret_cast<uint32_t*>(smem + RING);
-  int* gstarts = reinterpret_cast<int*>(gunits + kMaxExperts + 1);
+  int* gstarts = reinterpret_cast<int*>(gunits + (GM == kGroupContract ? kMaxEntries : kMaxExperts) + 1);
   uint32_t U = tiles_m * tiles_n * (uint32_t)nsplit;
   if constexpr (GROUPED) {
     const int lane = threadIdx.x & 63;
     if (threadIdx.x < 64) {
-      if constexpr (GM == kGroupContract)
-        group_table_blocks(grp.offsets, grp.experts, grp.tokens, gstarts, gunits, lane);
-      else
+      if constexpr (GM == kGroupContract) {
+        group_table_blocks(grp.offsets, grp.experts, grp.tokens, grp.split, gstarts, gunits, lane);
+        if (grp.split.sets > 0 && blockIdx.x == 0) list_split(gunits, grp.split_list, lane);
+      } else
         group_table_rows(grp.offsets, grp.experts, grp.tokens, BM, tiles_n, gstarts, gunits, lane);
     }
     __syncthreads();
     if constexpr (GM == kGroupContract)
-      U *= __builtin_amdgcn_readfirstlane(gunits[kMaxExperts]);
+      U *= __builtin_amdgcn_readfirstlane(gunits[kMaxEntries]);
     else
       U = __builtin_amdgcn_readfirstlane(gunits[grp.experts]);
     if constexpr (GM == kGroupContract && OUTF32 != 2) {

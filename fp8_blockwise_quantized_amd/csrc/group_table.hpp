@@ -10,11 +10,16 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "plan.hpp"
+
 namespace fp8bq {
 
 constexpr int kMaxExperts = 512;
 constexpr int kExpertsPerLane = kMaxExperts / 64;
 constexpr int kGroupTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;  // unit counts and starts
+// Contraction over the tokens: a list of (expert, chunk) entries, its length, and starts.
+constexpr int kMaxEntries = kMaxExperts + kMaxSets;
+constexpr int kContractTableBytes = ((kMaxEntries + 1 + kMaxExperts + 1) * 4 + 15) / 16 * 16;
 
 // Inclusive wave scans by DPP: four shifts within the rows of 16 lanes, then each row's last lane into the
 // next row and lane 31 into the upper half.  Lanes without a source take 0, the identity of both operations.
@@ -124,13 +129,45 @@ __device__ __forceinline__ void group_block_counts(const int (&o)[kExpertsPerLan
   for (int i = 0; i < kExpertsPerLane; ++i) c[i] = (uint32_t)(o[i + 1] - o[i] + 127) / 128;
 }
 
-// starts[e] = first 128-token block of expert e in the padded layout, at most padded / 128; order[0 .. n) = the
-// experts that have a block, by the bit length of their block count, most first (in expert order within one
-// length); order[kMaxExperts] = n.  Products that contract over the blocks take the long experts first: a
-// last round of long units on few workgroups is what costs most (64 experts with shares from 1/5 to 1/300:
-// 614 us in expert order, contiguous per XCD).
-__device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E, int64_t padded, int* starts,
-                                                   uint32_t* order, int lane) {
+// The longest contraction, in blocks, that a product over the tokens gives one work unit: longer experts are
+// split into chunks of about equal length.  Each lane prices one length with the counts at hand (chunk_time)
+// and the cheapest is taken, the longest of equals; the last lane's splits nothing.
+__device__ __forceinline__ float group_chunk(const int* starts, int E, const GroupSplit& split, int lane) {
+  const float s = chunk_candidate(lane);
+  const float inv = 1.0f / s;
+  ChunkSums sums;
+  for (int e = 0; e < E; ++e) sums.add(starts[e + 1] - starts[e], s, inv);
+  uint32_t t = __float_as_uint(chunk_time(sums, s, split));  // (not negative: the bits are ordered)
+  const uint32_t mine = t;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)t, d);
+    t = o < t ? o : t;
+  }
+  const int best = 63 - __clzll((long long)__ballot(mine == t));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s), best));
+}
+
+// One entry of the list: chunk `chunk` of the `chunks` (1: whole) of expert `expert`, whose partial sums begin at set
+// `set` of the workspace.
+struct GroupEntry {
+  int expert, chunks, chunk, set;
+};
+__device__ __forceinline__ uint32_t pack_entry(int expert, int chunks, int chunk, int set) {
+  static_assert(kMaxExperts <= 512 && kMaxSets <= 64, "fields of an entry");
+  return (uint32_t)expert | (uint32_t)(chunks - 1) << 9 | (uint32_t)chunk << 15 | (uint32_t)set << 21;
+}
+__device__ __forceinline__ GroupEntry entry_of(uint32_t v) {
+  return GroupEntry{(int)(v & 511), (int)(v >> 9 & 63) + 1, (int)(v >> 15 & 63), (int)(v >> 21 & 63)};
+}
+
+// starts[e] = first 128-token block of expert e in the padded layout, at most padded / 128; order[0 .. n) = the chunks
+// (GroupEntry) of the experts that have a block, by the bit length of the chunk's block count, most first (in
+// expert order within one length); order[kMaxEntries] = n.  Products that contract over the blocks take the long
+// chunks first: a last round of long units on few workgroups is what costs most (64 experts with shares from
+// 1/5 to 1/300: 614 us in expert order, contiguous per XCD, and 402 us so).
+__device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E, int64_t padded,
+                                                   const GroupSplit& split, int* starts, uint32_t* order, int lane) {
   int o[kExpertsPerLane + 1];
   group_offsets(offsets, E, padded, lane, o);
   uint32_t c[kExpertsPerLane];
@@ -140,7 +177,6 @@ __device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E
   for (int i = 0; i < kExpertsPerLane; ++i) mine += c[i];
   uint32_t at = wave_scan_add(mine) - mine;
   const uint32_t cap = (uint32_t)(padded / 128);
-  uint32_t lengths = 0;  // bit l: an expert of mine has a count of l + 1 bits
 #pragma unroll
   for (int i = 0; i < kExpertsPerLane; ++i) {
     const int j = kExpertsPerLane * lane + i;
@@ -149,9 +185,32 @@ __device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E
     const uint32_t b1 = at < cap ? at : cap;
     if (j <= E) starts[j] = (int)b0;
     c[i] = b1 - b0;
-    if (c[i]) lengths |= 1u << (31 - __clz((int)c[i]));
   }
   if (lane == 63 && E == kMaxExperts) starts[E] = (int)(at < cap ? at : cap);
+  int chunks[kExpertsPerLane];
+  uint32_t sets = 0;  // partial sums of my experts
+#pragma unroll
+  for (int i = 0; i < kExpertsPerLane; ++i) chunks[i] = c[i] ? 1 : 0;
+  if (split.sets > 0) {
+    const float s = group_chunk(starts, E, split, lane), inv = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < kExpertsPerLane; ++i) {
+      chunks[i] = c[i] ? chunks_of((int)c[i], s, inv) : 0;
+      sets += chunks[i] > 1 ? (uint32_t)chunks[i] : 0u;
+    }
+  }
+  uint32_t set = wave_scan_add(sets) - sets;
+  uint32_t first[kExpertsPerLane];
+  uint32_t lengths = 0;  // bit l: an expert of mine has chunks of l + 1 bits
+#pragma unroll
+  for (int i = 0; i < kExpertsPerLane; ++i) {
+    first[i] = set;
+    if (chunks[i] > 1) {
+      set += (uint32_t)chunks[i];
+      c[i] /= (uint32_t)chunks[i];
+    }
+    if (c[i]) lengths |= 1u << (31 - __clz((int)c[i]));
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) lengths |= (uint32_t)__shfl_xor((int)lengths, d);
   uint32_t n = 0;
@@ -160,15 +219,33 @@ __device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E
     lengths &= ~(1u << l);
     uint32_t have = 0;
 #pragma unroll
-    for (int i = 0; i < kExpertsPerLane; ++i) have += c[i] && 31 - __clz((int)c[i]) == l ? 1u : 0u;
+    for (int i = 0; i < kExpertsPerLane; ++i) have += c[i] && 31 - __clz((int)c[i]) == l ? (uint32_t)chunks[i] : 0u;
     const uint32_t upto = wave_scan_add(have);
     uint32_t p = n + upto - have;
 #pragma unroll
     for (int i = 0; i < kExpertsPerLane; ++i)
-      if (c[i] && 31 - __clz((int)c[i]) == l) order[p++] = (uint32_t)(kExpertsPerLane * lane + i);
+      if (c[i] && 31 - __clz((int)c[i]) == l)
+        for (int k = 0; k < chunks[i]; ++k)
+          order[p++] = pack_entry(kExpertsPerLane * lane + i, chunks[i], k, chunks[i] > 1 ? (int)first[i] : 0);
     n += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
   }
-  if (lane == 0) order[kMaxExperts] = n;
+  if (lane == 0) order[kMaxEntries] = n;
+}
+
+// list[0] = experts that are split, list[1 ..] their first entries.
+__device__ __forceinline__ void list_split(const uint32_t* order, uint32_t* list, int lane) {
+  static_assert((1 + kMaxSets / 2) * 4 <= (int)kSplitListBytes, "a split expert takes two sets at least");
+  const int entries = (int)order[kMaxEntries];
+  uint32_t n = 0;
+  for (int b = 0; b < entries; b += 64) {
+    const uint32_t v = b + lane < entries ? order[b + lane] : 0;
+    const GroupEntry e = entry_of(v);
+    const bool take = e.chunks > 1 && e.chunk == 0;
+    const uint64_t m = __ballot(take);
+    if (take) list[1 + n + __popcll(m & (((uint64_t)1 << lane) - 1))] = v;
+    n += (uint32_t)__popcll(m);
+  }
+  if (lane == 0) list[0] = n;
 }
 
 // The expert of unit u: pre[e] <= u < pre[e+1], by a count of the experts that end at or before u (all

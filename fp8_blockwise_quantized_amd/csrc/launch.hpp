@@ -90,6 +90,7 @@ struct GroupDesc {
   const int64_t* offsets;
   int experts;
   int64_t tokens;
+  void* ws;  // kOpWgrad: plan.ws_gemm bytes
 };
 hipError_t launch_grouped_gemm(int op, const GemmDesc& d, const GroupDesc& g, const GemmPlan& plan, hipStream_t st);
 

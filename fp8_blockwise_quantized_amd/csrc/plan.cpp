@@ -5,7 +5,8 @@
 
 namespace fp8bq {
 
-// FP8BQ_GEMM_TILE=<0..4> forces a tile shape (a TileShape value; tuning aid); read once.
+// FP8BQ_GEMM_TILE=<0..4> forces a tile shape (a TileShape value; tuning aid; the grouped and the MXFP4 products have the
+// shapes 0, 3 and 4 only and ignore the others); read once.
 static int forced_shape() {
   static const int v = [] {
     const char* e = std::getenv("FP8BQ_GEMM_TILE");
@@ -13,6 +14,10 @@ static int forced_shape() {
     return (x >= 0 && x <= 4) ? x : -1;
   }();
   return v;
+}
+
+static bool forced_planned_shape() {
+  return forced_shape() == k128x128 || forced_shape() == k256x256 || forced_shape() == k64x64;
 }
 
 static int64_t cdiv(int64_t a, int64_t b) { return a / b + (a % b != 0 ? 1 : 0); }  // a >= 0, b > 0
@@ -115,45 +120,86 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
   return p;
 }
 
-GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu_count) {
+// Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that
+// adds up the chunks costs 3 us, also where the counts then split nothing (32 experts, 32768 tokens, 2048 x 1408,
+// shares within a factor of 4: 171 us without, 165-170 with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).  With 62% of the tokens on
+// one expert it saves (us without and with) 363 / 199 and 112 / 34 there, 39 / 32 at 8000 tokens on 4 experts of
+// 1024 x 1024, nothing at 4096 tokens.
+constexpr int64_t kMinSplitBlocks = 48;
+
+// Splitting of the grouped wgrad's long experts with tiles of shape s: up to two sets of partial sums for every
+// expert's worth of tiles that the workgroups hold at once, none where one expert's tiles fill them or
+// where its contraction cannot be long.  A set is written and read back at about 5 TB/s.
+static GroupSplit group_split(bool may, int64_t E, int64_t padded, int64_t N, int64_t K, int64_t slots, int s) {
+  const double tiles = (double)cdiv(N, tile_rows(s)) * (double)cdiv(K, tile_cols(s));
+  const int64_t longest = (padded - 127 * E) / 128 + 1;  // (padded holds all tokens and up to 127 rows an expert)
+  GroupSplit g = {0, (float)tiles, (float)slots, (float)blocks_per_cu(s),
+                  (float)(8.0 * (double)N * (double)K / 5.0e6 / block_us(s)), (float)(3.0 / block_us(s))};
+  if (!may || longest <= kMinSplitBlocks || tiles >= (double)slots) return g;
+  const double sets = 2.0 * (double)slots / tiles + 1.0;
+  g.sets = sets < (double)kMaxSets ? (int)sets : kMaxSets;
+  return g;
+}
+
+GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu_count, bool may_split) {
   GemmPlan p;
   const int64_t cus = cu_count > 0 ? cu_count : 256;
   const int64_t used = T < E ? (T > 0 ? T : 1) : E;
   const int64_t share = cdiv(T, used);
-  const int64_t rows = op == kOpWgrad ? N : share;
   const int64_t cols = op == kOpFprop ? N : K;
-  const int64_t nkb = op == kOpWgrad ? cdiv(share, 128) : (op == kOpFprop ? K : N) / 128;
+  const int64_t nkb = (op == kOpFprop ? K : N) / 128;
   const int shapes[3] = {k256x256, k128x128, k64x64};
   double best = 0.0;
   for (int i = 0; i < 3; ++i) {
     const int s = shapes[i];
-    // ragged shares end half a tile short on average (a quarter with 256 rows, whose last tile may be a short one)
-    double tiles_m = op == kOpWgrad ? (double)cdiv(rows, tile_rows(s))
-                                    : (double)share / tile_rows(s) + (s == k256x256 ? 0.25 : 0.5);
-    tiles_m = tiles_m < 1.0 ? 1.0 : tiles_m;
-    const double units = (double)used * tiles_m * (double)cdiv(cols, tile_cols(s));
     const double slots = (double)(cus * blocks_per_cu(s));
-    const double full = (double)(int64_t)(units / slots);
-    const double frac = units / slots - full;
-    const double us = (full + (frac > 0.0 ? 0.5 * (1.0 + frac) : 0.0)) * (double)nkb * block_us(s);
+    double us;
+    if (op == kOpWgrad) {
+      // what the kernel will find, if the shares are equal
+      const GroupSplit g = group_split(may_split, E, T, N, K, (int64_t)slots, s);
+      us = 3.0e38;
+      for (int l = g.sets > 0 ? 0 : 63; l < 64; ++l) {
+        ChunkSums one;
+        one.add((int)cdiv(share, 128), chunk_candidate(l), 1.0f / chunk_candidate(l));
+        if (one.units > kMaxSets) continue;
+        one.units *= (int)used;
+        one.sets *= (int)used;
+        one.blocks *= (int)used;
+        const double t = (double)chunk_time(one, chunk_candidate(l), g) * block_us(s);
+        us = t < us ? t : us;
+      }
+    } else {
+      // ragged shares end half a tile short on average (a quarter with 256 rows, whose last tile may be a short one)
+      double tiles_m = (double)share / tile_rows(s) + (s == k256x256 ? 0.25 : 0.5);
+      tiles_m = tiles_m < 1.0 ? 1.0 : tiles_m;
+      const double units = (double)used * tiles_m * (double)cdiv(cols, tile_cols(s));
+      const double full = (double)(int64_t)(units / slots);
+      const double frac = units / slots - full;
+      us = (full + (frac > 0.0 ? 0.5 * (1.0 + frac) : 0.0)) * (double)nkb * block_us(s);
+    }
     if (i == 0 || us < best) {
       best = us;
       p.shape = s;
     }
   }
-  if (forced_shape() >= 0) p.shape = forced_shape();
+  if (forced_planned_shape()) p.shape = forced_shape();
   p.tile_m = tile_rows(p.shape);
   p.tile_n = tile_cols(p.shape);
   p.tiles_n = cdiv(cols, p.tile_n);
   p.tiles_m = op == kOpWgrad ? cdiv(N, p.tile_m) : T / p.tile_m + used;  // upper bound over the experts
-  const double units = (double)p.tiles_m * (double)p.tiles_n * (op == kOpWgrad ? (double)E : 1.0);
+  const int64_t slots = cus * blocks_per_cu(p.shape);
+  const int64_t g = slots >= 8 ? slots - slots % 8 : slots;
+  if (op == kOpWgrad) {
+    p.group_split = group_split(may_split, E, T, N, K, g, p.shape);
+    const size_t sets = (size_t)p.group_split.sets;
+    p.ws_gemm = sets > 0 ? kSplitListBytes + sets * (size_t)N * (size_t)K * 4 : 0;
+  }
+  const double units = (double)p.tiles_m * (double)p.tiles_n * (op == kOpWgrad ? (double)(E + p.group_split.sets) : 1.0);
   if (units >= 2147483647.0) {
     p.fits = false;
     return p;
   }
   p.units = (int64_t)units;
-  const int64_t slots = cus * blocks_per_cu(p.shape);
-  const int64_t g = slots >= 8 ? slots - slots % 8 : slots;
   p.grid = p.units < g ? p.units : g;
   return p;
 }
@@ -204,7 +250,7 @@ MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_c
       }
     }
   }
-  if (forced_shape() >= 0) p.shape = forced_shape();
+  if (forced_planned_shape()) p.shape = forced_shape();
   p.tiles_n = cdiv(N, tile_cols(p.shape));
   p.tiles_m = E == 0 ? cdiv(M, tile_rows(p.shape)) : M / tile_rows(p.shape) + used;
   const int64_t units = p.tiles_m * p.tiles_n * p.split_k;  // (sizes are limited by the validation)

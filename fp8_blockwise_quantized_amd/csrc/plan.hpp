@@ -31,6 +31,60 @@ inline int tile_cols(int shape) {
 inline int blocks_per_cu(int shape) { return shape == k64x64 ? 4 : shape == k128x128 ? 2 : 1; }
 constexpr int kMaxSplit = 8;
 
+// Splitting of long experts in a product grouped by expert that contracts over the tokens (wgrad).  The counts are
+// on the device, so the kernel chooses there how long a chunk of the contraction may be; the host gives it what
+// it needs for that: sets of partial sums [N, K] that the workspace holds (0: no splitting), output tiles an expert,
+// workgroups (in all and on a compute unit), and in units of one block's time what writing and adding up one set costs
+// and what the pass that adds them costs besides.  The kernel leaves its choice in the workspace for the pass that adds the sets up: two kernels that computed it apart might round
+// differently.
+constexpr int kMaxSets = 64;
+constexpr size_t kSplitListBytes = 256;  // in front of the sets: count and entries of the split experts (half the sets)
+struct GroupSplit {
+  int sets;
+  float tiles, slots, per_cu, set_cost, sum_cost;
+};
+#if defined(__HIPCC__)
+#define FP8BQ_HOST_DEVICE __host__ __device__
+#else
+#define FP8BQ_HOST_DEVICE
+#endif
+// Lengths of chunk to choose from, in blocks: 4 x 1.15^i, and one that splits nothing.
+FP8BQ_HOST_DEVICE inline float chunk_candidate(int i) {
+  return i == 63 ? 1e9f : 4.0f * __builtin_exp2f(0.2f * (float)i);
+}
+// Chunks of n > 0 blocks, none much longer than s = 1 / inv (n of them at most).
+FP8BQ_HOST_DEVICE inline int chunks_of(int n, float s, float inv) {
+  return (float)n <= s ? 1 : (int)__builtin_ceilf((float)n * inv);
+}
+struct ChunkSums {
+  int units = 0, sets = 0, blocks = 0;
+  float longest = 0.0f;
+  FP8BQ_HOST_DEVICE void add(int n, float s, float inv) {
+    if (n <= 0) return;
+    const int c = chunks_of(n, s, inv);
+    const float len = (float)n <= s ? (float)n : s;
+    units += c;
+    sets += c > 1 ? c : 0;
+    blocks += n;
+    longest = len > longest ? len : longest;
+  }
+};
+// Blocks of time of a product with those chunks: its longest chunk, or its share of all of them (each with a block's
+// time for its first loads and its output) and half a chunk for the last round; and the sets.  A block takes
+// half the time where a compute unit has one workgroup instead of as many as it holds (128 x 128 tiles 0.69 and
+// 1.2 us, 64 x 64 0.49 and 0.94).  Splitting has to be worth 3%.
+FP8BQ_HOST_DEVICE inline float chunk_time(const ChunkSums& c, float s, const GroupSplit& g) {
+  if (c.sets > g.sets) return 3.0e38f;
+  const float units = (float)c.units * g.tiles;
+  const float share = ((float)c.blocks + (float)c.units) * g.tiles / g.slots;
+  const float last = units > g.slots ? 0.5f * (float)c.blocks / (float)(c.units > 0 ? c.units : 1) : 0.0f;
+  const float on_cu = __builtin_ceilf(units * g.per_cu / g.slots);
+  const float rate = g.per_cu > 1.0f && on_cu < g.per_cu ? 0.5f + 0.5f * (on_cu - 1.0f) / (g.per_cu - 1.0f) : 1.0f;
+  const float longest = rate * (c.longest + 1.0f);
+  const float t = share + last > longest ? share + last : longest;
+  return c.sets == 0 ? 0.97f * t : t + (float)c.sets * g.set_cost + g.sum_cost;
+}
+
 struct GemmPlan {
   int shape = k128x128;
   int tile_m = 128;
@@ -41,6 +95,7 @@ struct GemmPlan {
   int64_t grid = 0;   // persistent workgroups launched
   size_t ws_gemm = 0;       // workspace for split partial sums
   size_t ws_transpose = 0;  // workspace for dgrad's transposed weight codes
+  GroupSplit group_split = {};
   // false when the product is too large for one launch (more than 2^28 - 1 output tiles of
   // 128x128, or a dgrad transpose buffer past 2^62 bytes); the plan is then empty
   bool fits = true;
@@ -54,7 +109,8 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count);
 // Plan of a product grouped by expert: tile shape and persistent grid.  op is kOpFprop, kOpDgrad or
 // kOpWgrad; T tokens on E experts; N, K as in plan_gemm.  The tokens of each expert are known on the device
 // only, so the shape is chosen for equal shares and the grid covers the most tiles any shares can give.
-GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu_count);
+// Without may_split no expert's contraction is split (no workspace).
+GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu_count, bool may_split = true);
 
 // Rows that hold T tokens with every expert's padded to whole 128-token blocks, whatever their shares.
 inline int64_t grouped_padded_rows(int64_t T, int64_t E) { return (T + 127 * (E < T ? E : T)) / 128 * 128; }

@@ -358,6 +358,21 @@ int validate_gemm(const GemmArgs& g, size_t ws_needed, bool* empty, bool* zero_f
   return kOk;
 }
 
+int check_grouped_workspace(const GroupedArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed) {
+  if (ws_needed == 0) return kOk;
+  if (ws == nullptr || ws_bytes < ws_needed) return kErrWorkspace;
+  if (((uintptr_t)ws & 15u) != 0) return kErrAlign;
+  if (ws_needed >= (size_t)1 << 62) return kErrShape;
+  const int64_t n = (int64_t)ws_needed;
+  const Mat w{ws, 1, n, n, 1};  // (wgrad: dY^T [N, T], X^T [K, T] -> dW [E N, K])
+  const Mat m[] = {Mat{g.qa, g.N, g.T, g.ldqa, 1},          Mat{g.sa, g.T / 128, g.N, g.ldsa, 4},
+                   Mat{g.qb, g.K, g.T, g.ldqb, 1},          Mat{g.sb, g.T / 128, g.K, g.ldsb, 4},
+                   Mat{g.out, g.E * g.N, g.K, g.ldout, g.out_t == 0 ? 2 : 4}, Mat{g.offsets, 1, g.E + 1, g.E + 1, 8}};
+  for (const Mat& v : m)
+    if (overlaps(w, v)) return kErrOverlap;
+  return kOk;
+}
+
 static bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
 
 int validate_grouped(const GroupedArgs& g, bool* empty, bool* zero_fill) {

@@ -114,6 +114,7 @@ struct GroupedArgs {
   const void* out; int out_t; int64_t ldout;
 };
 int validate_grouped(const GroupedArgs& g, bool* empty, bool* zero_fill);
+int check_grouped_workspace(const GroupedArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed);
 
 // Grouped token-axis quantizer, with the row quantizer when q or s is given (then both must be).
 int validate_quant_grouped(const void* x, int xt, int64_t T, int64_t C, int64_t ldx, const void* offsets, int64_t E,

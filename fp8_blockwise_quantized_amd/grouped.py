@@ -6,7 +6,8 @@ the experts' weights stacked, W [E N, K].  Raw entry points, tensors in place of
     fp8bq_quantize_act_grouped(x, offsets, fmt_rows, q, s, fmt_cols, qt, st)     (q and s may be None)
     fp8bq_grouped_gemm_fprop(qx, sx, fx, offsets, qw, sw, fw, y)
     fp8bq_grouped_gemm_dgrad(qdy, sdy, fdy, offsets, qwt, sw, fw, dx)
-    fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=False)
+    fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=False, ws=None)
+    fp8bq_grouped_gemm_wgrad_workspace_size(E, padded, N, K)   (without ws no expert's contraction is split)
     fp8bq_grouped_padded_rows(T, E)
 
 Allocating helpers:
@@ -16,16 +17,16 @@ Allocating helpers:
     grouped_gemm_fprop(qx, sx, offsets, qw, sw, fx=E4M3, fw=E4M3, out_dtype=bf16, out=None) -> y [T, N]
     grouped_gemm_dgrad(qdy, sdy, offsets, qwt, sw, fdy=E4M3, fw=E4M3, out_dtype=bf16, out=None) -> dx [T, K]
     grouped_gemm_wgrad(qdyt, sdyt, qxt, sxt, offsets, fdy=E4M3, fx=E4M3, out_dtype=bf16, out=None,
-                       accumulate=False) -> dw [E N, K]
+                       accumulate=False, ws=None) -> dw [E N, K]
 
 Rows of y and dx that belong to no expert are left as they are (undefined in a tensor made here).
 """
 
 import torch
 
-from . import (E4M3, IN_BF16, IN_F32, OUT_BF16, OUT_F32, OUT_F32_ACCUM, _c_i64, _c_int, _c_vp, _entry, _pad4, _RESTYPES,
-               _SIGS, lib)
-from ._marshal import F32, HI, U8, experts, matrix, stacked, stream
+from . import (E4M3, IN_BF16, IN_F32, OUT_BF16, OUT_F32, OUT_F32_ACCUM, _c_i64, _c_int, _c_sz, _c_vp, _entry, _pad4,
+               _RESTYPES, _SIGS, lib)
+from ._marshal import F32, HI, U8, experts, matrix, space, stacked, stream
 
 MAX_EXPERTS = 512
 
@@ -37,13 +38,19 @@ _SIGS.update({
                                    _c_i64, _c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp],
     "fp8bq_grouped_gemm_fprop": _GEMM,
     "fp8bq_grouped_gemm_dgrad": _GEMM,
-    "fp8bq_grouped_gemm_wgrad": _GEMM,
+    "fp8bq_grouped_gemm_wgrad": _GEMM[:-1] + [_c_vp, _c_sz, _c_vp],
+    "fp8bq_grouped_gemm_wgrad_workspace_size": [_c_i64] * 4,
 })
 _RESTYPES["fp8bq_grouped_padded_rows"] = _c_i64
+_RESTYPES["fp8bq_grouped_gemm_wgrad_workspace_size"] = _c_sz
 
 
 def fp8bq_grouped_padded_rows(T, E):
     return int(lib().fp8bq_grouped_padded_rows(int(T), int(E)))
+
+
+def fp8bq_grouped_gemm_wgrad_workspace_size(E, padded, N, K):
+    return lib().fp8bq_grouped_gemm_wgrad_workspace_size(E, padded, N, K)
 
 
 def _out(t, accumulate=False):
@@ -94,7 +101,7 @@ def fp8bq_grouped_gemm_dgrad(qdy, sdy, fdy, offsets, qwt, sw, fw, dx):
 
 
 @_entry
-def fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=False):
+def fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=False, ws=None):
     N, padded = qdyt.shape
     dev = qdyt.get_device()
     op, E = experts(offsets, dev)
@@ -104,8 +111,9 @@ def fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumul
     qxtp, ldqxt = matrix(qxt, "qxt", (K, padded), U8, dev)
     sxtp, ldsxt = matrix(sxt, "sxt", (padded // 128, K), F32, dev)
     dwp, lddw = matrix(dw, "dw", (E * N, K), F32 if accumulate else HI, dev)
+    wsp, ws_bytes = space(ws, dev)
     return (E, padded, N, K, op, qdytp, ldqdyt, sdytp, ldsdyt, fdy, qxtp, ldqxt, sxtp, ldsxt, fx, dwp,
-            _out(dw, accumulate), lddw, stream(dev))
+            _out(dw, accumulate), lddw, wsp, ws_bytes, stream(dev))
 
 
 def _cols_outputs(x, offsets):
@@ -147,11 +155,17 @@ def grouped_gemm_dgrad(qdy, sdy, offsets, qwt, sw, fdy=E4M3, fw=E4M3, out_dtype=
 
 
 def grouped_gemm_wgrad(qdyt, sdyt, qxt, sxt, offsets, fdy=E4M3, fx=E4M3, out_dtype=torch.bfloat16, out=None,
-                       accumulate=False):
-    """accumulate=True adds the result to `out` (an FP32 main-grad buffer) instead of overwriting it."""
+                       accumulate=False, ws=None):
+    """accumulate=True adds the result to `out` (an FP32 main-grad buffer) instead of overwriting it.  ws: a uint8
+    tensor of the workspace size (made here if None)."""
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate=True needs an FP32 `out` tensor holding the running sum")
-    dw = out if out is not None else qdyt.new_empty(((offsets.shape[0] - 1) * qdyt.shape[0], qxt.shape[0]),
-                                                    dtype=out_dtype)
-    fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=accumulate)
+    E = offsets.shape[0] - 1
+    N, padded = qdyt.shape
+    K = qxt.shape[0]
+    dw = out if out is not None else qdyt.new_empty((E * N, K), dtype=out_dtype)
+    if ws is None:
+        size = fp8bq_grouped_gemm_wgrad_workspace_size(E, padded, N, K)
+        ws = qdyt.new_empty(size) if size else None
+    fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumulate=accumulate, ws=ws)
     return dw

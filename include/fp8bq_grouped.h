@@ -81,11 +81,15 @@ int fp8bq_grouped_gemm_dgrad(int64_t E, int64_t T, int64_t N, int64_t K, const i
  *   qxt/sxt    from fp8bq_quantize_act_grouped(X):  qxt [K, padded],  sxt [padded / 128][K].
  *   dw         [E N, K] of type dwt (BF16, FP32, or FP32 accumulated into), row stride lddw.  An expert
  *              without tokens gets zeros, or keeps its values when accumulating.
+ *   ws         NULL, or at least fp8bq_grouped_gemm_wgrad_workspace_size(E, padded, N, K) bytes, 16-byte aligned.
+ *              With it the contraction of experts with many more tokens than the others is split over several
+ *              workgroups (FP32 partial sums, added in a fixed order); without it no expert's is.
  */
+size_t fp8bq_grouped_gemm_wgrad_workspace_size(int64_t E, int64_t padded, int64_t N, int64_t K);
 int fp8bq_grouped_gemm_wgrad(int64_t E, int64_t padded, int64_t N, int64_t K, const int64_t* offsets,
                              const uint8_t* qdyt, int64_t ldqdyt, const float* sdyt, int64_t ldsdyt, fp8bq_fp8 fdy,
                              const uint8_t* qxt, int64_t ldqxt, const float* sxt, int64_t ldsxt, fp8bq_fp8 fx,
-                             void* dw, fp8bq_out dwt, int64_t lddw, void* stream);
+                             void* dw, fp8bq_out dwt, int64_t lddw, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

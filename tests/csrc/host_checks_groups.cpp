@@ -68,7 +68,34 @@ static void check_plan(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, 
   }
 }
 
+// Splitting of long experts: a chunk is never empty, no more sets are taken than there are, and the choice that
+// splits nothing is always open.
+static void check_chunks() {
+  for (int i = 0; i < 64; ++i) {
+    const float s = chunk_candidate(i);
+    EXPECT(s >= 4.0f && (i == 0 || s > chunk_candidate(i - 1)));
+    for (int n = 1; n < 1 << 24; n += 1 + n / 7) {
+      const int c = chunks_of(n, s, 1.0f / s);
+      EXPECT(c >= 1 && c <= n && (i != 63 || c == 1) && (double)n / c <= 1.001 * s);
+    }
+  }
+  for (int it = 0; it < 20000; ++it) {
+    const GroupSplit g{(int)(rng() % (kMaxSets + 1)), (float)(1 + rng() % 600), 512.0f, (float)(1 << rng() % 3),
+                       (float)(rng() % 1000) / 100.0f, 2.5f};
+    int n[40];
+    const int E = 1 + (int)(rng() % 40);
+    for (int e = 0; e < E; ++e) n[e] = rng() % 3 ? (int)(rng() % 10) : (int)(rng() % 3000);
+    for (int i = 0; i < 64; ++i) {
+      ChunkSums c;
+      for (int e = 0; e < E; ++e) c.add(n[e], chunk_candidate(i), 1.0f / chunk_candidate(i));
+      const float t = chunk_time(c, chunk_candidate(i), g);
+      EXPECT(t >= 0.0f && (c.sets <= g.sets ? t < 1e30f : t > 1e30f) && (i != 63 || c.sets == 0));
+    }
+  }
+}
+
 int main() {
+  check_chunks();
   bool empty = false, zero = false;
   for (int it = 0; it < 300000; ++it) {
     const int64_t E = pick_experts(), T = pick_size(), N = pick_size(), K = pick_size();
@@ -80,6 +107,11 @@ int main() {
     if (st == kOk && !empty && !zero) {
       const GemmPlan p = plan_grouped(g.op, E, T, N, K, cus);
       if (p.fits) EXPECT(p.grid >= 1 && p.grid <= p.units && p.units < ((int64_t)1 << 31));
+      const int64_t sets = p.group_split.sets;
+      EXPECT(sets >= 0 && sets <= kMaxSets && (g.op == kOpWgrad || sets == 0));
+      if (p.fits) EXPECT(p.ws_gemm == (sets ? kSplitListBytes + (size_t)sets * (size_t)N * (size_t)K * 4 : 0));
+      EXPECT(plan_grouped(g.op, E, T, N, K, cus, false).ws_gemm == 0);
+      EXPECT(documented(check_grouped_workspace(g, pick_ptr(), (size_t)pick_size(), p.ws_gemm)));
     }
     if (T >= 0 && T < ((int64_t)1 << 30) && E >= 1 && E <= kMaxGroupExperts) {
       const int64_t padded = grouped_padded_rows(T, E);
@@ -126,6 +158,10 @@ int main() {
   EXPECT(plan_mx(true, 0, 1, 11264, 2048, 256).fused);
   EXPECT(!plan_mx(true, 0, 16384, 11264, 2048, 256).skinny && plan_mx(true, 0, 16384, 11264, 2048, 256).shape == k256x256);
   EXPECT(plan_grouped(kOpFprop, 64, 32768, 2816, 2048, 256).shape == k256x256);
+  // one expert with everything and few tiles is split, the tiles of one expert that fill the card are not
+  EXPECT(plan_grouped(kOpWgrad, 1, 30080, 256, 256, 256).group_split.sets > 8);
+  EXPECT(plan_grouped(kOpWgrad, 8, 32768, 5632, 4096, 256).group_split.sets == 0);
+  EXPECT(plan_grouped(kOpWgrad, 8, 1920, 2048, 1408, 256).group_split.sets == 0);
   if (failures) {
     std::fprintf(stderr, "%d failures\n", failures);
     return 1;

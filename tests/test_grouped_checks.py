@@ -26,20 +26,22 @@ def quant(x=P(0), xt=0, T=T, C=K, ldx=K, off=P(9), E=E, fr=0, q=P(1), ldq=K, s=P
 
 
 def gemm(op="fprop", E=E, T=T, N=N, K=K, off=P(9), a=P(0), lda=None, sa=P(1), ldsa=None, fa=0, b=P(2), ldb=None,
-         sb=P(3), ldsb=None, fb=0, out=P(4), ot=0, ldo=None):
+         sb=P(3), ldsb=None, fb=0, out=P(4), ot=0, ldo=None, ws=NUL, ws_bytes=0):
     if op == "wgrad":
         T = TP if T == 300 else T
     d = {"fprop": (K, 304, K, 3, N), "dgrad": (N, 304, E * N, 3, K), "wgrad": (T, N, T, K, K)}[op]
     lda, ldsa, ldb, ldsb, ldo = (v if v is not None else w for v, w in zip((lda, ldsa, ldb, ldsb, ldo), d))
+    space = (ws, ws_bytes) if op == "wgrad" else ()
     return getattr(fq.lib(), "fp8bq_grouped_gemm_" + op)(E, T, N, K, off, a, lda, sa, ldsa, fa, b, ldb, sb, ldsb, fb,
-                                                         out, ot, ldo, NUL)
+                                                         out, ot, ldo, *space, NUL)
 
 
 def test_header_and_binding_agree():
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "fp8bq_grouped.h")).read(), flags=re.S)
     names = set(re.findall(r"\b(fp8bq_[a-z0-9_]+)\s*\(", text))
     assert names == {"fp8bq_grouped_padded_rows", "fp8bq_quantize_act_grouped", "fp8bq_grouped_gemm_fprop",
-                     "fp8bq_grouped_gemm_dgrad", "fp8bq_grouped_gemm_wgrad"}
+                     "fp8bq_grouped_gemm_dgrad", "fp8bq_grouped_gemm_wgrad",
+                     "fp8bq_grouped_gemm_wgrad_workspace_size"}
     for n in names:
         assert hasattr(fq, n) and hasattr(fq.lib(), n)
 
@@ -84,6 +86,20 @@ def test_product_refusals_of_one_op():
     assert gemm("fprop", ot=2) == DTYPE and gemm("dgrad", ot=2) == DTYPE
     assert gemm("wgrad", T=700) == SHAPE
     assert gemm("fprop", K=0) == SHAPE and gemm("dgrad", N=0) == SHAPE
+
+
+def test_weight_gradient_workspace():
+    """Needed only to split long experts: absent for few tokens, refused when too small, misaligned or shared."""
+    size = fq.fp8bq_grouped_gemm_wgrad_workspace_size
+    assert size(4, 768, 256, 384) == 0 and size(4, 0, 256, 384) == 0
+    for bad in ((0, 8192, 128, 128), (513, 8192, 128, 128), (4, 8200, 128, 128), (4, 8192, 100, 128), (4, -128, 128, 128)):
+        assert size(*bad) == 0
+    n = size(4, 8192, 128, 256)
+    assert n > 0 and (n - 256) % (128 * 256 * 4) == 0
+    if HAVE_GPU:
+        return  # (fake pointers)
+    big = dict(E=4, T=8192, N=128, K=256)
+    assert gemm("wgrad", **big) == DEVICE and gemm("wgrad", ws=P(5), ws_bytes=n, **big) == DEVICE
 
 
 def test_padded_rows_hold_any_shares():
