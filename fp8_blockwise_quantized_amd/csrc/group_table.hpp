@@ -132,12 +132,12 @@ __device__ __forceinline__ void group_block_counts(const int (&o)[kExpertsPerLan
 // The longest contraction, in blocks, that a product over the tokens gives one work unit: longer experts are
 // split into chunks of about equal length.  Each lane prices one length with the counts at hand (chunk_time)
 // and the cheapest is taken, the longest of equals; the last lane's splits nothing.
-__device__ __forceinline__ float group_chunk(const int* starts, int E, const GroupSplit& split, int lane) {
+__device__ __forceinline__ float group_chunk(const int* starts, int E, int longest, const GroupSplit& split, int lane) {
   const float s = chunk_candidate(lane);
   const float inv = 1.0f / s;
-  ChunkSums sums;
+  ChunkSums sums(longest, s);
   for (int e = 0; e < E; ++e) sums.add(starts[e + 1] - starts[e], s, inv);
-  uint32_t t = __float_as_uint(chunk_time(sums, s, split));  // (not negative: the bits are ordered)
+  uint32_t t = __float_as_uint(chunk_time(sums, split));  // (not negative: the bits are ordered)
   const uint32_t mine = t;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -192,11 +192,24 @@ __device__ __forceinline__ void group_table_blocks(const int64_t* offsets, int E
 #pragma unroll
   for (int i = 0; i < kExpertsPerLane; ++i) chunks[i] = c[i] ? 1 : 0;
   if (split.sets > 0) {
-    const float s = group_chunk(starts, E, split, lane), inv = 1.0f / s;
+    int longest = 0, used = 0, blocks = 0;
 #pragma unroll
     for (int i = 0; i < kExpertsPerLane; ++i) {
-      chunks[i] = c[i] ? chunks_of((int)c[i], s, inv) : 0;
-      sets += chunks[i] > 1 ? (uint32_t)chunks[i] : 0u;
+      longest = (int)c[i] > longest ? (int)c[i] : longest;
+      used += chunks[i];
+      blocks += (int)c[i];
+    }
+    longest = __builtin_amdgcn_readlane(wave_scan_max(longest), 63);
+    const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)wave_scan_add((uint32_t)(used + blocks)), 63);
+    // While the longest is well below a workgroup's share of the blocks, whole experts balance: nothing to choose
+    // (the choice takes some 50 instructions an expert).
+    if ((float)longest > 0.4f * (float)all * split.tiles / split.slots) {
+      const float s = group_chunk(starts, E, longest, split, lane), inv = 1.0f / s;
+#pragma unroll
+      for (int i = 0; i < kExpertsPerLane; ++i) {
+        chunks[i] = c[i] ? chunks_of((int)c[i], s, inv) : 0;
+        sets += chunks[i] > 1 ? (uint32_t)chunks[i] : 0u;
+      }
     }
   }
   uint32_t set = wave_scan_add(sets) - sets;

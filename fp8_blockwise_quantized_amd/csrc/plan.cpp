@@ -121,10 +121,11 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
 }
 
 // Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that
-// adds up the chunks costs 3 us, also where the counts then split nothing (32 experts, 32768 tokens, 2048 x 1408,
-// shares within a factor of 4: 171 us without, 165-170 with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).  With 62% of the tokens on
-// one expert it saves (us without and with) 363 / 199 and 112 / 34 there, 39 / 32 at 8000 tokens on 4 experts of
-// 1024 x 1024, nothing at 4096 tokens.
+// adds up the chunks costs 3 us, also where the counts then split nothing (32 experts, 32768 tokens, 2048 x 1408, no
+// expert much above the others: 161 us without, 164 us with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).
+// Uneven experts gain more (us, whole and split): 25% (62%) of the tokens on one of the 32 experts 217 / 184
+// (358 / 204), 62% on one of the 8 experts 111 / 34, the same at 8000 tokens on 4 experts of 1024 x 1024
+// 38 / 32; at 4096 tokens nothing.
 constexpr int64_t kMinSplitBlocks = 48;
 
 // Splitting of the grouped wgrad's long experts with tiles of shape s: up to two sets of partial sums for every
@@ -159,13 +160,12 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
       const GroupSplit g = group_split(may_split, E, T, N, K, (int64_t)slots, s);
       us = 3.0e38;
       for (int l = g.sets > 0 ? 0 : 63; l < 64; ++l) {
-        ChunkSums one;
-        one.add((int)cdiv(share, 128), chunk_candidate(l), 1.0f / chunk_candidate(l));
-        if (one.units > kMaxSets) continue;
-        one.units *= (int)used;
-        one.sets *= (int)used;
-        one.blocks *= (int)used;
-        const double t = (double)chunk_time(one, chunk_candidate(l), g) * block_us(s);
+        const int n = (int)cdiv(share, 128);
+        const float len = chunk_candidate(l);
+        if ((float)n / len > (float)kMaxSets) continue;
+        ChunkSums even(n, len);
+        even.add(n, len, 1.0f / len, (int)used);
+        const double t = (double)chunk_time(even, g) * block_us(s);
         us = t < us ? t : us;
       }
     } else {

@@ -56,32 +56,52 @@ FP8BQ_HOST_DEVICE inline float chunk_candidate(int i) {
 FP8BQ_HOST_DEVICE inline int chunks_of(int n, float s, float inv) {
   return (float)n <= s ? 1 : (int)__builtin_ceilf((float)n * inv);
 }
+// The chunks of all experts, by length against the longest: over a half, over a quarter, and the others.
 struct ChunkSums {
-  int units = 0, sets = 0, blocks = 0;
-  float longest = 0.0f;
-  FP8BQ_HOST_DEVICE void add(int n, float s, float inv) {
+  float top;  // the longest chunk
+  int sets = 0;
+  int units[3] = {0, 0, 0}, blocks[3] = {0, 0, 0};
+  // longest: the most blocks of an expert
+  FP8BQ_HOST_DEVICE ChunkSums(int longest, float s) : top((float)longest < s ? (float)longest : s) {}
+  FP8BQ_HOST_DEVICE void add(int n, float s, float inv, int experts = 1) {
     if (n <= 0) return;
     const int c = chunks_of(n, s, inv);
-    const float len = (float)n <= s ? (float)n : s;
-    units += c;
-    sets += c > 1 ? c : 0;
-    blocks += n;
-    longest = len > longest ? len : longest;
+    sets += c > 1 ? experts * c : 0;
+    const float total = (float)c * top;  // the chunks' blocks if each were the longest
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const bool in = i == 0 ? 2.0f * (float)n > total : i == 1 ? 2.0f * (float)n <= total && 4.0f * (float)n > total
+                                                                : 4.0f * (float)n <= total;
+      units[i] += in ? experts * c : 0;
+      blocks[i] += in ? experts * n : 0;
+    }
   }
 };
-// Blocks of time of a product with those chunks: its longest chunk, or its share of all of them (each with a block's
-// time for its first loads and its output) and half a chunk for the last round; and the sets.  A block takes
+// Blocks of time of a product with those chunks, longest first on the workgroups in turn: everyone's share of the blocks
+// (each chunk with a block's time for its first loads and its output), half a chunk for the last round, and what the
+// longest chunk has more than the first round's average; at least the longest chunk; and the sets.  A block takes
 // half the time where a compute unit has one workgroup instead of as many as it holds (128 x 128 tiles 0.69 and
 // 1.2 us, 64 x 64 0.49 and 0.94).  Splitting has to be worth 3%.
-FP8BQ_HOST_DEVICE inline float chunk_time(const ChunkSums& c, float s, const GroupSplit& g) {
+FP8BQ_HOST_DEVICE inline float chunk_time(const ChunkSums& c, const GroupSplit& g) {
   if (c.sets > g.sets) return 3.0e38f;
-  const float units = (float)c.units * g.tiles;
-  const float share = ((float)c.blocks + (float)c.units) * g.tiles / g.slots;
-  const float last = units > g.slots ? 0.5f * (float)c.blocks / (float)(c.units > 0 ? c.units : 1) : 0.0f;
+  const int count = c.units[0] + c.units[1] + c.units[2], blocks = c.blocks[0] + c.blocks[1] + c.blocks[2];
+  const float units = (float)count * g.tiles;
+  float left = g.slots, first = 0.0f;  // the first round's workgroups and blocks
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float u = (float)c.units[i] * g.tiles, take = u < left ? u : left;
+    first += c.units[i] > 0 ? take * (float)c.blocks[i] / (float)c.units[i] : 0.0f;
+    left -= take;
+  }
+  float t = (float)(blocks + count) * g.tiles / g.slots;
+  if (units > g.slots) {
+    const float over = c.top - first / g.slots;
+    t += 0.5f * (float)blocks / (float)count + (over > 0.0f ? over : 0.0f);
+  }
   const float on_cu = __builtin_ceilf(units * g.per_cu / g.slots);
   const float rate = g.per_cu > 1.0f && on_cu < g.per_cu ? 0.5f + 0.5f * (on_cu - 1.0f) / (g.per_cu - 1.0f) : 1.0f;
-  const float longest = rate * (c.longest + 1.0f);
-  const float t = share + last > longest ? share + last : longest;
+  const float longest = rate * (c.top + 1.0f);
+  t = t > longest ? t : longest;
   return c.sets == 0 ? 0.97f * t : t + (float)c.sets * g.set_cost + g.sum_cost;
 }
 

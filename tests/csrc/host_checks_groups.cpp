@@ -2,6 +2,7 @@
 // with g++ and the address and undefined-behaviour sanitizers: random and extreme arguments never trigger
 // undefined behaviour, every status is a documented one, and every plan of accepted sizes is consistent.  Prints
 // "ok" and exits 0 on success.
+#include <algorithm>
 #include <cstdint>
 #include <cstdio>
 #include <random>
@@ -86,9 +87,9 @@ static void check_chunks() {
     const int E = 1 + (int)(rng() % 40);
     for (int e = 0; e < E; ++e) n[e] = rng() % 3 ? (int)(rng() % 10) : (int)(rng() % 3000);
     for (int i = 0; i < 64; ++i) {
-      ChunkSums c;
+      ChunkSums c(*std::max_element(n, n + E), chunk_candidate(i));
       for (int e = 0; e < E; ++e) c.add(n[e], chunk_candidate(i), 1.0f / chunk_candidate(i));
-      const float t = chunk_time(c, chunk_candidate(i), g);
+      const float t = chunk_time(c, g);
       EXPECT(t >= 0.0f && (c.sets <= g.sets ? t < 1e30f : t > 1e30f) && (i != 63 || c.sets == 0));
     }
   }
