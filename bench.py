@@ -717,7 +717,7 @@ def summarize(ops, dur_ms, med_ms=None, min_ms=None):
 
 
 # Kernel instance names as profilers print them: gemm_tn_kernel<OP, BM, BN, waves_m, waves_n, LDS
-# stages, scale mode, fmtA, fmtB, f32 out>; the tile shape comes from the library's plan query.
+# stages, scale mode, fmtA, fmtB, f32 out, group mode>; the tile shape comes from the library's plan query.
 _TILE_ARGS = {(64, 64): "64, 64, 4, 1, 2", (128, 128): "128, 128, 2, 2, 2", (128, 256): "128, 256, 2, 4, 2",
               (256, 128): "256, 128, 4, 2, 2", (256, 256): "256, 256, 2, 4, 2"}
 def gemm_kernel(fq, o):
@@ -727,7 +727,7 @@ def gemm_kernel(fq, o):
     tm, tn, split = fq.fp8bq_gemm_plan(*o["plan"])
     kop, sbm = o["kid"]
     name = (f"void fp8bq::gemm_tn_kernel<{kop}, {_TILE_ARGS[(tm, tn)]}, {sbm}, "
-            f"0, 0, 0>(fp8bq::GemmDesc, unsigned int, unsigned int, int, float*)")
+            f"0, 0, 0, 0>(fp8bq::GemmDesc, unsigned int, unsigned int, int, float*, fp8bq::GroupArgs<0>)")
     return name, split == 1
 
 
@@ -739,8 +739,9 @@ def _traffic(kernel):
         return None
     try:
         t = json.load(open(path))
-        src = open(os.path.join(ROOT, "fp8_blockwise_quantized_amd", "csrc", "gemm.hip"), "rb").read()
-        if t.get("gemm_hip_sha256") != hashlib.sha256(src).hexdigest():
+        csrc = os.path.join(ROOT, "fp8_blockwise_quantized_amd", "csrc")
+        src = b"".join(open(os.path.join(csrc, f), "rb").read() for f in ("gemm.hip", "gemm_kernel.hpp"))
+        if t.get("gemm_source_sha256") != hashlib.sha256(src).hexdigest():
             return None
         k = t.get("kernels", {}).get(kernel)
         return k.get("bytes_per_launch") if k else None

@@ -155,6 +155,12 @@ __device__ __forceinline__ Unit unit_of(uint32_t u, uint32_t tiles_m, uint32_t t
 //                   of the columns of W^T [K, E N];
 //   kGroupContract  wgrad: the contraction runs over an expert's 128-token blocks (operands quantized
 //                   along the tokens, every expert's tokens padded to whole blocks); C is stacked.
+// Bound by the matrix pipes at the clock the card's power allows, as the dense products, and by what ragged
+// experts add.  32768 tokens: fprop on 64 experts of 2816 x 2048 239 us (1.58 PFLOP/s; matrix pipes busy 45% of the
+// cycles; a tenth of the tiles' rows are past an expert's end); dgrad on 32 experts of 2048 x 1408 106 us
+// (the dense product of the same size 94-112), 115 us with the largest expert 2.5 times the average; wgrad there
+// 148 and 160 us (dense, contracted in one piece: 125-135): 32 times the outputs, 184 MB, which all workgroups
+// write at the end of a round while no matrix pipe works, about 9 us a round.
 enum GroupMode : int { kGroupNone = 0, kGroupRowsMode = 1, kGroupWindow = 2, kGroupContract = 3 };
 template <int GM>
 struct GroupArgs {
@@ -757,8 +763,9 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
 
 // Grouped rows with 256 x 256 tiles and, for an expert's last rows where at most 128 are left, one 128 x 256 tile:
 // a 256-row tile there would multiply more rows that do not exist than rows that do (a quarter of all rows with
-// 512 tokens an expert; 32 experts, 32768 tokens, 2048 x 1408: 123 us with 256-row tiles alone, 113 us so).  A workgroup takes its tall units, then its short ones, counted on over both lists, so
-// that the short units fill the tall list's last round.
+// 512 tokens an expert; 32 experts, 32768 tokens, 2048 x 1408: 123 us with 256-row tiles alone, 113 us so).  A
+// workgroup takes its tall units, then its short ones, counted on over both lists, so that the short units fill
+// the tall list's last round.
 template <int OP, int SBM, int FA, int FB, int OUTF32, int GM>
 __global__ __launch_bounds__(512, 2) void gemm_tn_grouped_kernel(GemmDesc d, uint32_t tiles_n, GroupArgs<GM> grp) {
   constexpr int RING = ring_bytes<256, 256, 2, SBM>();

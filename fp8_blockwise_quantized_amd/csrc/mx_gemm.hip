@@ -13,7 +13,8 @@
 // last MFMAs of the stage whose slot it takes.  16-byte chunks are XOR-swizzled by row.  The MFMA's first operand
 // is the B patch: lane l ends with row l % 32 of the A patch and 16 of the B patch's 32 columns, B patch rows
 // being permuted so that those 16 are two runs of eight.
-// Measured alternatives (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3; this form 285 / 122 / 284):
+// Measured alternatives (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3; this form 280 / 119 / 275, that
+// is 2.7 / 3.2 / 4.0 PFLOP/s):
 // loads all issued after the barrier 294 / 132 / 287; four stages of 128 values 304 / 128 / 295; 128 x 256 tiles, two
 // workgroups per CU 345 / 148 / 344.  Without the loads 8192^3 takes 228 us, without loads, barriers and
 // writes 217: the matrix pipes with the LDS reads they need are the larger part, at the clock the card's power

@@ -4,9 +4,9 @@
 // Bound by HBM: 2 (BF16) or 4 (FP32) bytes read and 0.53 written per element and layout.  16384 x 5632 BF16 takes
 // 36 us in one layout and 56 us in both when it lies in the Infinity Cache (6.5 and 5.0 TB/s), 51-54 and 66 us from HBM
 // (4.4-4.6 TB/s; a copy reaches 6.3 there).  Persistent workgroups that read a tile ahead were no faster from
-// HBM (52-56 us), non-temporal reads and writes 10% faster there and 20-30% slower from the cache: not taken.  A workgroup of
-// four waves owns a tile of 128 rows by 128 columns; a wave holds 32 rows of it, a thread a patch of 8 rows by
-// 8 columns (eight independent 16-byte loads of BF16).  A row block is then 4 neighbouring lanes (two DPP
+// HBM (52-56 us), non-temporal reads and writes 10% faster there and 20-30% slower from the cache: not taken.
+// A workgroup of four waves owns a tile of 128 rows by 128 columns; a wave holds 32 rows of it, a thread a patch of
+// 8 rows by 8 columns (eight independent 16-byte loads of BF16).  A row block is then 4 neighbouring lanes (two DPP
 // exchanges) and a column block the 4 lanes of the wave that are 16 apart, so neither maximum needs LDS or a
 // barrier; only the transposed codes are staged in LDS, for stores of 64 contiguous bytes per column.
 #include "launch.hpp"
