@@ -102,6 +102,17 @@ __device__ __forceinline__ v8i lds_patch(const uint8_t* patch_base, PatchLane pl
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+// Two 16-byte values a lane (half 0 and half 1 of its row's output) of rows l % 16, exchanged between the lanes i and
+// i ^ 8 of every 16 (row_ror:8), so that `upper` holds rows 0 .. 7 and `lower` rows 8 .. 15, half 0 in the lanes
+// i < 8 and half 1 in the others: one store then writes whole 128-byte lines.
+__device__ __forceinline__ void join_halves(v4i half0, v4i half1, v4i& upper, v4i& lower) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    upper[k] = __builtin_amdgcn_update_dpp(half0[k], half1[k], 0x128, 0xF, 0xC, false);
+    lower[k] = __builtin_amdgcn_update_dpp(half1[k], half0[k], 0x128, 0xF, 0x3, false);
+  }
+}
+
 // Raw buffer descriptor over [base, base + bytes): loads past the end read zeros instead of
 // faulting.  Word 3 is the gfx9 raw-buffer format word.
 constexpr int kRsrcWord3 = 0x00020000;
@@ -637,6 +648,34 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
         if (part || OUTF32) {
           const int64_t ldc = part ? N : d.ldc;
           float* c0 = (part ? partial + (int64_t)C.split * M * N : reinterpret_cast<float*>(d.c)) + crow * ldc + ccol;
+          if constexpr (!CHK && !PERM && NI % 2 == 0) {
+            // whole lines here too: patches j and j + 1 are 32 consecutive columns
+            const int h = (lane >> 3) & 1;
+            c0 += -8 * h * ldc + 16 * h;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+#pragma unroll
+              for (int j = 0; j < NI; j += 2) {
+                v4i upper, lower;
+                join_halves(__builtin_bit_cast(v4i, acc[i][j]), __builtin_bit_cast(v4i, acc[i][j + 1]), upper, lower);
+                v4f* cu = reinterpret_cast<v4f*>(c0 + 16 * i * ldc + 16 * j);
+                v4f* cl = reinterpret_cast<v4f*>(c0 + (16 * i + 8) * ldc + 16 * j);
+                v4f u = __builtin_bit_cast(v4f, upper), l = __builtin_bit_cast(v4f, lower);
+                if (part) {  // (read again at once)
+                  *cu = u;
+                  *cl = l;
+                  continue;
+                }
+                if (OUTF32 == 2) {
+                  u = *cu + u;
+                  l = *cl + l;
+                }
+                __builtin_nontemporal_store(u, cu);
+                __builtin_nontemporal_store(l, cl);
+              }
+            }
+            return;
+          }
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             float* ci = c0 + 16 * i * ldc;
@@ -650,6 +689,36 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
                 *cij = acc[i][j];
             }
           }
+        } else if constexpr (!CHK && NI == 4) {
+          // Whole 128-byte lines, past the caches.  Of row l % 16 a lane has columns 8 (l / 16) .. +7 of both 32-column
+          // halves (in natural order lanes l and l + 16 swap first, so that it has eight consecutive columns there
+          // too, and the lane groups 16 (g % 2) + 8 (g / 2)).  us with 64-byte cached stores, 64-byte past the
+          // caches, and this: wgrad of 64 experts of 2816 x 2048, 32768 tokens 392 / 336 / 334, 4096 tokens
+          // 213 / 240 / 153; fprop of 32 experts of 2048 x 1408, 32768 tokens 123 / 115 / 110.
+          const int g = lane >> 4, h = (lane >> 3) & 1;
+          uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + (crow - 8 * h) * d.ldc + ccol + 32 * h;
+          if constexpr (!PERM) c0 += -4 * g + 16 * (g & 1) + 8 * (g >> 1);
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            v4i p[2], upper, lower;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const v4f& a = acc[i][2 * t];
+              const v4f& b = acc[i][2 * t + 1];
+              const uint32_t a0 = pack_bf16x2(a[0], a[1]), a1 = pack_bf16x2(a[2], a[3]);
+              const uint32_t b0 = pack_bf16x2(b[0], b[1]), b1 = pack_bf16x2(b[2], b[3]);
+              if constexpr (PERM) {
+                p[t] = (v4i){(int)a0, (int)a1, (int)b0, (int)b1};
+              } else {
+                const auto lo = __builtin_amdgcn_permlane16_swap(a0, b0, false, false);
+                const auto hi = __builtin_amdgcn_permlane16_swap(a1, b1, false, false);
+                p[t] = (v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]};
+              }
+            }
+            join_halves(p[0], p[1], upper, lower);
+            __builtin_nontemporal_store(upper, reinterpret_cast<v4i*>(c0 + 16 * i * d.ldc));
+            __builtin_nontemporal_store(lower, reinterpret_cast<v4i*>(c0 + (16 * i + 8) * d.ldc));
+          }
         } else if constexpr (PERM) {
           uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + crow * d.ldc + ccol;
 #pragma unroll
@@ -662,23 +731,6 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
               const v4f& b = acc[i][2 * t + 1];
               *reinterpret_cast<uint4*>(ci + 32 * t) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
                                                                    pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
-            }
-          }
-        } else if constexpr (!CHK && NI % 2 == 0) {
-          // Two patches' four columns each (8 bytes): lanes l and l + 16 swap, so that a lane has eight
-          // consecutive columns of one patch and an output row's four lanes write 64 contiguous bytes.
-          const int g = lane >> 4;
-          uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + crow * d.ldc + ccol - 4 * g + 16 * (g & 1) + 8 * (g >> 1);
-#pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            uint16_t* ci = c0 + 16 * i * d.ldc;
-#pragma unroll
-            for (int j = 0; j < NI; j += 2) {
-              const v4f& a = acc[i][j];
-              const v4f& b = acc[i][j + 1];
-              const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[0], a[1]), pack_bf16x2(b[0], b[1]), false, false);
-              const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[2], a[3]), pack_bf16x2(b[2], b[3]), false, false);
-              *reinterpret_cast<uint4*>(ci + 16 * j) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
             }
           }
         } else {
