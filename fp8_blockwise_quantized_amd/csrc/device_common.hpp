@@ -220,4 +220,15 @@ __device__ __forceinline__ TileRC tile_of_block(uint32_t ncols) {
 // fp32 value of the nearest BF16 number (ties to even).
 __device__ __forceinline__ float round_bf16(float v) { return bf16lo(pack_bf16x2(v, 0.0f)); }
 
+// Two 16-byte values a lane (half 0 and half 1 of its row's output) of rows l % 16, exchanged between the lanes i and
+// i ^ 8 of every 16 (row_ror:8), so that `upper` holds rows 0 .. 7 and `lower` rows 8 .. 15, half 0 in the lanes
+// i < 8 and half 1 in the others: one store then writes whole 128-byte lines.
+__device__ __forceinline__ void join_halves(v4i half0, v4i half1, v4i& upper, v4i& lower) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    upper[k] = __builtin_amdgcn_update_dpp(half0[k], half1[k], 0x128, 0xF, 0xC, false);
+    lower[k] = __builtin_amdgcn_update_dpp(half1[k], half0[k], 0x128, 0xF, 0x3, false);
+  }
+}
+
 }  // namespace fp8bq

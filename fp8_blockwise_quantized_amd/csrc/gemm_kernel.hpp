@@ -102,17 +102,6 @@ __device__ __forceinline__ v8i lds_patch(const uint8_t* patch_base, PatchLane pl
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// Two 16-byte values a lane (half 0 and half 1 of its row's output) of rows l % 16, exchanged between the lanes i and
-// i ^ 8 of every 16 (row_ror:8), so that `upper` holds rows 0 .. 7 and `lower` rows 8 .. 15, half 0 in the lanes
-// i < 8 and half 1 in the others: one store then writes whole 128-byte lines.
-__device__ __forceinline__ void join_halves(v4i half0, v4i half1, v4i& upper, v4i& lower) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    upper[k] = __builtin_amdgcn_update_dpp(half0[k], half1[k], 0x128, 0xF, 0xC, false);
-    lower[k] = __builtin_amdgcn_update_dpp(half1[k], half0[k], 0x128, 0xF, 0x3, false);
-  }
-}
-
 // Raw buffer descriptor over [base, base + bytes): loads past the end read zeros instead of
 // faulting.  Word 3 is the gfx9 raw-buffer format word.
 constexpr int kRsrcWord3 = 0x00020000;

@@ -13,12 +13,11 @@
 // last MFMAs of the stage whose slot it takes.  16-byte chunks are XOR-swizzled by row.  The MFMA's first operand
 // is the B patch: lane l ends with row l % 32 of the A patch and 16 of the B patch's 32 columns, B patch rows
 // being permuted so that those 16 are two runs of eight.
-// Measured alternatives (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3; this form 280 / 119 / 275, that
-// is 2.7 / 3.2 / 4.0 PFLOP/s):
-// loads all issued after the barrier 294 / 132 / 287; four stages of 128 values 304 / 128 / 295; 128 x 256 tiles, two
-// workgroups per CU 345 / 148 / 344.  Without the loads 8192^3 takes 228 us, without loads, barriers and
-// writes 217: the matrix pipes with the LDS reads they need are the larger part, at the clock the card's power
-// allows them.
+// Measured (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3): 222 / 99 / 252, that is 3.4 / 3.8 / 4.4 PFLOP/s.
+// Alternatives, against 285 / 122 / 284 for this form with other stores on a slower card: loads all issued after the
+// barrier 294 / 132 / 287; four stages of 128 values 304 / 128 / 295; 128 x 256 tiles, two workgroups per CU
+// 345 / 148 / 344.  Without the loads 8192^3 took 228 us, without loads, barriers and writes 217: the matrix pipes
+// with the LDS reads they need are the larger part, at the clock the card's power allows them.
 //
 // A lane's operand is block l / 32 of a 64-long step; it shifts the row's scale word by 8 (l / 32) once per
 // 128-long stretch, and the instruction's byte select (0 or 2) picks the step.  The words of a contraction's
@@ -345,23 +344,46 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
           // writes 64 contiguous bytes of 16 rows (four lanes each) and not 32 of 32 rows
           uint16_t* s0 = reinterpret_cast<uint16_t*>(d.c) +
                          ((int64_t)C.m0 + wm * WTM + (lane & 15)) * d.ldc + n0 + ccol + (lane & 16);
+          auto rows = [&](const v16f& v, v4i& x, v4i& y) {  // rows 0 .. 15 and 16 .. 31 of the patch
 #pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-              const v16f& v = acc[i][j];
-              uint32_t x[4], y[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const auto p = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[2 * r], v[2 * r + 1]),
-                                                                pack_bf16x2(v[8 + 2 * r], v[9 + 2 * r]), false, false);
-                x[r] = p[0];
-                y[r] = p[1];
-              }
-              uint16_t* s = s0 + 32 * i * d.ldc + 32 * j;
-              *reinterpret_cast<uint4*>(s) = make_uint4(x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<uint4*>(s + 16 * d.ldc) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int r = 0; r < 4; ++r) {
+              const auto p = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[2 * r], v[2 * r + 1]),
+                                                              pack_bf16x2(v[8 + 2 * r], v[9 + 2 * r]), false, false);
+              x[r] = (int)p[0];
+              y[r] = (int)p[1];
             }
+          };
+          if constexpr (NI == 2) {
+            // two patches side by side: whole 128-byte lines, past the caches (us with 64-byte cached stores, whole lines
+            // cached, and this: 16384 x 11264 x 2048 252 / 251 / 222, 4096 x 2560 x 2048 22.0 / 22.0 / 19.9, 32768 rows
+            // on 64 experts of 2816 x 2048 141 / 139 / 118, 8192^3 248 / 248 / 252)
+            const int half = (lane >> 3) & 1;
+            s0 += 32 * half - 8 * half * d.ldc;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              v4i x[2], y[2], upper, lower;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) rows(acc[i][j], x[j], y[j]);
+              uint16_t* s = s0 + 32 * i * d.ldc;
+              join_halves(x[0], x[1], upper, lower);
+              __builtin_nontemporal_store(upper, reinterpret_cast<v4i*>(s));
+              __builtin_nontemporal_store(lower, reinterpret_cast<v4i*>(s + 8 * d.ldc));
+              join_halves(y[0], y[1], upper, lower);
+              __builtin_nontemporal_store(upper, reinterpret_cast<v4i*>(s + 16 * d.ldc));
+              __builtin_nontemporal_store(lower, reinterpret_cast<v4i*>(s + 24 * d.ldc));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int j = 0; j < NI; ++j) {
+                v4i x, y;
+                rows(acc[i][j], x, y);
+                uint16_t* s = s0 + 32 * i * d.ldc + 32 * j;
+                *reinterpret_cast<v4i*>(s) = x;
+                *reinterpret_cast<v4i*>(s + 16 * d.ldc) = y;
+              }
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < MI; ++i)
