@@ -42,6 +42,8 @@ Allocating helpers (outputs created with torch on the input's device):
     hyperball_step(w, g, lr=1e-4, weight_decay=0.1, eps=1e-8, radius=0.0) -> norms:
         in-place normalized update of an FP32 weight (and projection onto `radius` if > 0)
         (accumulate=True: out, an FP32 main-grad buffer, receives out + dW)
+
+The layer grouped by expert is in ``grouped.py`` and the layer in MXFP4 in ``mx.py``; their names are here too.
 """
 
 import ctypes
