@@ -150,6 +150,27 @@ def test_larger_products(M, N, K):
     check(fq.gemm_mxfp4(qa, sa, qb, sb), a, b, False, (M, N, K))
 
 
+@pytest.mark.parametrize("M,N,K", [(800, 1024, 160), (3000, 2560, 1024), (4096, 4100, 288)])
+def test_full_tiles_in_every_output_type(M, N, K):
+    """Tiles of every size away from the edges, in outputs with guard columns."""
+    say("mx gemm outputs", M, N, K)
+    qa, sa, a = operand(M, K, 17)
+    qb, sb, b = operand(N, K, 18, 0.02)
+    wide = torch.full((M, N + 12), 7.0, device="cuda")
+    one = fq.gemm_mxfp4(qa, sa, qb, sb, out=wide[:, :N])
+    check(one, a, b, True, (M, N, K))
+    half = torch.full((M, N + 12), 7.0, dtype=torch.bfloat16, device="cuda")
+    fq.gemm_mxfp4(qa, sa, qb, sb, out=half[:, :N])
+    assert torch.equal(half[:, :N], one.to(torch.bfloat16))
+    start = torch.randn(M, N, device="cuda")
+    acc = torch.full((M, N + 12), 7.0, device="cuda")
+    acc[:, :N] = start
+    fq.gemm_mxfp4(qa, sa, qb, sb, out=acc[:, :N], accumulate=True)
+    assert torch.equal(acc[:, :N], start + one)
+    for v in (wide, half, acc):
+        assert torch.all(v[:, N:] == 7.0)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 512, 2048), (4, 33, 96), (13, 200, 5632), (16, 64, 128), (40, 130, 608),
                                    (700, 264, 544)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
