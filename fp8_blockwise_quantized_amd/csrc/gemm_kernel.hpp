@@ -158,9 +158,9 @@ __device__ __forceinline__ Unit unit_of(uint32_t u, uint32_t tiles_m, uint32_t t
 // Bound by the matrix pipes at the clock the card's power allows, as the dense products, and by what ragged
 // experts add.  32768 tokens: fprop on 64 experts of 2816 x 2048 239 us (1.58 PFLOP/s; matrix pipes busy 45% of the
 // cycles; a tenth of the tiles' rows are past an expert's end); dgrad on 32 experts of 2048 x 1408 106 us
-// (the dense product of the same size 94-112), 115 us with the largest expert 2.5 times the average; wgrad there
-// 148 and 160 us (dense, contracted in one piece: 125-135): 32 times the outputs, 184 MB, which all workgroups
-// write at the end of a round while no matrix pipe works, about 9 us a round.
+// (the dense product of the same size 94-112), 112 us with the largest expert 2.5 times the average; wgrad there
+// 155 us (dense, contracted in one piece: 125-135): 32 times the outputs, 184 MB, which a workgroup writes at the
+// end of a round while its matrix pipes idle.
 enum GroupMode : int { kGroupNone = 0, kGroupRowsMode = 1, kGroupWindow = 2, kGroupContract = 3 };
 template <int GM>
 struct GroupArgs {

@@ -122,9 +122,9 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
 
 // Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that
 // adds up the chunks costs 3 us, also where the counts then split nothing (32 experts, 32768 tokens, 2048 x 1408, no
-// expert much above the others: 161 us without, 164 us with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).
-// Uneven experts gain more (us, whole and split): 25% (62%) of the tokens on one of the 32 experts 217 / 184
-// (358 / 204), 62% on one of the 8 experts 111 / 34, the same at 8000 tokens on 4 experts of 1024 x 1024
+// expert much above the others: 155 us without, 158 us with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).
+// Uneven experts gain more (us, whole and split): 25% (62%) of the tokens on one of the 32 experts 189 / 166
+// (306 / 182), 62% on one of the 8 experts 111 / 34, the same at 8000 tokens on 4 experts of 1024 x 1024
 // 38 / 32; at 4096 tokens nothing.
 constexpr int64_t kMinSplitBlocks = 48;
 

@@ -33,10 +33,10 @@ constexpr int kMaxSplit = 8;
 
 // Splitting of long experts in a product grouped by expert that contracts over the tokens (wgrad).  The counts are
 // on the device, so the kernel chooses there how long a chunk of the contraction may be; the host gives it what
-// it needs for that: sets of partial sums [N, K] that the workspace holds (0: no splitting), output tiles an expert,
-// workgroups (in all and on a compute unit), and in units of one block's time what writing and adding up one set costs
-// and what the pass that adds them costs besides.  The kernel leaves its choice in the workspace for the pass that adds the sets up: two kernels that computed it apart might round
-// differently.
+// it needs for that: sets of partial sums [N, K] that the workspace holds (0: no splitting), output tiles an
+// expert, workgroups (in all and on a compute unit), and in units of one block's time what writing and adding up
+// one set costs and what the pass that adds them costs besides.  The kernel leaves its choice in the workspace for
+// the pass that adds the sets up: two kernels that computed it apart might round differently.
 constexpr int kMaxSets = 64;
 constexpr size_t kSplitListBytes = 256;  // in front of the sets: count and entries of the split experts (half the sets)
 struct GroupSplit {
