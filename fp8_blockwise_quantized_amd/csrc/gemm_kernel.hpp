@@ -772,13 +772,17 @@ __global__ __launch_bounds__(WGM* WGN * 64, (StageMinBlocks<BM, BN, WGM * WGN, N
   if constexpr (GROUPED) {
     const int lane = threadIdx.x & 63;
     if (threadIdx.x < 64) {
-      if constexpr (GM == kGroupContract) {
+      if constexpr (GM == kGroupContract)
         group_table_blocks(grp.offsets, grp.experts, grp.tokens, grp.split, gstarts, gunits, lane);
-        if (grp.split.sets > 0 && blockIdx.x == 0) list_split(gunits, grp.split_list, lane);
-      } else
+      else
         group_table_rows(grp.offsets, grp.experts, grp.tokens, BM, tiles_n, gstarts, gunits, lane);
     }
     __syncthreads();
+    // (a step of its own behind the barrier: in the branch above it the compiler took the whole tile loop's uniform
+    // values into vector registers where no other step followed the barrier, and spilled 73 of them)
+    if constexpr (GM == kGroupContract) {
+      if (grp.split.sets > 0 && blockIdx.x == 0 && threadIdx.x < 64) list_split(gunits, grp.split_list, lane);
+    }
     if constexpr (GM == kGroupContract)
       U *= __builtin_amdgcn_readfirstlane(gunits[kMaxEntries]);
     else

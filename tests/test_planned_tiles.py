@@ -1,0 +1,39 @@
+"""The planner's choices for the sizes of tile_cases.py (host only, built with g++)."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from tile_cases import WGRAD, padded
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    csrc = os.path.join(ROOT, "fp8_blockwise_quantized_amd", "csrc")
+    exe = str(tmp_path_factory.mktemp("plan") / "planned_tiles")
+    r = subprocess.run([gxx, "-std=c++17", "-O1", "-I", csrc, os.path.join(ROOT, "tests", "csrc", "planned_tiles.cpp"),
+                        os.path.join(csrc, "plan.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    env = {k: v for k, v in os.environ.items() if k != "FP8BQ_GEMM_TILE"}
+
+    def ask(*args):
+        r = subprocess.run([exe], input=" ".join(str(a) for a in args) + "\n", capture_output=True, text=True, env=env)
+        assert r.returncode == 0, r.stderr
+        return [int(v) for v in r.stdout.split()]
+
+    return ask
+
+
+@pytest.mark.parametrize("name", sorted(WGRAD))
+def test_grouped_weight_gradients(plan, name):
+    counts, N, K, rows, split = WGRAD[name]
+    for ws in (0, 1):
+        tile, _, sets = plan("grouped", 2, len(counts), padded(counts), N, K, ws)
+        assert tile == rows and (sets > 0) == (split and ws == 1)
