@@ -220,6 +220,19 @@ __device__ __forceinline__ TileRC tile_of_block(uint32_t ncols) {
 // fp32 value of the nearest BF16 number (ties to even).
 __device__ __forceinline__ float round_bf16(float v) { return bf16lo(pack_bf16x2(v, 0.0f)); }
 
+// A store that the caches keep, or one past them (uniform choice).  The empty asms keep the two apart: the compiler
+// would make them one store before or behind the branch, and that one the caches keep.
+template <typename V>
+__device__ __forceinline__ void store_line(V v, V* p, bool past) {
+  if (past) {
+    asm volatile("");
+    __builtin_nontemporal_store(v, p);
+    asm volatile("");
+  } else {
+    *p = v;
+  }
+}
+
 // Two 16-byte values a lane (half 0 and half 1 of its row's output) of rows l % 16, exchanged between the lanes i and
 // i ^ 8 of every 16 (row_ror:8), so that `upper` holds rows 0 .. 7 and `lower` rows 8 .. 15, half 0 in the lanes
 // i < 8 and half 1 in the others: one store then writes whole 128-byte lines.

@@ -632,6 +632,7 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
         part = !C.whole;
         if (part) crow = mrow;
       }
+      const bool past = d.past && !part;  // (partial sums are read again at once)
       auto write = [&](auto checked) {
         constexpr bool CHK = decltype(checked)::value;
         if (part || OUTF32) {
@@ -650,17 +651,12 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
                 v4f* cu = reinterpret_cast<v4f*>(c0 + 16 * i * ldc + 16 * j);
                 v4f* cl = reinterpret_cast<v4f*>(c0 + (16 * i + 8) * ldc + 16 * j);
                 v4f u = __builtin_bit_cast(v4f, upper), l = __builtin_bit_cast(v4f, lower);
-                if (part) {  // (read again at once)
-                  *cu = u;
-                  *cl = l;
-                  continue;
-                }
-                if (OUTF32 == 2) {
+                if (OUTF32 == 2 && !part) {
                   u = *cu + u;
                   l = *cl + l;
                 }
-                __builtin_nontemporal_store(u, cu);
-                __builtin_nontemporal_store(l, cl);
+                store_line(u, cu, past && OUTF32 != 2);
+                store_line(l, cl, past && OUTF32 != 2);
               }
             }
             return;
@@ -679,11 +675,11 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
             }
           }
         } else if constexpr (!CHK && NI == 4) {
-          // Whole 128-byte lines, past the caches.  Of row l % 16 a lane has columns 8 (l / 16) .. +7 of both 32-column
-          // halves (in natural order lanes l and l + 16 swap first, so that it has eight consecutive columns there
-          // too, and the lane groups 16 (g % 2) + 8 (g / 2)).  us with 64-byte cached stores, 64-byte past the
-          // caches, and this: wgrad of 64 experts of 2816 x 2048, 32768 tokens 392 / 336 / 334, 4096 tokens
-          // 213 / 240 / 153; fprop of 32 experts of 2048 x 1408, 32768 tokens 123 / 115 / 110.
+          // Whole 128-byte lines, past the caches or not (stores_past_caches).  Of row l % 16 a lane has columns
+          // 8 (l / 16) .. +7 of both 32-column halves (in natural order lanes l and l + 16 swap first, so that it has eight
+          // consecutive columns there too, and the lane groups 16 (g % 2) + 8 (g / 2)).  us with 64-byte stores, whole
+          // lines, and whole lines past the caches: wgrad of 64 experts of 2816 x 2048, 32768 tokens 375 / 378 / 324, 4096 tokens 211 / 211 / 159 (64-byte
+          // stores past the caches took more than cached ones there); fprop of 64 such experts 233 / 236 / 229.
           const int g = lane >> 4, h = (lane >> 3) & 1;
           uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + (crow - 8 * h) * d.ldc + ccol + 32 * h;
           if constexpr (!PERM) c0 += -4 * g + 16 * (g & 1) + 8 * (g >> 1);
@@ -705,8 +701,8 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
               }
             }
             join_halves(p[0], p[1], upper, lower);
-            __builtin_nontemporal_store(upper, reinterpret_cast<v4i*>(c0 + 16 * i * d.ldc));
-            __builtin_nontemporal_store(lower, reinterpret_cast<v4i*>(c0 + (16 * i + 8) * d.ldc));
+            store_line(upper, reinterpret_cast<v4i*>(c0 + 16 * i * d.ldc), past);
+            store_line(lower, reinterpret_cast<v4i*>(c0 + (16 * i + 8) * d.ldc), past);
           }
         } else if constexpr (PERM) {
           uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + crow * d.ldc + ccol;

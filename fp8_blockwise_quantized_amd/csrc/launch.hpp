@@ -81,6 +81,7 @@ struct GemmDesc {
   int fa, fb;    // FP8 format of A and B
   int out_f32;   // 0: BF16 output, 1: FP32 output, 2: FP32 output accumulated into (c += result)
   int sb_mode;   // SbMode
+  int past;      // full output tiles are stored past the caches (stores_past_caches)
 };
 
 hipError_t launch_gemm(int op, const GemmDesc& d, const GemmPlan& plan, void* ws, hipStream_t st);
@@ -120,6 +121,7 @@ struct MxDesc {
   void* c;
   int64_t ldc;
   int out_t;      // 0: BF16, 1: FP32, 2: FP32 accumulated into
+  int past;       // as in GemmDesc
   int64_t M, N, K;
 };
 // offsets null: one dense product.  Else A's rows are sorted by expert and B is stacked [experts N, K].

@@ -299,6 +299,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
       const int64_t m = (int64_t)C.m0 + arow, n0 = (int64_t)C.n0 + wn * WTN + 8 * h;
       int64_t ccol = 0;
       if constexpr (GROUPED) ccol = C.ccol;
+      const bool past = d.past && nsplit == 1;  // (partial sums are read again at once)
       const bool full = vec && (int64_t)C.m0 + BM <= mlim && (int64_t)C.n0 + BN <= nlim;
       if (nsplit > 1 || OUT != 0) {
         const int64_t ldo = nsplit > 1 ? ldp : d.ldc;
@@ -331,10 +332,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
                 v4f s = __builtin_bit_cast(v4f, w[q]);
                 v4f* o4 = reinterpret_cast<v4f*>(o + (32 * i + 8 * q) * ldo + 32 * j);
                 if (add) s = *o4 + s;
-                if (nsplit > 1)
-                  *o4 = s;  // (read again at once)
-                else
-                  __builtin_nontemporal_store(s, o4);
+                store_line(s, o4, past && OUT != 2);
               }
             }
         } else {
@@ -375,9 +373,9 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
             }
           };
           if constexpr (NI == 2) {
-            // two patches side by side: whole 128-byte lines, past the caches (us with 64-byte cached stores, whole lines
-            // cached, and this: 16384 x 11264 x 2048 252 / 251 / 222, 4096 x 2560 x 2048 22.0 / 22.0 / 19.9, 32768 rows
-            // on 64 experts of 2816 x 2048 141 / 139 / 118, 8192^3 248 / 248 / 252)
+            // two patches side by side: whole 128-byte lines.  Where they go past the caches (stores_past_caches) that is
+            // what makes it worth it: us with 64-byte stores, whole lines, and whole lines past the caches
+            // 16384 x 11264 x 2048 242 / 238 / 209, 4096 x 2560 x 2048 20.4 / 20.6 / 18.4.
             const int half = (lane >> 3) & 1;
             s0 += 32 * half - 8 * half * d.ldc;
 #pragma unroll
@@ -387,11 +385,11 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
               for (int j = 0; j < 2; ++j) rows(acc[i][j], x[j], y[j]);
               uint16_t* s = s0 + 32 * i * d.ldc;
               join_halves(x[0], x[1], upper, lower);
-              __builtin_nontemporal_store(upper, reinterpret_cast<v4i*>(s));
-              __builtin_nontemporal_store(lower, reinterpret_cast<v4i*>(s + 8 * d.ldc));
+              store_line(upper, reinterpret_cast<v4i*>(s), past);
+              store_line(lower, reinterpret_cast<v4i*>(s + 8 * d.ldc), past);
               join_halves(y[0], y[1], upper, lower);
-              __builtin_nontemporal_store(upper, reinterpret_cast<v4i*>(s + 16 * d.ldc));
-              __builtin_nontemporal_store(lower, reinterpret_cast<v4i*>(s + 24 * d.ldc));
+              store_line(upper, reinterpret_cast<v4i*>(s + 16 * d.ldc), past);
+              store_line(lower, reinterpret_cast<v4i*>(s + 24 * d.ldc), past);
             }
           } else {
 #pragma unroll

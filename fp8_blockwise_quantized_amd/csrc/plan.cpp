@@ -120,6 +120,31 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
   return p;
 }
 
+// Stored past the caches, an output neither pushes what is in them out nor has to be written back from the L2 when the
+// kernel ends; kept, it is there for whatever reads it or is written over it next.  us of the product and of the product
+// with a reader of its output, each kept / past; output, and output and operands, in MB.  BF16, read by the row quantizer:
+//   8, 16      14.0 / 13.2    21.4 / 21.3        past
+//   34, 54     33.5 / 31.7    43.4 / 42.7
+//   67, 105    62.9 / 63.0    80.6 / 85.2        past all the same: other work's operands lose more than the reader gains (a
+//                                                decoder block's step, six of whose outputs have 67 or 84 MB, 2562 / 2529)
+//   134, 168   115 / 125      152 / 167          kept
+//   134, 205   118 / 118      154 / 161
+//   185, 225   169 / 168      230 / 219          past: all of it does not fit the 256 MB cache beside its reader
+//   369, 426   350 / 308      476 / 433
+// (MXFP4: 21, 29 MB 20.6 / 18.4 and 28.6 / 27.1; 134, 152 MB 76 / 83 and 112 / 125; 369, 399 MB 235 / 195 and 365 / 323.
+// Weight gradients of 64 experts, 738 MB, 376 / 320 and 652 / 613.)  FP32, read by a copy to BF16:
+//   17, 21     13.2 / 12.4    20.9 / 20.1        past
+//   67, 76     28.9 / 28.5    44.1 / 43.8
+//   268, 285   99 / 109       183 / 187          kept
+//   268, 336   279 / 279      351 / 367
+//   369, 529   748 / 728      848 / 827          past
+//   738, 768   297 / 241      507 / 466
+// Added to the output, whose lines the addition has just read: 268 MB 182 / 183, 1476 MB 818 / 827: kept.
+bool stores_past_caches(int out_t, double out, double operands) {
+  if (out_t == 2) return false;
+  return out < 100e6 || (out_t == 1 ? out > 320e6 : out + operands > 215e6);
+}
+
 // Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that
 // adds up the chunks costs 3 us, also where the counts then split nothing (32 experts, 32768 tokens, 2048 x 1408, no
 // expert much above the others: 155 us without, 158 us with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).

@@ -59,3 +59,101 @@ def test_grouped_weight_gradients(name):
         assert close(dw, y, lim)
         assert untouched(big, one) and untouched(wide, acc) and untouched(half, dw)
     assert torch.all(ws[size:] == 0xFF)
+
+
+# Outputs of 105 to 120 MB stay in the caches, parts of them go past: the two kinds of store give the same bits, and neither
+# writes outside.
+
+def codes(rows, cols, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(0, 255, (rows, cols), dtype=torch.uint8, device="cuda", generator=g)
+
+
+def finite_fp8(rows, cols, seed):
+    q = codes(rows, cols, seed)
+    return torch.where(q & 127 == 127, torch.zeros_like(q), q)  # (no E4M3 NaN)
+
+
+def scales(rows, cols, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.rand(rows, cols, device="cuda", generator=g) + 0.5
+
+
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_kept_and_streamed_outputs_of_the_dense_products(dtype):
+    say("tiles stores dense", dtype)
+    M, N, K = 26000 if dtype == torch.bfloat16 else 13000, 2048, 256
+    q, s, w, sw = finite_fp8(M, K, 1), scales(K // 128, M, 2), finite_fp8(N, K, 3), scales(N // 128, K // 128, 4)
+    big, y = guarded(M, N, dtype)
+    fq.gemm_fprop(q, s, w, sw, out=y)
+    half = M // 8 * 4
+    for a, b in ((0, half), (half, M)):
+        assert torch.equal(y[a:b], fq.gemm_fprop(q[a:b], s[:, a:b].contiguous(), w, sw, out_dtype=dtype))
+    assert untouched(big, y)
+    T, N, K = 256, 12800, 4096 if dtype == torch.bfloat16 else 2048
+    q, s, w, sw = finite_fp8(N, T, 5), scales(T // 128, N, 6), finite_fp8(K, T, 7), scales(T // 128, K, 8)
+    big, y = guarded(N, K, dtype)
+    fq.gemm_wgrad(q, s, w, sw, out=y)
+    for a, b in ((0, 6400), (6400, N)):
+        assert torch.equal(y[a:b], fq.gemm_wgrad(q[a:b], s[:, a:b].contiguous(), w, sw, out_dtype=dtype))
+    if dtype == torch.float32:
+        start = torch.randn(N, K, device="cuda")
+        acc = start.clone()
+        fq.gemm_wgrad(q, s, w, sw, out=acc, accumulate=True)
+        assert torch.equal(acc, start + y)
+    assert untouched(big, y)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_kept_and_streamed_outputs_of_the_grouped_products(dtype):
+    say("tiles stores grouped", dtype)
+    E, N, K = 4, 2048, 256
+    T = 26000 if dtype == torch.bfloat16 else 13000
+    cuts = torch.tensor([0, 3, T // 3, T // 3, T], device="cuda")
+    x, dy = (torch.randn(T, c, device="cuda").to(torch.bfloat16) for c in (K, N))
+    w = torch.randn(E * N, K, device="cuda").to(torch.bfloat16)
+    qw, sw, qwt = fq.quantize_weight_dual(w, fq.E4M3)
+    q, s = fq.quantize_act_1x128(x)
+    big, y = guarded(T, N, dtype)
+    fq.grouped_gemm_fprop(q, s, cuts, qw, sw, out=y)
+    for a, b, e in ((0, 3, 0), (3, T // 3, 1), (T // 3, T, 3)):
+        one = fq.grouped_gemm_fprop(q[a:b], fq.quantize_act_1x128(x[a:b])[1], torch.tensor([0, b - a], device="cuda"),
+                                    qw[e * N:(e + 1) * N], sw[e * N // 128:(e + 1) * N // 128], out_dtype=dtype)
+        assert torch.equal(y[a:b], one)
+    assert untouched(big, y)
+    E, N, K = 32, 1024, 1664 if dtype == torch.bfloat16 else 896
+    counts = [70 * (e % 3) for e in range(E)]
+    off, (qdyt, sdyt), (qxt, sxt) = operands(counts, N, K, 600)
+    big, y = guarded(E * N, K, dtype)
+    fq.grouped_gemm_wgrad(qdyt, sdyt, qxt, sxt, off, fq.E5M2, out=y)
+    want, lim = expected(counts, qdyt, sdyt, qxt, sxt)
+    assert close(y, want, lim)
+    assert untouched(big, y)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_kept_and_streamed_outputs_of_the_mxfp4_products(dtype):
+    say("tiles stores mx", dtype)
+    M, N, K = 26000 if dtype == torch.bfloat16 else 13000, 2056, 320
+    x, w = (torch.randn(r, K, device="cuda").to(torch.bfloat16) for r in (M, N))
+    qa, sa = fq.quantize_mxfp4(x)
+    qb, sb = fq.quantize_mxfp4(w)
+    big, y = guarded(M, N, dtype)
+    fq.gemm_mxfp4(qa, sa, qb, sb, out=y)
+    half = M // 8 * 4
+    for a, b in ((0, half), (half, M)):
+        assert torch.equal(y[a:b], fq.gemm_mxfp4(qa[a:b], sa[:, a:b].contiguous(), qb, sb, out_dtype=dtype))
+    if dtype == torch.float32:
+        start = torch.randn(M, N, device="cuda")
+        acc = start.clone()
+        fq.gemm_mxfp4(qa, sa, qb, sb, out=acc, accumulate=True)
+        assert torch.equal(acc, start + y)
+    off = torch.tensor([0, 5, 5, M], device="cuda")
+    qe, se = fq.quantize_mxfp4(torch.cat([w, w, w]))
+    both, g = guarded(M, N, dtype)
+    fq.grouped_gemm_mxfp4(qa, sa, off, qe, se, out=g)
+    assert torch.equal(g, y)
+    assert untouched(big, y) and untouched(both, g)
