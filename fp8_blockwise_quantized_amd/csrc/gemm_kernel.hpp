@@ -617,8 +617,11 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
     // patch j (permuted B rows) or 16*j + 4*(l/16) .. +3 (natural order); only tiles that reach past
     // M or N check bounds.
     {
-      const int64_t mrow = (int64_t)C.m0 + wm * WTM + (lane & 15);
-      const int64_t ncol = (int64_t)C.n0 + wn * WTN + (PERM ? 8 : 4) * (lane >> 4);
+      // (the lane's place in the output is worked out here: kept in registers over the loop it cost spills)
+      int el = lane;
+      asm volatile("" : "+v"(el));
+      const int64_t mrow = (int64_t)C.m0 + wm * WTM + (el & 15);
+      const int64_t ncol = (int64_t)C.n0 + wn * WTN + (PERM ? 8 : 4) * (el >> 4);
       auto jcol = [](int j) { return PERM ? 32 * (j >> 1) + 4 * (j & 1) : 16 * j; };  // patch j's offset from ncol
       const int64_t mlim = m_end(C), nlim = n_end(C);
       const bool full = (int64_t)C.m0 + BM <= mlim && (int64_t)C.n0 + BN <= nlim;
@@ -640,7 +643,7 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
           float* c0 = (part ? partial + (int64_t)C.split * M * N : reinterpret_cast<float*>(d.c)) + crow * ldc + ccol;
           if constexpr (!CHK && !PERM && NI % 2 == 0) {
             // whole lines here too: patches j and j + 1 are 32 consecutive columns
-            const int h = (lane >> 3) & 1;
+            const int h = (el >> 3) & 1;
             c0 += -8 * h * ldc + 16 * h;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
@@ -680,7 +683,7 @@ __device__ __forceinline__ void gemm_tn_units(const GemmDesc& d, uint32_t tiles_
           // consecutive columns there too, and the lane groups 16 (g % 2) + 8 (g / 2)).  us with 64-byte stores, whole
           // lines, and whole lines past the caches: wgrad of 64 experts of 2816 x 2048, 32768 tokens 375 / 378 / 324, 4096 tokens 211 / 211 / 159 (64-byte
           // stores past the caches took more than cached ones there); fprop of 64 such experts 233 / 236 / 229.
-          const int g = lane >> 4, h = (lane >> 3) & 1;
+          const int g = el >> 4, h = (el >> 3) & 1;
           uint16_t* c0 = reinterpret_cast<uint16_t*>(d.c) + (crow - 8 * h) * d.ldc + ccol + 32 * h;
           if constexpr (!PERM) c0 += -4 * g + 16 * (g & 1) + 8 * (g >> 1);
 #pragma unroll

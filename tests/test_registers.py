@@ -84,6 +84,11 @@ def test_grouped_weight_gradient_added_to_the_output(all_kernels):
     assert [k for k in mine if k[2] or k[3]] == []
 
 
+def test_no_kernel_spills(all_kernels):
+    assert len(all_kernels) > 300
+    assert [k for k in all_kernels if k[2] or k[3]] == []
+
+
 def test_both_kinds_of_store(folder):
     """Every product kernel that stores whole lines of full tiles can store them past the caches and not: fprop and dgrad in
     BF16, wgrad and the MXFP4 products in BF16 and FP32 (the 64-row MXFP4 tile in FP32 only)."""
