@@ -6,7 +6,7 @@ import subprocess
 
 import pytest
 
-from tile_cases import WGRAD, padded
+from tile_cases import MX_GROUPED, MX_SPLIT, ROWS, WGRAD, padded
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -50,3 +50,24 @@ def test_outputs_that_the_caches_hold_for_their_reader_are_kept_there(plan):
     assert past(16384, 11264, 2048) and past(8192, 11264, 2048) and past(16384, 2048, 2048) and past(2048, 2048, 2048)
     assert not past(8192, 8192, 2048, 1) and past(16384, 11264, 2048, 1) and past(2048, 2048, 2048, 1)
     assert not past(8192, 8192, 2048, 2) and not past(16384, 11264, 2048, 2) and not past(2048, 2048, 2048, 2)
+
+
+@pytest.mark.parametrize("name", sorted(ROWS))
+def test_grouped_rows(plan, name):
+    counts, N, K, fprop, dgrad = ROWS[name]
+    for op, rows in ((0, fprop), (1, dgrad)):
+        assert plan("grouped", op, len(counts), sum(counts), N, K, 0)[0] == rows
+
+
+@pytest.mark.parametrize("name", sorted(MX_GROUPED))
+def test_grouped_mxfp4(plan, name):
+    counts, N, K, rows = MX_GROUPED[name]
+    for linear in (0, 1):
+        assert plan("mx", linear, len(counts), sum(counts), N, K)[0] == rows
+
+
+@pytest.mark.parametrize("M,N,K,rows,parts", MX_SPLIT)
+def test_split_mxfp4(plan, M, N, K, rows, parts):
+    for linear in (0, 1):
+        tile, _, split = plan("mx", linear, 0, M, N, K)
+        assert (tile, split) == (rows, parts)
