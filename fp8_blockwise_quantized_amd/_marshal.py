@@ -34,9 +34,7 @@ def _refuse(t, name, shape, dtypes, device):
 
 
 def matrix(t, name, shape, dtypes, device):
-    """(address, leading dimension) of a matrix of the given shape with unit column stride; (0, 0) for None."""
-    if t is None:
-        return 0, 0
+    """(address, leading dimension) of a matrix of the given shape with unit column stride."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.get_device() != device:
         _refuse(t, name, shape, dtypes, device)
     rows, cols = shape
@@ -49,9 +47,7 @@ def matrix(t, name, shape, dtypes, device):
 
 
 def scale_words(t, name, shape, device):
-    """(address, leading dimension in words) of scales [words, rows, 4]; (0, 0) for None."""
-    if t is None:
-        return 0, 0
+    """(address, leading dimension in words) of scales [words, rows, 4]."""
     if not isinstance(t, torch.Tensor) or t.dtype not in U8 or t.shape != shape or t.get_device() != device:
         _refuse(t, name, shape, U8, device)
     words, rows, _ = shape
@@ -63,15 +59,24 @@ def scale_words(t, name, shape, device):
     return t.data_ptr(), ld // 4 if words > 1 else rows
 
 
-def experts(offsets, device):
-    """(address, E) of an offsets tensor of E + 1 entries."""
+NONE = (0, 0)  # of an output that is not wanted
+
+
+def experts_of(offsets):
+    """E of an offsets tensor of E + 1 entries."""
     if not isinstance(offsets, torch.Tensor):
         raise TypeError("offsets must be a torch tensor")
     if offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous 1-D tensor of E + 1 entries")
+    return offsets.shape[0] - 1
+
+
+def experts(offsets, device):
+    """(address, E) of an offsets tensor of E + 1 entries."""
+    E = experts_of(offsets)
     if offsets.dtype not in I64 or offsets.get_device() != device:
         _refuse(offsets, "offsets", offsets.shape, I64, device)
-    return offsets.data_ptr(), offsets.shape[0] - 1
+    return offsets.data_ptr(), E
 
 
 def space(ws, device):

@@ -26,7 +26,7 @@ import torch
 
 from . import (E4M3, IN_BF16, IN_F32, OUT_BF16, OUT_F32, OUT_F32_ACCUM, _c_i64, _c_int, _c_sz, _c_vp, _entry, _pad4,
                _RESTYPES, _SIGS, lib)
-from ._marshal import F32, HI, U8, experts, matrix, space, stacked, stream
+from ._marshal import F32, HI, NONE, U8, experts, experts_of, matrix, space, stacked, stream
 
 MAX_EXPERTS = 512
 
@@ -62,10 +62,12 @@ def fp8bq_quantize_act_grouped(x, offsets, fmt_rows, q, s, fmt_cols, qt, st):
     T, C = x.shape
     dev = x.get_device()
     op, E = experts(offsets, dev)
+    if not isinstance(qt, torch.Tensor) or qt.dim() != 2:
+        raise TypeError("qt must be a 2-D torch tensor")
     padded = qt.shape[1]
     xp, ldx = matrix(x, "x", (T, C), HI, dev)
-    qp, ldq = matrix(q, "q", (T, C), U8, dev)
-    sp, lds = matrix(s, "s", (C // 128, T), F32, dev)
+    qp, ldq = matrix(q, "q", (T, C), U8, dev) if q is not None else NONE
+    sp, lds = matrix(s, "s", (C // 128, T), F32, dev) if s is not None else NONE
     qtp, ldqt = matrix(qt, "qt", (C, padded), U8, dev)
     stp, ldst = matrix(st, "st", (padded // 128, C), F32, dev)
     return (xp, IN_BF16 if x.dtype == torch.bfloat16 else IN_F32, T, C, ldx, op, E, fmt_rows, qp, ldq, sp, lds, fmt_cols,
@@ -118,7 +120,7 @@ def fp8bq_grouped_gemm_wgrad(qdyt, sdyt, fdy, qxt, sxt, fx, offsets, dw, accumul
 
 def _cols_outputs(x, offsets):
     T, C = x.shape
-    padded = fp8bq_grouped_padded_rows(T, offsets.shape[0] - 1)
+    padded = fp8bq_grouped_padded_rows(T, experts_of(offsets))
     return x.new_empty((C, padded), dtype=torch.uint8), x.new_empty((padded // 128, C), dtype=torch.float32)
 
 
@@ -142,7 +144,7 @@ def quantize_act_grouped_dual(x, offsets, fmt_rows=E4M3, fmt_cols=E4M3):
 
 
 def grouped_gemm_fprop(qx, sx, offsets, qw, sw, fx=E4M3, fw=E4M3, out_dtype=torch.bfloat16, out=None):
-    N = stacked(qw.shape[0], offsets.shape[0] - 1, "qw")
+    N = stacked(qw.shape[0], experts_of(offsets), "qw")
     y = out if out is not None else qx.new_empty((qx.shape[0], N), dtype=out_dtype)
     fp8bq_grouped_gemm_fprop(qx, sx, fx, offsets, qw, sw, fw, y)
     return y
@@ -160,7 +162,7 @@ def grouped_gemm_wgrad(qdyt, sdyt, qxt, sxt, offsets, fdy=E4M3, fx=E4M3, out_dty
     tensor of the workspace size (made here if None)."""
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate=True needs an FP32 `out` tensor holding the running sum")
-    E = offsets.shape[0] - 1
+    E = experts_of(offsets)
     N, padded = qdyt.shape
     K = qxt.shape[0]
     dw = out if out is not None else qdyt.new_empty((E * N, K), dtype=out_dtype)

@@ -29,7 +29,7 @@ import functools
 import torch
 
 from . import OUT_BF16, OUT_F32, OUT_F32_ACCUM, IN_BF16, IN_F32, _RESTYPES, _SIGS, _c_i64, _c_int, _c_sz, _c_vp, _entry, lib
-from ._marshal import F32, HI, U8, experts, matrix, scale_words, space, stacked, stream
+from ._marshal import F32, HI, NONE, U8, experts, experts_of, matrix, scale_words, space, stacked, stream
 
 _OUT_WS = [_c_vp, _c_int, _c_i64, _c_vp, _c_sz, _c_vp]
 _CODES = [_c_vp, _c_i64, _c_vp, _c_i64]
@@ -83,10 +83,10 @@ def fp8bq_quantize_mxfp4(x, q, s, qt, st):
     R, C = x.shape
     dev = x.get_device()
     xp, ldx = matrix(x, "x", (R, C), HI, dev)
-    qp, ldq = matrix(q, "q", (R, C // 2), U8, dev)
-    sp, lds = scale_words(s, "s", (_words(C), R, 4), dev)
-    qtp, ldqt = matrix(qt, "qt", (C, (R + 31) // 32 * 16), U8, dev)
-    stp, ldst = scale_words(st, "st", (_words(R), C, 4), dev)
+    qp, ldq = matrix(q, "q", (R, C // 2), U8, dev) if q is not None else NONE
+    sp, lds = scale_words(s, "s", (_words(C), R, 4), dev) if s is not None else NONE
+    qtp, ldqt = matrix(qt, "qt", (C, (R + 31) // 32 * 16), U8, dev) if qt is not None else NONE
+    stp, ldst = scale_words(st, "st", (_words(R), C, 4), dev) if st is not None else NONE
     return xp, _in(x), R, C, ldx, qp, ldq, sp, lds, qtp, ldqt, stp, ldst, stream(dev)
 
 
@@ -213,7 +213,7 @@ def linear_mxfp4(x, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
 
 def grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     T, K2 = qa.shape
-    E = offsets.shape[0] - 1
+    E = experts_of(offsets)
     N = stacked(qw.shape[0], E, "qw")
     y = _output(out, T, N, out_dtype, qa)
     if ws is None:
@@ -224,7 +224,7 @@ def grouped_gemm_mxfp4(qa, sa, offsets, qw, sw, out_dtype=torch.bfloat16, out=No
 
 def grouped_linear_mxfp4(x, offsets, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     T, K = x.shape
-    E = offsets.shape[0] - 1
+    E = experts_of(offsets)
     N = stacked(qw.shape[0], E, "qw")
     y = _output(out, T, N, out_dtype, x)
     if ws is None:
