@@ -173,14 +173,17 @@ def quantize_mxfp4_dual(x):
     return q, s, qt, st
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 @functools.lru_cache(maxsize=4096)
 def _ws_bytes(op, device, *sizes):
-    """Workspace of an operation at these sizes: a function of the sizes and the device alone."""
+    """Workspace of an operation at these sizes on the current device, of that index: a function of these alone."""
     return getattr(lib(), op)(*sizes)
 
 
 def _space(op, like, *sizes):
-    n = _ws_bytes(op, like.get_device(), *sizes)
+    n = _ws_bytes(op, _current_device() if like.is_cuda else -1, *sizes)
     return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
