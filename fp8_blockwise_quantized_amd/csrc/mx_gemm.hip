@@ -476,14 +476,17 @@ template <int BM, int BN, int WGM, int WGN, int STEPS, int NST, int OUT>
 static hipError_t launch_tile(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, int vec,
                               hipStream_t st) {
   const int64_t ldp = (d.N + 3) / 4 * 4;
-  if (grp.offsets)
-    hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, STEPS, NST, OUT, true>), dim3((unsigned)p.grid), dim3(WGM * WGN * 64), 0,
-                       st, d, (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, 1, (float*)nullptr, ldp, vec,
-                       GroupArgs<kGroupRowsMode>{grp.offsets, grp.experts, d.M});
-  else
-    hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, STEPS, NST, OUT, false>), dim3((unsigned)p.grid), dim3(WGM * WGN * 64), 0,
-                       st, d, (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, p.split_k, (float*)ws, ldp, vec,
-                       GroupArgs<kGroupNone>{});
+  const dim3 grid((unsigned)p.grid), block(WGM * WGN * 64);
+  if constexpr (OUT != 2) {  // (a grouped product is not added to the output)
+    if (grp.offsets) {
+      hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, STEPS, NST, OUT, true>), grid, block, 0, st, d,
+                         (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, 1, (float*)nullptr, ldp, vec,
+                         GroupArgs<kGroupRowsMode>{grp.offsets, grp.experts, d.M});
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WGM, WGN, STEPS, NST, OUT, false>), grid, block, 0, st, d,
+                     (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, p.split_k, (float*)ws, ldp, vec, GroupArgs<kGroupNone>{});
   return hipGetLastError();
 }
 

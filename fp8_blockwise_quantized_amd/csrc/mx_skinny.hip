@@ -214,22 +214,20 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void mx_skinny_kernel(MxDesc 
   }
 }
 
-template <typename TA, int OUT>
-static hipError_t launch_groups(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
-  if (grp.offsets)
-    hipLaunchKernelGGL((mx_skinny_kernel<TA, OUT, true>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st, d, grp,
-                       p.split_k);
-  else
-    hipLaunchKernelGGL((mx_skinny_kernel<TA, OUT, false>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st, d,
-                       grp, p.split_k);
+template <typename TA, int OUT, bool GROUPED>
+static hipError_t launch_one(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
+  hipLaunchKernelGGL((mx_skinny_kernel<TA, OUT, GROUPED>), dim3((unsigned)p.grid), dim3(kSkinnyWaves * 64), 0, st, d, grp,
+                     p.split_k);
   return hipGetLastError();
 }
 
 template <typename TA>
 static hipError_t launch_out(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
-  if (d.out_t == 0) return launch_groups<TA, 0>(d, grp, p, st);
-  if (d.out_t == 1) return launch_groups<TA, 1>(d, grp, p, st);
-  return launch_groups<TA, 2>(d, grp, p, st);
+  if (grp.offsets) return d.out_t == 0 ? launch_one<TA, 0, true>(d, grp, p, st) : launch_one<TA, 1, true>(d, grp, p, st);
+  if constexpr (std::is_same_v<TA, uint8_t>) {  // (only the dense product of codes is added to the output)
+    if (d.out_t == 2) return launch_one<TA, 2, false>(d, grp, p, st);
+  }
+  return d.out_t == 0 ? launch_one<TA, 0, false>(d, grp, p, st) : launch_one<TA, 1, false>(d, grp, p, st);
 }
 
 hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {

@@ -526,6 +526,7 @@ int validate_mx(const MxArgs& g, bool* empty, bool* zero_fill) {
   *empty = false;
   *zero_fill = false;
   if (g.a_type < 0 || g.a_type > 2 || g.out_t < 0 || g.out_t > 2) return kErrDtype;
+  if (g.out_t == 2 && (g.E != 0 || g.a_type != 2)) return kErrDtype;  // only the dense product of codes is added to C
   if (g.E < 0 || g.E > kMaxGroupExperts || g.M < 0 || g.N < 0 || g.K < 0 || g.K % 32 != 0) return kErrShape;
   if (g.M == 0 || g.N == 0) {
     *empty = true;

@@ -61,7 +61,7 @@ int fp8bq_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* qa, int64_t
 /*
  * Linear layer with 4-bit weights: Y [M, N] = Q(X [M, K]) . W [N, K]^T, X quantized by the rule above inside the
  * call.  The result is that of fp8bq_quantize_mxfp4 followed by fp8bq_gemm_mxfp4 up to the order of the FP32 sum.
- *   x   [M, K] BF16 or FP32, row stride ldx.
+ *   x   [M, K] BF16 or FP32, row stride ldx.   y  [M, N] BF16 or FP32.
  *   ws  at least fp8bq_linear_mxfp4_workspace_size(M, N, K) bytes (0 for a few tokens: the codes of X then
  *       never leave the registers).
  */
@@ -74,6 +74,7 @@ int fp8bq_linear_mxfp4(int64_t M, int64_t N, int64_t K, const void* x, fp8bq_in 
  * The two grouped by expert (offsets [E + 1], stacked weights and untouched rows as in fp8bq_grouped.h):
  *   Y_e [n_e, N] = X_e [n_e, K] . W_e [N, K]^T for the rows of every expert e.
  *   qa/sa  codes of X [T, K] (row outputs);  x  X itself.   qw  [E N, K / 2];  sw  [ceil(K / 128)][E N] words.
+ *   y  [T, N] BF16 or FP32.
  *   K % 32 == 0, K >= 32; N any; E N < 2^30.
  */
 size_t fp8bq_grouped_gemm_mxfp4_workspace_size(int64_t E, int64_t T, int64_t N, int64_t K);
