@@ -53,13 +53,6 @@ struct MxTile {
   static constexpr int kMinWaves = kBlocks * NW / 4;
   static_assert(kLds <= 160 * 1024, "LDS ring does not fit");
 };
-// 16-byte chunk swizzle inside a row of 64 or 128 bytes: any 16 lanes of a fragment read (rows r .. r + 15, one
-// logical chunk) cover all 64 banks once.
-template <int STEPS>
-__device__ __forceinline__ int mx_swz(int row) {
-  return STEPS == 2 ? (row >> 2) & 3 : swz(row);
-}
-
 template <int BM, int BN, int WGM, int WGN, int STEPS, int NST, int OUT, bool GROUPED>
 __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NST>::kMinWaves)) void mx_gemm_kernel(
     MxDesc d, uint32_t tiles_m, uint32_t tiles_n, int nsplit, float* __restrict__ partial, int64_t ldp, int vec,
@@ -74,6 +67,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
   constexpr int SJ = STEPS / 2 * (BM + BN) / 64;         // scale jobs of 64 words
   constexpr int SL = SJ > NW ? SJ / NW : 1;              // (with fewer jobs than waves some are loaded twice)
   constexpr int LOADS = AL + BL + SL;
+  static_assert(CH == 8, "the chunk swizzle is that of 128-byte rows");
   static_assert((SJ % NW == 0 || NW % SJ == 0) && BM / RPL % NW == 0 && BN / RPL % NW == 0, "loads split evenly");
   // (one array: a second __shared__ object makes the compiler wait for every LDS-DMA load in flight before
   // each LDS read)
@@ -141,13 +135,13 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
     for (int i = 0; i < AL; ++i) {
       const int row = RPL * (wid + NW * i) + lane / CH;
       const int64_t r = row < mleft ? row : mleft;
-      aoff[i] = (uint32_t)(r * d.lda) + (uint32_t)(((lane % CH) ^ mx_swz<STEPS>(row)) * 16);
+      aoff[i] = (uint32_t)(r * d.lda) + (uint32_t)(((lane % CH) ^ swz(row)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
       const int row = RPL * (wid + NW * i) + lane / CH;
       const int64_t r = row < nleft ? row : nleft;
-      boff[i] = (uint32_t)(r * d.ldb) + (uint32_t)(((lane % CH) ^ mx_swz<STEPS>(mx_rho(row))) * 16);
+      boff[i] = (uint32_t)(r * d.ldb) + (uint32_t)(((lane % CH) ^ swz(mx_rho(row))) * 16);
     }
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
@@ -168,7 +162,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
     } else {
       const int q = i - AL - BL;
       const int word = STEPS / 2 * lkb + sword[q];
-      const bool in = STEPS == 2 || word < nwords;  // (past the last word: zeros)
+      const bool in = word < nwords;  // (past the last word: zeros)
       dma4(rsrc_of(sbase[q] + (in ? word : 0) * sld[q], in ? sbytes[q] : 0u), soff[q],
            stg + Tile::kSA + 256 * ((wid + NW * q) % SJ));
     }
@@ -198,7 +192,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
   int ckb = C.kb0;
   const int r32 = lane & 31, h = lane >> 5;
   const int arow = wm * WTM + r32, brow = wn * WTN + mx_row_of_rho(r32);
-  const int sw = mx_swz<STEPS>(r32);  // (patches start at multiples of 32 rows)
+  const int sw = swz(r32);  // (patches start at multiples of 32 rows)
   auto aread = [&](const uint8_t* stg, int i, int step) {
     return *reinterpret_cast<const v4i*>(stg + (arow + 32 * i) * Tile::kRow + (((2 * step + h) ^ sw) << 4));
   };
