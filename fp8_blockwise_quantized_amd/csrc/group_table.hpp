@@ -2,7 +2,8 @@
 //
 // offsets[0..E] (int64, on the device) hold where each expert's tokens begin; the tokens of expert e
 // are offsets[e] .. offsets[e+1]-1.  The values come from a router on the device, so a kernel makes them
-// safe itself: each is clamped to [0, T] and to at least the one before it, whatever the buffer holds.
+// safe itself: each is clamped to [0, T] (the padded rows where the contraction runs over the tokens) and to at
+// least the one before it, whatever the buffer holds.
 // One wave builds the tables in LDS: lane l owns experts 8l .. 8l+7 and two wave scans (a maximum for
 // the clamped offsets, a sum for the counts) join the lanes; about a microsecond, most of it the load.
 #pragma once

@@ -12,9 +12,9 @@
  * with the quantization rule, scale layouts, accumulation and output types of fp8bq.h.
  *
  * The counts stay on the device: no call reads offsets on the host or waits for it.  The kernels make the
- * offsets safe themselves (each is taken as at least the one before it and at most T), so no content of
- * that buffer leads to an access outside the matrices; offsets that do not ascend give unspecified
- * values.  offsets[0] > 0 or offsets[E] < T is allowed: rows outside every expert are not read, and their
+ * offsets safe themselves (each is taken as at least the one before it and at most the rows that the call
+ * knows: T, for wgrad the padded ones), so no content of that buffer leads to an access outside the
+ * matrices; offsets that do not ascend, or lie past T, give unspecified values.  offsets[0] > 0 or offsets[E] < T is allowed: rows outside every expert are not read, and their
  * output rows are left as they are (a token buffer may be larger than the step's tokens).
  *
  * Conventions, alignment, errors and stream order as in fp8bq.h; offsets is 8-byte aligned.
