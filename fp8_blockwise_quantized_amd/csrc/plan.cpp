@@ -123,6 +123,8 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
 // Stored past the caches, an output neither pushes what is in them out nor has to be written back from the L2 when the
 // kernel ends; kept, it is there for whatever reads it or is written over it next.  us of the product and of the product
 // with a reader of its output, each kept / past; output, and output and operands, in MB.  BF16, read by the row quantizer:
+//   2, 7       8.4 / 8.4      12.6 / 13.4        kept
+//   4, 11      10.4 / 10.2    15.4 / 15.8
 //   8, 16      14.0 / 13.2    21.4 / 21.3        past
 //   34, 54     33.5 / 31.7    43.4 / 42.7
 //   67, 105    62.9 / 63.0    80.6 / 85.2        past all the same: other work's operands lose more than the reader gains (a
@@ -142,7 +144,7 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
 // Added to the output, whose lines the addition has just read: 268 MB 182 / 183, 1476 MB 818 / 827: kept.
 bool stores_past_caches(int out_t, double out, double operands) {
   if (out_t == 2) return false;
-  return out < 100e6 || (out_t == 1 ? out > 320e6 : out + operands > 215e6);
+  return out >= 6e6 && (out < 100e6 || (out_t == 1 ? out > 320e6 : out + operands > 215e6));
 }
 
 // Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that

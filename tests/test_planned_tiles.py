@@ -41,12 +41,13 @@ def test_grouped_weight_gradients(plan, name):
 
 def test_outputs_that_the_caches_hold_for_their_reader_are_kept_there(plan):
     """BF16 outputs from 100 MB on that fit the 256 MB cache with their operands (8192 x 8192 x 2048, 32768 x 2048 x 2048)
-    are not stored past it; those that do not, and smaller ones, are.  FP32 outputs stay up to 320 MB, and what is added
-    to an output always."""
+    are not stored past it; those that do not, and smaller ones, are, down to 6 MB.  FP32 outputs stay up to 320 MB, and
+    what is added to an output always."""
     def past(M, N, K, out=0):
         return plan("stores", out, (4 if out else 2) * M * N, (M + N) * K) == [1]
 
     assert not past(8192, 8192, 2048) and not past(32768, 2048, 2048)
+    assert not past(512, 2048, 2048) and not past(1, 11264, 2048)
     assert past(16384, 11264, 2048) and past(8192, 11264, 2048) and past(16384, 2048, 2048) and past(2048, 2048, 2048)
     assert not past(8192, 8192, 2048, 1) and past(16384, 11264, 2048, 1) and past(2048, 2048, 2048, 1)
     assert not past(8192, 8192, 2048, 2) and not past(16384, 11264, 2048, 2) and not past(2048, 2048, 2048, 2)
