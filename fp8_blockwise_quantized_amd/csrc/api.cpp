@@ -98,7 +98,8 @@ static int run_gemm(const GemmArgs& g, void* stream) {
     d.sb_kstride = g.ldsb;     // sxt[mb * ldsxt + k]
     d.sb_nstride = 0;
   }
-  d.past = stores_past_caches(g.out_t, (double)d.M * (double)d.N * oes, ((double)d.M + (double)d.N) * (double)d.K);
+  d.past = stores_past_caches(g.out_t, (double)d.M * (double)d.N * oes, ((double)d.M + (double)d.N) * (double)d.K,
+                              d.ldc * oes % 8192 == 0);
   void* ws_gemm = plan.ws_gemm ? (uint8_t*)g.ws + plan.ws_transpose : nullptr;
   const int kop = g.op == kOpDgradWt ? kOpDgrad : (g.op == kOpTensor ? kOpFprop : g.op);
   return launched(launch_gemm(kop, d, plan, ws_gemm, s));

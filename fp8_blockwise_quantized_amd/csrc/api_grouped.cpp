@@ -46,7 +46,8 @@ static int run_grouped(const GroupedArgs& g, void* ws, size_t ws_bytes, void* st
   d.sb_nstride = g.op == kOpFprop ? g.ldsb : g.op == kOpDgrad ? 1 : 0;
   const double rows_b = g.op == kOpWgrad ? (double)g.K : (double)g.E * (double)d.N;
   const double out = (g.op == kOpWgrad ? (double)g.E : 1.0) * (double)d.M * (double)d.N * (g.out_t == 0 ? 2 : 4);
-  d.past = stores_past_caches(g.out_t, out, ((double)d.M + rows_b) * (double)d.K);
+  d.past = stores_past_caches(g.out_t, out, ((double)d.M + rows_b) * (double)d.K,
+                              g.op != kOpWgrad && d.ldc * (g.out_t == 0 ? 2 : 4) % 8192 == 0);
   return launched(launch_grouped_gemm(g.op, d, GroupDesc{(const int64_t*)g.offsets, (int)g.E, g.T, plan.ws_gemm ? ws : nullptr}, plan,
                                       s));
 }

@@ -76,7 +76,8 @@ static int run_mx(const MxArgs& g, void* ws, size_t ws_bytes, void* stream) {
   d.N = g.N;
   d.K = g.K;
   d.past = stores_past_caches(g.out_t, (double)g.M * (double)g.N * (g.out_t == 0 ? 2 : 4),
-                              ((double)g.M + (g.E ? (double)g.E : 1.0) * (double)g.N) * (double)g.K * 0.53);
+                              ((double)g.M + (g.E ? (double)g.E : 1.0) * (double)g.N) * (double)g.K * 0.53,
+                              g.ldout * (g.out_t == 0 ? 2 : 4) % 16384 == 0);
   if (linear && !plan.fused) {
     uint8_t* q = (uint8_t*)ws;
     uint32_t* sc = (uint32_t*)((uint8_t*)ws + space.codes);

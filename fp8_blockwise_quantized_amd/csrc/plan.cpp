@@ -121,30 +121,33 @@ GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count) {
 }
 
 // Stored past the caches, an output neither pushes what is in them out nor has to be written back from the L2 when the
-// kernel ends; kept, it is there for whatever reads it or is written over it next.  us of the product and of the product
-// with a reader of its output, each kept / past; output, and output and operands, in MB.  BF16, read by the row quantizer:
-//   2, 7       8.4 / 8.4      12.6 / 13.4        kept
-//   4, 11      10.4 / 10.2    15.4 / 15.8
-//   8, 16      14.0 / 13.2    21.4 / 21.3        past
-//   34, 54     33.5 / 31.7    43.4 / 42.7
-//   67, 105    62.9 / 63.0    80.6 / 85.2        past all the same: other work's operands lose more than the reader gains (a
-//                                                decoder block's step, six of whose outputs have 67 or 84 MB, 2562 / 2529)
-//   134, 168   115 / 125      152 / 167          kept
-//   134, 205   118 / 118      154 / 161
-//   185, 225   169 / 168      230 / 219          past: all of it does not fit the 256 MB cache beside its reader
-//   369, 426   350 / 308      476 / 433
-// (MXFP4: 21, 29 MB 20.6 / 18.4 and 28.6 / 27.1; 134, 152 MB 76 / 83 and 112 / 125; 369, 399 MB 235 / 195 and 365 / 323.
-// Weight gradients of 64 experts, 738 MB, 376 / 320 and 652 / 613.)  FP32, read by a copy to BF16:
-//   17, 21     13.2 / 12.4    20.9 / 20.1        past
-//   67, 76     28.9 / 28.5    44.1 / 43.8
-//   268, 285   99 / 109       183 / 187          kept
-//   268, 336   279 / 279      351 / 367
-//   369, 529   748 / 728      848 / 827          past
-//   738, 768   297 / 241      507 / 466
-// Added to the output, whose lines the addition has just read: 268 MB 182 / 183, 1476 MB 818 / 827: kept.
-bool stores_past_caches(int out_t, double out, double operands) {
-  if (out_t == 2) return false;
-  return out >= 6e6 && (out < 100e6 || (out_t == 1 ? out > 320e6 : out + operands > 215e6));
+// kernel ends; kept, it is there for whatever reads it next, and the caches spread its lines over the memory channels:
+// where rows lie a multiple of 8 KB apart, the rows of a tile share a few channels, and stores past the caches wait for
+// those.  us of one product after the other, and in turn with the quantizer of three inputs, each kept / past:
+//   BF16 rows of a multiple of 8 KB (MXFP4: 16 KB), output and operands within the 256 MB cache: kept
+//     8192 x 8192 x 2048 (134 MB)     124 / 133    137 / 143     (rows 512 bytes longer 124 / 123, 137 / 136)
+//     8192 x 4096 x 2048 (67 MB)      63 / 68      74 / 79       16384 x 4096 x 2048 (134 MB)  123 / 126   149 / 144
+//     wgrad 2048 x 8192 x 8192        136 / 146    152 / 156     MXFP4 8192 x 8192 x 2048      74 / 84     85 / 92
+//   the same with less output (48 MB): past
+//     wgrad 2048 x 4096 x 4096        38 / 37      47 / 46       MXFP4 2048 x 8192 x 2048      22 / 22     29 / 29
+//   or more than the cache: past
+//     16384 x 8192 x 2048 (268 MB)    248 / 247    295 / 268     (12288 x 8192 x 2048, 201 MB    180 / 187   207 / 203)
+//   other BF16 rows: past
+//     16384 x 2048 x 2048 (67 MB)     65 / 65      87 / 82       32768 x 2048 x 2048 (134 MB)  122 / 124   173 / 167
+//     MXFP4 16384 x 3328 x 2048       70 / 69      89 / 85       16384 x 11264 x 2048 (369 MB) 350 / 308
+//     (a decoder block's step, six of whose outputs have 67 or 84 MB, 2562 / 2529)
+//   MXFP4 rows of 8 KB: past (16384 x 4096 x 2048 72 / 80 and 93 / 97, but through the linear layer 104 / 96)
+//   grouped weight gradients, whose rows' tiles are dealt out otherwise: past whatever the rows
+//     8 experts of 2048 x 4096        93 / 85      125 / 107     8 experts of 1024 x 8192      46 / 42     57 / 54
+//   below 6 MB: kept (512 x 2048 x 2048 with the quantizer that reads it 12.6 / 13.4; 4 MB 15.4 / 15.8; 8 MB 21.4 / 21.3)
+// FP32, alone and with a copy to BF16 that reads it: 17 MB 13.2 / 12.4 and 20.9 / 20.1, 67 MB 28.9 / 28.5 and 44.1 / 43.8:
+// past; 268 MB 99 / 109 and 183 / 187, 279 / 279 and 351 / 367: kept; 369 MB 748 / 728 and 848 / 827, 738 MB 297 / 241
+// and 507 / 466: past.  Added to the output, whose lines the addition has just read: 268 MB 182 / 183, 1476 MB
+// 818 / 827: kept.
+bool stores_past_caches(int out_t, double out, double operands, bool crowded) {
+  if (out_t == 2 || out < 6e6) return false;
+  if (out_t == 1) return out < 100e6 || out > 320e6;
+  return !crowded || out < 48e6 || out + operands > 215e6;
 }
 
 // Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that

@@ -126,9 +126,9 @@ struct GemmPlan {
 // dY[M,N] W[N,K]; wgrad: dW[N,K] = dY[M,N]^T X[M,K]).
 GemmPlan plan_gemm(int op, int64_t M, int64_t N, int64_t K, int cu_count);
 
-// Whether a product with that many bytes of output and of operands stores its full output tiles past the caches.
-// out_t: 0 BF16, 1 FP32, 2 FP32 added to the output.
-bool stores_past_caches(int out_t, double out, double operands);
+// Whether a product with that many bytes of output and of operands stores its full output tiles past the caches.  out_t:
+// 0 BF16, 1 FP32, 2 FP32 added to the output; crowded: the output's rows lie a multiple of 8 KB (MXFP4: 16 KB) apart.
+bool stores_past_caches(int out_t, double out, double operands, bool crowded);
 
 // Plan of a product grouped by expert: tile shape and persistent grid.  op is kOpFprop, kOpDgrad or
 // kOpWgrad; T tokens on E experts; N, K as in plan_gemm.  The tokens of each expert are known on the device

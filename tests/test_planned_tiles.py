@@ -39,16 +39,19 @@ def test_grouped_weight_gradients(plan, name):
         assert tile == rows and (sets > 0) == (split and ws == 1)
 
 
-def test_outputs_that_the_caches_hold_for_their_reader_are_kept_there(plan):
-    """BF16 outputs from 100 MB on that fit the 256 MB cache with their operands (8192 x 8192 x 2048, 32768 x 2048 x 2048)
-    are not stored past it; those that do not, and smaller ones, are, down to 6 MB.  FP32 outputs stay up to 320 MB, and
-    what is added to an output always."""
-    def past(M, N, K, out=0):
-        return plan("stores", out, (4 if out else 2) * M * N, (M + N) * K) == [1]
+def test_which_outputs_the_caches_keep(plan):
+    """BF16 outputs of 48 MB and more whose rows lie a multiple of 8 KB apart, where they fit the 256 MB cache with their
+    operands (8192 x 8192 x 2048), and all below 6 MB; FP32 outputs from 100 to 320 MB and below 6; whatever is added to
+    its output."""
+    def past(M, N, K, out=0, ld=None):
+        size = 4 if out else 2
+        return plan("stores", out, size * M * N, (M + N) * K, int(size * (ld or N) % 8192 == 0)) == [1]
 
-    assert not past(8192, 8192, 2048) and not past(32768, 2048, 2048)
+    assert not past(8192, 8192, 2048) and not past(8192, 4096, 2048) and not past(4096, 16384, 1024)
+    assert past(8192, 8192, 2048, ld=8448) and past(8192, 7936, 2048) and not past(8192, 7936, 2048, ld=8192)
+    assert past(16384, 8192, 2048) and past(4096, 4096, 4096)
+    assert past(16384, 11264, 2048) and past(16384, 2048, 2048) and past(16384, 2560, 2048) and past(2048, 2048, 2048)
     assert not past(512, 2048, 2048) and not past(1, 11264, 2048)
-    assert past(16384, 11264, 2048) and past(8192, 11264, 2048) and past(16384, 2048, 2048) and past(2048, 2048, 2048)
     assert not past(8192, 8192, 2048, 1) and past(16384, 11264, 2048, 1) and past(2048, 2048, 2048, 1)
     assert not past(8192, 8192, 2048, 2) and not past(16384, 11264, 2048, 2) and not past(2048, 2048, 2048, 2)
 
