@@ -156,11 +156,12 @@ __device__ __forceinline__ Unit unit_of(uint32_t u, uint32_t tiles_m, uint32_t t
 //   kGroupContract  wgrad: the contraction runs over an expert's 128-token blocks (operands quantized
 //                   along the tokens, every expert's tokens padded to whole blocks); C is stacked.
 // Bound by the matrix pipes at the clock the card's power allows, as the dense products, and by what ragged
-// experts add.  32768 tokens: fprop on 64 experts of 2816 x 2048 239 us (1.58 PFLOP/s; matrix pipes busy 45% of the
-// cycles; a tenth of the tiles' rows are past an expert's end); dgrad on 32 experts of 2048 x 1408 106 us
-// (the dense product of the same size 94-112), 112 us with the largest expert 2.5 times the average; wgrad there
-// 155 us (dense, contracted in one piece: 125-135): 32 times the outputs, 184 MB, which a workgroup writes at the
-// end of a round while its matrix pipes idle.
+// experts add.  32768 tokens, us with the operands from HBM (kernel trace), and one after the other on the same ones
+// where that differs: fprop on 64 experts of 2816 x 2048 235-240 (1.6 PFLOP/s; matrix pipes busy 47% of the cycles; a
+// tenth of the tiles' rows are past an expert's end); on 32 experts of 2048 x 1408 dgrad 135-141, 102-111 (35%; the dense
+// product of that size 100) and wgrad 174-185, 141-149 (32%; dense, contracted in one piece, 125): 32 times the outputs,
+// 184 MB, which a workgroup writes at the end of a round while its matrix pipes idle.  wgrad into FP32 there 165-190, added
+// to FP32 284-299: the old values are read where they are added, with nothing between to hide it.
 enum GroupMode : int { kGroupNone = 0, kGroupRowsMode = 1, kGroupWindow = 2, kGroupContract = 3 };
 template <int GM>
 struct GroupArgs {

@@ -4,20 +4,23 @@
 // (v_mfma_scale_f32_32x32x64_f8f6f4, two blocks per operand row), so the whole contraction accumulates in one
 // set of FP32 registers and nothing is folded afterwards.
 //
-// Bound by the matrix pipes at large sizes (a lane of four instructions of this kind reaches 7.1 PFLOP/s on
-// the card): LDS then has to deliver 1 KB per 32-row patch and 64-long step.  A wave tile of 128 x 64 needs 6
-// patch reads for 8 MFMAs of 32 cycles, three quarters of the LDS bandwidth with eight waves.
+// Bound at large sizes by the LDS reads that feed the matrix pipes (busy 46% of the cycles at 16384 x 11264 x 2048; four
+// instructions of this kind on end reach 7.1 PFLOP/s on the card): LDS has to deliver 1 KB per 32-row patch and
+// 64-long step.  A wave tile of 128 x 64 needs 6 patch reads for 8 MFMAs of 32 cycles, three quarters of the LDS
+// bandwidth with eight waves.
 //
 // Layout.  A stage holds 256 values (128 bytes) of the tile's rows of A and B and the two scale words of each
 // row, and arrives by direct global->LDS loads into a ring of two stages; a stage's loads go out between the
 // last MFMAs of the stage whose slot it takes.  16-byte chunks are XOR-swizzled by row.  The MFMA's first operand
 // is the B patch: lane l ends with row l % 32 of the A patch and 16 of the B patch's 32 columns, B patch rows
 // being permuted so that those 16 are two runs of eight.
-// Measured (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3): 222 / 99 / 252, that is 3.4 / 3.8 / 4.4 PFLOP/s.
+// Measured (us for 16384 x 11264 x 2048 / 2048 x 5632 x 16384 / 8192^3): 196-219 / 99 / 245-252, that is 3.4-3.9 / 3.8 /
+// 4.4-4.5 PFLOP/s, by card.
 // Alternatives, against 285 / 122 / 284 for this form with other stores on a slower card: loads all issued after the
 // barrier 294 / 132 / 287; four stages of 128 values 304 / 128 / 295; 128 x 256 tiles, two workgroups per CU
-// 345 / 148 / 344.  Without the loads 8192^3 took 228 us, without loads, barriers and writes 217: the matrix pipes
-// with the LDS reads they need are the larger part, at the clock the card's power allows them.
+// 345 / 148 / 344.  Without the loads 8192^3 took 228 us, without loads, barriers and writes 217 (the bare instructions
+// would take 155): the matrix pipes with the LDS reads they need are the larger part, at the clock the card's power
+// allows them.
 //
 // A lane's operand is block l / 32 of a 64-long step; it shifts the row's scale word by 8 (l / 32) once per
 // 128-long stretch, and the instruction's byte select (0 or 2) picks the step.  The words of a contraction's

@@ -151,11 +151,10 @@ bool stores_past_caches(int out_t, double out, double operands, bool crowded) {
 }
 
 // Blocks of 128 tokens that the longest expert has to be able to have before the grouped wgrad may split it.  The pass that
-// adds up the chunks costs 3 us, also where the counts then split nothing (32 experts, 32768 tokens, 2048 x 1408, no
-// expert much above the others: 155 us without, 158 us with it; 8 experts, 30000 tokens, 512 x 512, even: 30 and 33 us).
-// Uneven experts gain more (us, whole and split): 25% (62%) of the tokens on one of the 32 experts 189 / 166
-// (306 / 182), 62% on one of the 8 experts 111 / 34, the same at 8000 tokens on 4 experts of 1024 x 1024
-// 38 / 32; at 4096 tokens nothing.
+// adds up the chunks costs 3 us, also where the counts then split nothing (8 experts, 30000 tokens, 512 x 512, even:
+// 30 and 33 us).  Uneven experts gain more (us, whole and split; 32 experts of 2048 x 1408, 32768 tokens): 25% (62%) of
+// the tokens on one of the 32 experts 198 / 166 (313 / 169), 62% on one of the 8 experts 105 / 32, the same at 8000
+// tokens on 4 experts of 1024 x 1024 35 / 32; at 4096 tokens nothing.
 constexpr int64_t kMinSplitBlocks = 48;
 
 // Splitting of the grouped wgrad's long experts with tiles of shape s: up to two sets of partial sums for every
