@@ -43,7 +43,8 @@ Allocating helpers (outputs created with torch on the input's device):
         in-place normalized update of an FP32 weight (and projection onto `radius` if > 0)
         (accumulate=True: out, an FP32 main-grad buffer, receives out + dW)
 
-The layer grouped by expert is in ``grouped.py`` and the layer in MXFP4 in ``mx.py``; their names are here too.
+The layer grouped by expert is in ``grouped.py``, the layer in MXFP4 in ``mx.py`` and the layer in 8-bit integers in
+``int8.py``; their names are here too.
 """
 
 import ctypes
@@ -690,3 +691,10 @@ from .mx import (fp8bq_gemm_mxfp4, fp8bq_gemm_mxfp4_workspace_size, fp8bq_groupe
                  fp8bq_grouped_linear_mxfp4_workspace_size, fp8bq_linear_mxfp4, fp8bq_linear_mxfp4_workspace_size,
                  fp8bq_quantize_mxfp4, gemm_mxfp4, grouped_gemm_mxfp4, grouped_linear_mxfp4, linear_mxfp4,
                  quantize_mxfp4, quantize_mxfp4_dual, quantize_mxfp4_t)
+
+# the linear layer in 8-bit integers (include/fp8bq_int8.h)
+from .int8 import (fp8bq_gemm_int8, fp8bq_gemm_int8_workspace_size, fp8bq_grouped_gemm_int8,  # noqa: E402,F401
+                   fp8bq_grouped_gemm_int8_workspace_size, fp8bq_grouped_linear_int8,
+                   fp8bq_grouped_linear_int8_workspace_size, fp8bq_linear_int8, fp8bq_linear_int8_workspace_size,
+                   fp8bq_quantize_int8, fp8bq_quantize_int8_t, fp8bq_quantize_int8_t_workspace_size, gemm_int8,
+                   grouped_gemm_int8, grouped_linear_int8, linear_int8, quantize_int8, quantize_int8_t)

@@ -6,9 +6,13 @@ the first tensor's, passed around as its index (tensor.get_device(): an integer,
 one that is no CUDA (HIP) device and comes last, so that a wrong type or shape is named first.
 """
 
+import functools
+
 import torch
 
 U8 = (torch.uint8,)
+I8 = (torch.int8,)
+I32 = (torch.int32,)
 F32 = (torch.float32,)
 I64 = (torch.int64,)
 HI = (torch.bfloat16, torch.float32)
@@ -90,6 +94,31 @@ def space(ws, device):
     if ws.get_device() != device:
         raise ValueError(f"ws is on {ws.device}, the call's tensors elsewhere")
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def vector(t, name, n, dtypes, device):
+    """Address of a contiguous vector of n elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != (n,) or t.get_device() != device:
+        _refuse(t, name, (n,), dtypes, device)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name}: expected a contiguous vector")
+    return t.data_ptr()
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def on_its_device(fn):
+    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that."""
+
+    @functools.wraps(fn)
+    def call(first, *args, **kwargs):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda or first.get_device() == _current_device():
+            return fn(first, *args, **kwargs)
+        with torch.cuda.device(first.get_device()):
+            return fn(first, *args, **kwargs)
+
+    return call
 
 
 def stacked(rows, E, what):

@@ -134,6 +134,31 @@ hipError_t launch_mx_skinny(const MxDesc& d, const MxGroups& grp, const MxPlan& 
 // Many rows, A in codes; ws: p.ws bytes of partial sums.
 hipError_t launch_mx_gemm(const MxDesc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st);
 
+// 8-bit integers with a scale for each row: quantizers of rows, and of columns with transposed codes
+// (ws: int8_col_chunks(R, C) * C floats), and products C[m, n] = sa[m] sb[n] sum_k A[m, k] B[n, k].
+hipError_t launch_int8_rows(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
+                            hipStream_t st);
+int int8_col_chunks(int64_t R, int64_t C);
+hipError_t launch_int8_cols(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, uint8_t* qt, int64_t ldqt,
+                            float* st_, void* ws, hipStream_t st);
+struct Int8Desc {
+  const void* a;  // codes (lda bytes a row) with scales sa, or BF16 / FP32 values (lda elements a row)
+  int64_t lda;
+  const float* sa;
+  int a_type;     // MxA
+  const uint8_t* b;
+  int64_t ldb;
+  const float* sb;
+  void* c;
+  int64_t ldc;
+  int out_t;      // as in MxDesc
+  int past;
+  int64_t M, N, K;
+};
+// Groups and plans as for MXFP4.
+hipError_t launch_int8_skinny(const Int8Desc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st);
+hipError_t launch_int8_gemm(const Int8Desc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st);
+
 // Byte-matrix transpose: dst[c * ldd + r] = src[r * lds + c] for r < R, c < C (R, C multiples of 128).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t lds, uint8_t* dst, int64_t ldd, int64_t R, int64_t C,
                                hipStream_t st);

@@ -30,18 +30,9 @@
 // Workgroups are persistent and the ring runs on across tiles, as in the FP8 kernel.
 #include "gemm_kernel.hpp"
 #include "mx_common.hpp"
+#include "tile_store.hpp"
 
 namespace fp8bq {
-
-// B patch: tile row n of MFMA row rho = 8 a + 4 h + b (lane half h, accumulators 4 a + b), so that a half holds
-// columns 8 h .. +7 and 16 + 8 h .. +7 of the patch; and the inverse.
-__device__ __forceinline__ int mx_row_of_rho(int rho) {
-  const int a = rho >> 3, h = (rho >> 2) & 1, b = rho & 3;
-  return 16 * (a >> 1) + 8 * h + 4 * (a & 1) + b;
-}
-__device__ __forceinline__ int mx_rho(int n) {
-  return 8 * (2 * ((n >> 4) & 1) + ((n >> 2) & 1)) + 4 * ((n >> 3) & 1) + (n & 3);
-}
 
 // LDS ring: NST stages of STEPS 64-long steps.
 template <int BM, int BN, int NW, int STEPS, int NST>
@@ -144,7 +135,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
     for (int i = 0; i < BL; ++i) {
       const int row = RPL * (wid + NW * i) + lane / CH;
       const int64_t r = row < nleft ? row : nleft;
-      boff[i] = (uint32_t)(r * d.ldb) + (uint32_t)(((lane % CH) ^ swz(mx_rho(row))) * 16);
+      boff[i] = (uint32_t)(r * d.ldb) + (uint32_t)(((lane % CH) ^ swz(rho_of_row(row))) * 16);
     }
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
@@ -194,7 +185,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
   UnitT C = L;
   int ckb = C.kb0;
   const int r32 = lane & 31, h = lane >> 5;
-  const int arow = wm * WTM + r32, brow = wn * WTN + mx_row_of_rho(r32);
+  const int arow = wm * WTM + r32, brow = wn * WTN + row_of_rho(r32);
   const int sw = swz(r32);  // (patches start at multiples of 32 rows)
   auto aread = [&](const uint8_t* stg, int i, int step) {
     return *reinterpret_cast<const v4i*>(stg + (arow + 32 * i) * Tile::kRow + (((2 * step + h) ^ sw) << 4));
@@ -301,127 +292,11 @@ __global__ __launch_bounds__(WGM* WGN * 64, (MxTile<BM, BN, WGM * WGN, STEPS, NS
       if (nsplit > 1 || OUT != 0) {
         const int64_t ldo = nsplit > 1 ? ldp : d.ldc;
         float* o = (nsplit > 1 ? partial + (int64_t)C.split * d.M * ldp : reinterpret_cast<float*>(d.c)) + m * ldo + n0 + ccol;
-        const bool add = OUT == 2 && nsplit == 1;
-        if (full) {
-          // A lane's four 16-byte chunks of a patch row and the four rows 8 apart of the lanes l ^ 8, l ^ 16, l ^ 24 change
-          // places, so that a store instruction writes eight rows of a patch, whole 128-byte lines (us with the chunks
-          // where they are and so, added to the output: 8192^3 395 / 347, 16384 x 2048 x 5632 138 / 117).
-          o += 16 * (lane >> 4 & 1) + 4 * (lane >> 3 & 1) - (lane & 24) * ldo;
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-              const v16f& v = acc[i][j];
-              v4i x[4], w[4];  // chunks 0 and 1 of rows l % 16 and 16 + l % 16; then rows l % 8 + 0, 8, 16, 24
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[4 * r + k]),
-                                                                  __float_as_uint(v[8 + 4 * r + k]), false, false);
-                  x[r][k] = (int)p[0];
-                  x[2 + r][k] = (int)p[1];
-                }
-              join_halves(x[0], x[1], w[0], w[1]);
-              join_halves(x[2], x[3], w[2], w[3]);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                v4f s = __builtin_bit_cast(v4f, w[q]);
-                v4f* o4 = reinterpret_cast<v4f*>(o + (32 * i + 8 * q) * ldo + 32 * j);
-                if (add) s = *o4 + s;
-                store_line(s, o4, past && OUT != 2);
-              }
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int64_t c = 32 * j + 16 * (r >> 1) + 4 * (r & 1);
-                float* p = o + 32 * i * ldo + c;
-                if (m + 32 * i >= mlim || n0 + c >= nlim) continue;
-                if (vec && n0 + c + 4 <= nlim) {
-                  v4f w = {acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
-                  if (add) w = *reinterpret_cast<v4f*>(p) + w;
-                  *reinterpret_cast<v4f*>(p) = w;
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    if (n0 + c + k < nlim) p[k] = add ? p[k] + acc[i][j][4 * r + k] : acc[i][j][4 * r + k];
-                }
-              }
-        }
+        store_tile_f32<OUT == 2>(acc, o, ldo, TileEdge{m, n0, mlim, nlim, full, vec != 0}, OUT == 2 && nsplit == 1,
+                                 OUT != 0 && past, lane);
       } else {
         uint16_t* o = reinterpret_cast<uint16_t*>(d.c) + m * d.ldc + n0 + ccol;
-        if (full) {
-          // a lane's two 16-byte chunks of a patch row: lanes l and l + 16 swap one, so that a store instruction
-          // writes 64 contiguous bytes of 16 rows (four lanes each) and not 32 of 32 rows
-          uint16_t* s0 = reinterpret_cast<uint16_t*>(d.c) +
-                         ((int64_t)C.m0 + wm * WTM + (lane & 15)) * d.ldc + n0 + ccol + (lane & 16);
-          auto rows = [&](const v16f& v, v4i& x, v4i& y) {  // rows 0 .. 15 and 16 .. 31 of the patch
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const auto p = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[2 * r], v[2 * r + 1]),
-                                                              pack_bf16x2(v[8 + 2 * r], v[9 + 2 * r]), false, false);
-              x[r] = (int)p[0];
-              y[r] = (int)p[1];
-            }
-          };
-          if constexpr (NI == 2) {
-            // two patches side by side: whole 128-byte lines.  Where they go past the caches (stores_past_caches) that is
-            // what makes it worth it: us with 64-byte stores, whole lines, and whole lines past the caches
-            // 16384 x 11264 x 2048 242 / 238 / 209, 4096 x 2560 x 2048 20.4 / 20.6 / 18.4.
-            const int half = (lane >> 3) & 1;
-            s0 += 32 * half - 8 * half * d.ldc;
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-              v4i x[2], y[2], upper, lower;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) rows(acc[i][j], x[j], y[j]);
-              uint16_t* s = s0 + 32 * i * d.ldc;
-              join_halves(x[0], x[1], upper, lower);
-              store_line(upper, reinterpret_cast<v4i*>(s), past);
-              store_line(lower, reinterpret_cast<v4i*>(s + 8 * d.ldc), past);
-              join_halves(y[0], y[1], upper, lower);
-              store_line(upper, reinterpret_cast<v4i*>(s + 16 * d.ldc), past);
-              store_line(lower, reinterpret_cast<v4i*>(s + 24 * d.ldc), past);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-              for (int j = 0; j < NI; ++j) {
-                v4i x, y;
-                rows(acc[i][j], x, y);
-                uint16_t* s = s0 + 32 * i * d.ldc + 32 * j;
-                *reinterpret_cast<v4i*>(s) = x;
-                *reinterpret_cast<v4i*>(s + 16 * d.ldc) = y;
-              }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const int64_t c = 32 * j + 16 * r;
-                uint16_t* p = o + 32 * i * d.ldc + c;
-                if (m + 32 * i >= mlim || n0 + c >= nlim) continue;
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(acc[i][j][8 * r + 2 * k], acc[i][j][8 * r + 2 * k + 1]);
-                if (vec && n0 + c + 8 <= nlim) {
-                  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    if (n0 + c + k < nlim) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-                }
-              }
-        }
+        store_tile_bf16(acc, o, d.ldc, TileEdge{m, n0, mlim, nlim, full, vec != 0}, past, lane);
       }
 #pragma unroll
       for (int i = 0; i < MI; ++i)

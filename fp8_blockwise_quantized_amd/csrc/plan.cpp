@@ -237,29 +237,9 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
 // MI355X (8192 x 8192 x 8192 with each tile: 275, 340 and 500 us).
 static double mx_stage_us(int shape) { return shape == k256x256 ? 2.1 : shape == k64x64 ? 0.98 : 1.33; }
 
-MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count) {
-  MxPlan p;
-  const int64_t cus = cu_count > 0 ? cu_count : 256;
+// Shape, split and grid of the LDS-tiled kernels: nkb stages of 128 contraction bytes, expected rows p.rows.
+static void plan_tiles(MxPlan& p, int64_t E, int64_t M, int64_t N, int64_t nkb, int64_t cus) {
   const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
-  p.rows = cdiv(M, used);
-  // Few rows on few column tiles: the kernel without LDS staging.  From codes (us, one row and K = 2048; the
-  // tiled kernel second): N = 4096 3.6 / 6.5, 11264 4.7 / 6.5, 22528 6.4 / 7.1, 45056 11.5 / 10.1.
-  const int64_t tiles = used * cdiv(N, 16);
-  p.skinny = M <= 16 && tiles <= 1536;
-  if (p.skinny) {
-    // Every tile quantizes its rows itself while that costs less than a quantizer launch (us, fused and not):
-    // 16 rows, 11264 x 2048 9.4 / 10.5, 16384 x 2048 11.6 / 10.5; 8 rows, 16384 x 2048 9.1 / 9.9, 22528 x 2048
-    // 12.2 / 11.5; 16 rows, 2048 x 11264 15.7 / 12.8; 8 rows, 2048 x 11264 11.4 / 12.4.
-    const int64_t steps = tiles * cdiv(K, 128);
-    p.fused = linear && steps <= 300000 / (p.rows + 8) && p.rows * K <= 131072;
-    p.split_k = 8;
-    while (p.split_k > 1 && p.split_k > cdiv(K, 256)) p.split_k /= 2;
-    const int64_t groups = E == 0 ? 1 : used;
-    const int64_t units = groups * cdiv(N, 8 / p.split_k * 16);
-    p.grid = units < 16 * cus ? units : 16 * cus;
-    return p;
-  }
-  const int64_t nkb = cdiv(K, 256);
   const int shapes[3] = {k256x256, k128x128, k64x64};
   double best = 0.0;
   for (int i = 0; i < 3; ++i) {
@@ -287,6 +267,52 @@ MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_c
   const int64_t g = slots >= 8 ? slots - slots % 8 : slots;
   p.grid = units < g ? units : g;
   p.ws = p.split_k > 1 ? (size_t)p.split_k * (size_t)M * (size_t)(cdiv(N, 4) * 4) * 4 : 0;
+}
+
+MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count) {
+  MxPlan p;
+  const int64_t cus = cu_count > 0 ? cu_count : 256;
+  const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
+  p.rows = cdiv(M, used);
+  // Few rows on few column tiles: the kernel without LDS staging.  From codes (us, one row and K = 2048; the
+  // tiled kernel second): N = 4096 3.6 / 6.5, 11264 4.7 / 6.5, 22528 6.4 / 7.1, 45056 11.5 / 10.1.
+  const int64_t tiles = used * cdiv(N, 16);
+  p.skinny = M <= 16 && tiles <= 1536;
+  if (p.skinny) {
+    // Every tile quantizes its rows itself while that costs less than a quantizer launch (us, fused and not):
+    // 16 rows, 11264 x 2048 9.4 / 10.5, 16384 x 2048 11.6 / 10.5; 8 rows, 16384 x 2048 9.1 / 9.9, 22528 x 2048
+    // 12.2 / 11.5; 16 rows, 2048 x 11264 15.7 / 12.8; 8 rows, 2048 x 11264 11.4 / 12.4.
+    const int64_t steps = tiles * cdiv(K, 128);
+    p.fused = linear && steps <= 300000 / (p.rows + 8) && p.rows * K <= 131072;
+    p.split_k = 8;
+    while (p.split_k > 1 && p.split_k > cdiv(K, 256)) p.split_k /= 2;
+    const int64_t groups = E == 0 ? 1 : used;
+    const int64_t units = groups * cdiv(N, 8 / p.split_k * 16);
+    p.grid = units < 16 * cus ? units : 16 * cus;
+    return p;
+  }
+  plan_tiles(p, E, M, N, cdiv(K, 256), cus);
+  return p;
+}
+
+MxPlan plan_int8(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count) {
+  MxPlan p;
+  const int64_t cus = cu_count > 0 ? cu_count : 256;
+  const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
+  p.rows = cdiv(M, used);
+  const int64_t tiles = used * cdiv(N, 16);
+  p.skinny = M <= 16 && tiles <= 1536;
+  if (p.skinny) {
+    int64_t rows = 1;  // that a workgroup keeps in LDS when it quantizes them itself
+    while (rows < (E == 0 ? M : 16)) rows *= 2;
+    p.fused = linear && rows * (K + 144) <= 65536;
+    p.split_k = 8;
+    while (p.split_k > 1 && p.split_k > cdiv(K, 128)) p.split_k /= 2;
+    const int64_t units = used * cdiv(N, 8 / p.split_k * 16);
+    p.grid = units < 16 * cus ? units : 16 * cus;
+    return p;
+  }
+  plan_tiles(p, E, M, N, cdiv(K, 128), cus);
   return p;
 }
 

@@ -151,5 +151,7 @@ struct MxPlan {
   size_t ws = 0;       // workspace of the product itself
 };
 MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count);
+// The same for 8-bit integers (stages of 128 values instead of 256).
+MxPlan plan_int8(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_count);
 
 }  // namespace fp8bq

@@ -562,17 +562,103 @@ int validate_mx(const MxArgs& g, bool* empty, bool* zero_fill) {
   return kOk;
 }
 
-int check_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed) {
+// A workspace that is needed: large enough, aligned and apart from the call's matrices.
+template <int N>
+static int check_space(const Mat (&m)[N], const void* ws, size_t ws_bytes, size_t ws_needed) {
   if (ws_needed == 0) return kOk;
   if (ws == nullptr || ws_bytes < ws_needed) return kErrWorkspace;
   if (!aligned16(ws)) return kErrAlign;
   if (ws_needed >= (size_t)kMaxExtentBytes) return kErrShape;
   const Mat w{ws, 1, (int64_t)ws_needed, (int64_t)ws_needed, 1};
-  Mat m[6];
-  mx_mats(g, m);
-  for (int i = 0; i < 6; ++i)
+  for (int i = 0; i < N; ++i)
     if (overlaps(w, m[i])) return kErrOverlap;
   return kOk;
+}
+
+int check_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed) {
+  Mat m[6];
+  mx_mats(g, m);
+  return check_space(m, ws, ws_bytes, ws_needed);
+}
+
+// As mx_mats for 8-bit integers.
+static void int8_mats(const MxArgs& g, Mat (&m)[6]) {
+  const int64_t rows_b = g.E ? g.E * g.N : g.N;
+  const bool codes = g.a_type == 2;
+  m[0] = Mat{g.a, g.M, g.K, g.lda, codes ? 1 : g.a_type == 0 ? 2 : 4};
+  m[1] = Mat{g.sa, codes ? 1 : 0, g.M, g.M, 4};
+  m[2] = Mat{g.b, rows_b, g.K, g.ldb, 1};
+  m[3] = Mat{g.sb, 1, rows_b, rows_b, 4};
+  m[4] = Mat{g.out, g.M, g.N, g.ldout, g.out_t == 0 ? 2 : 4};
+  m[5] = Mat{g.offsets, g.E ? 1 : 0, g.E + 1, g.E + 1, 8};
+}
+
+int validate_int8(const MxArgs& g, bool* empty, bool* zero_fill) {
+  *empty = false;
+  *zero_fill = false;
+  if (g.a_type < 0 || g.a_type > 2 || g.out_t < 0 || g.out_t > 2) return kErrDtype;
+  if (g.out_t == 2 && (g.E != 0 || g.a_type != 2)) return kErrDtype;  // only the dense product of codes is added to C
+  if (g.E < 0 || g.E > kMaxGroupExperts || g.M < 0 || g.N < 0 || g.K < 0 || g.K % 16 != 0) return kErrShape;
+  if (g.K >= ((int64_t)1 << 17)) return kErrShape;  // 2^17 products of -128 times -128 pass the 32-bit sum
+  if (g.M == 0 || g.N == 0) {
+    *empty = true;
+    return kOk;
+  }
+  const int64_t kRows = (int64_t)1 << 30;
+  const int64_t copies = g.E ? g.E : 1;
+  if (g.M >= kRows || g.N >= kRows / copies) return kErrShape;
+  // work units of one launch: tiles of at least 16 x 16, every expert with a started one of its own
+  if ((g.M / 16 + copies) * (g.N / 16 + 1) >= ((int64_t)1 << 31)) return kErrShape;
+  Mat m[6];
+  int8_mats(g, m);
+  int st;
+  if (g.out == nullptr) return kErrNull;
+  if ((st = check_mat(m[4], false)) != kOk) return st;
+  if (g.K == 0) {
+    if (g.E) return kErrShape;  // (which rows belong to an expert is not known on the host)
+    *zero_fill = true;
+    return kOk;
+  }
+  for (int i = 0; i < 6; ++i)
+    if (m[i].rows && m[i].p == nullptr) return kErrNull;
+  if (g.E && !aligned8(g.offsets)) return kErrAlign;
+  if ((st = check_mat(m[0], true)) != kOk) return st;
+  if ((st = check_mat(m[2], true)) != kOk) return st;
+  if (m[1].rows && (st = check_mat(m[1], false)) != kOk) return st;
+  if ((st = check_mat(m[3], false)) != kOk) return st;
+  // one tile of a code operand is reached through a 31-bit buffer range
+  const int64_t kSpan = (int64_t)1 << 31;
+  if ((m[1].rows && 255 * g.lda + g.K >= kSpan) || 255 * g.ldb + g.K >= kSpan) return kErrLd;
+  for (int i = 0; i < 6; ++i)
+    if (i != 4 && overlaps(m[4], m[i])) return kErrOverlap;
+  return kOk;
+}
+
+int check_int8_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed) {
+  Mat m[6];
+  int8_mats(g, m);
+  return check_space(m, ws, ws_bytes, ws_needed);
+}
+
+int validate_int8_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, bool columns, const void* q,
+                        int64_t ldq, const void* s, const void* ws, size_t ws_bytes, size_t ws_needed, bool* empty) {
+  *empty = false;
+  if (in_esize(xt) == 0) return kErrDtype;
+  if (R < 0 || C < 0 || C % (columns ? 8 : 16) != 0) return kErrShape;
+  if (R == 0 || C == 0) {
+    *empty = true;
+    return kOk;
+  }
+  const int64_t kMost = (int64_t)1 << 31;
+  if (R >= kMost || C >= kMost || (R / 128 + 1) * (C / 128 + 1) >= kMost) return kErrShape;  // tiles of one launch
+  const Mat mx{x, R, C, ldx, in_esize(xt)};
+  const Mat mq = columns ? Mat{q, C, (R + 15) / 16 * 16, ldq, 1} : Mat{q, R, C, ldq, 1};
+  const int64_t n = columns ? C : R;
+  const Mat ms{s, 1, n, n, 4};
+  const int r = check_quant(mx, mq, ms, false);
+  if (r != kOk) return r;
+  const Mat m[3] = {mx, mq, ms};
+  return check_space(m, ws, ws_bytes, ws_needed);
 }
 
 }  // namespace fp8bq

@@ -137,6 +137,12 @@ struct MxArgs {
   const void* out; int out_t; int64_t ldout;
 };
 int validate_mx(const MxArgs& g, bool* empty, bool* zero_fill);
+// 8-bit integers (include/fp8bq_int8.h): the same arguments, sa [M] and sb [E N] being vectors (no ldsa, ldsb).
+int validate_int8(const MxArgs& g, bool* empty, bool* zero_fill);
+int check_int8_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed);
+// Quantizers: rows (q [R, C]) or transposed columns (q [C, 16 ceil(R / 16)]); s the scales.
+int validate_int8_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, bool columns, const void* q,
+                        int64_t ldq, const void* s, const void* ws, size_t ws_bytes, size_t ws_needed, bool* empty);
 int check_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed);
 
 }  // namespace fp8bq
