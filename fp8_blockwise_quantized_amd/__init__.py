@@ -43,8 +43,8 @@ Allocating helpers (outputs created with torch on the input's device):
         in-place normalized update of an FP32 weight (and projection onto `radius` if > 0)
         (accumulate=True: out, an FP32 main-grad buffer, receives out + dW)
 
-The layer grouped by expert is in ``grouped.py``, the layer in MXFP4 in ``mx.py`` and the layer in 8-bit integers in
-``int8.py``; their names are here too.
+The layer grouped by expert is in ``grouped.py``, the layer in MXFP4 in ``mx.py``, the layer in 8-bit integers in
+``int8.py``, routing and the experts' rows in ``route.py``; their names are here too.
 """
 
 import ctypes
@@ -698,3 +698,9 @@ from .int8 import (fp8bq_gemm_int8, fp8bq_gemm_int8_workspace_size, fp8bq_groupe
                    fp8bq_grouped_linear_int8_workspace_size, fp8bq_linear_int8, fp8bq_linear_int8_workspace_size,
                    fp8bq_quantize_int8, fp8bq_quantize_int8_t, fp8bq_quantize_int8_t_workspace_size, gemm_int8,
                    grouped_gemm_int8, grouped_linear_int8, linear_int8, quantize_int8, quantize_int8_t)
+
+# routing to experts and the experts' rows (include/fp8bq_route.h)
+from .route import (MAX_CHOICES, SCORE_SIGMOID, SCORE_SOFTMAX, combine_rows, combine_rows_backward,  # noqa: E402,F401
+                    expert_rows, fp8bq_combine_rows, fp8bq_combine_rows_backward, fp8bq_expert_rows,
+                    fp8bq_expert_rows_workspace_size, fp8bq_gather_rows, fp8bq_route_experts,
+                    fp8bq_route_experts_backward, gather_rows, route_experts, route_experts_backward)

@@ -159,6 +159,32 @@ struct Int8Desc {
 hipError_t launch_int8_skinny(const Int8Desc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st);
 hipError_t launch_int8_gemm(const Int8Desc& d, const MxGroups& grp, const MxPlan& p, void* ws, hipStream_t st);
 
+// Routing (include/fp8bq_route.h).  A token's k experts and weights from logits [T, E] of type xt; and the gradient.
+constexpr int kMaxRouteExperts = 512;
+struct RouteHow {
+  int experts, k;
+  int score;  // 0 softmax, 1 sigmoid
+  int groups, top_groups, group_best;
+  int renormalize;
+  double scale;
+};
+hipError_t launch_route(const void* x, int xt, int64_t T, int64_t ldx, const RouteHow& how, const float* bias,
+                        int32_t* experts, float* weights, hipStream_t st);
+hipError_t launch_route_backward(const float* dw, const void* x, int xt, int64_t T, int64_t ldx, const RouteHow& how,
+                                 const int32_t* experts, void* dx, int64_t lddx, hipStream_t st);
+// Rows of the experts: n = T k choices sorted by expert (ws: expert_rows_chunks(n) * E counts), and rows of width H
+// on their way there and back.
+int expert_rows_chunks(int64_t n);
+hipError_t launch_expert_rows(const int32_t* experts, int64_t n, int E, int64_t* offsets, int32_t* rows, int32_t* slots,
+                              void* ws, hipStream_t st);
+hipError_t launch_gather_rows(const void* x, int xt, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int64_t k,
+                              void* out, int64_t ldo, hipStream_t st);
+hipError_t launch_combine_rows(const void* y, int yt, int64_t T, int64_t k, int64_t H, int64_t ldy, const int32_t* rows,
+                               const float* weights, void* out, int ot, int64_t ldo, hipStream_t st);
+hipError_t launch_combine_rows_backward(const void* dout, int dt, int64_t lddo, const void* y, int yt, int64_t ldy, int64_t T,
+                                        int64_t k, int64_t H, const int32_t* rows, const float* weights,
+                                        const int32_t* slots, void* dy, int64_t lddy, float* dweights, hipStream_t st);
+
 // Byte-matrix transpose: dst[c * ldd + r] = src[r * lds + c] for r < R, c < C (R, C multiples of 128).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t lds, uint8_t* dst, int64_t ldd, int64_t R, int64_t C,
                                hipStream_t st);

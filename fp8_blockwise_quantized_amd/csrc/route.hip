@@ -1,0 +1,392 @@
+// Routing: from the router's logits [T, E] each token's k experts and their weights, and the logits' gradient.
+//
+// Mathematics.  s = softmax(x) or sigmoid(x), c = s + bias; groups of E / G experts score the sum of their best one or
+// two c, the best `top` groups stay; of their experts the k largest c are chosen, descending; w = scale s, or scale s /
+// (sum of the chosen s).  Without a bias and with groups scored by their best expert the order of c is that of x, and
+// no score is computed for the choice; a normalized softmax then needs the chosen logits only.
+//
+// Near scores: c is computed in 64 bits (about 1e-14, exp64 below) and compared by its first 43 bits and, where those
+// are equal, by the index, the lower first.  In 32 bits one token in some ten thousand would swap two experts.  FP64
+// runs at FP32's rate on this card, so what it costs is registers.
+//
+// Bound by instructions: 16384 tokens of 256 experts are 17 MB, 4 us at the copy's rate, and some 100 wave instructions
+// a token for scores and as many for the choice.  A token is shared by 16 lanes (many tokens) or 64 (few, where latency
+// counts).  The lanes are dealt to the groups first, so that a group's score is a reduction over neighbouring lanes; a
+// lane holds V consecutive experts of its group.  A key is the ordered bits of c with the inverted index in place of the
+// last nine, so keys are distinct, one maximum over the lanes names the winner, and it alone clears its slot.
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace fp8bq {
+
+// e^x in 64 bits for x <= 709 (below -708: 0): 2^n e^r, |r| <= ln 2 / 2, by the Taylor series to r^12 / 12! (the rest is
+// below 2 10^-16).
+__device__ __forceinline__ double exp64(double x) {
+  if (x < -708.0) return 0.0;  // (a NaN goes on)
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  // (ln 2 in two parts, as Cody and Waite do it: the first is its 32 bits behind the point, so n times it is exact)
+  double r = __builtin_fma(n, -0x1.62e42fee00000p-1, x);
+  r = __builtin_fma(n, -0x1.a39ef35793c76p-33, r);
+  double p = 1.0 / 479001600.0;
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+// 1 / v for v >= 1 (infinity: 0): the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double inverse64(double v) {
+  double r = __builtin_amdgcn_rcp(v);
+  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+  return r;
+}
+__device__ __forceinline__ double sigmoid64(double x) {
+  // (e^708 is finite, so the steps stay finite; e^-708 and below are zero as weights in FP32)
+  const double t = x < -708.0 ? -708.0 : x;
+  const double s = inverse64(1.0 + exp64(-(t > 708.0 ? 708.0 : t)));
+  return x < -708.0 ? 0.0 : s;
+}
+
+// Bits of a double in the order of the doubles (NaN: the lowest of all that are not excluded); the last nine bits hold
+// 511 - e.  Excluded slots have the key 0.
+__device__ __forceinline__ uint64_t key_of(double c, int e) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, c + 0.0);  // (-0 and 0 are equal)
+  const uint64_t o = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+  return (c != c ? 512ull : (o & ~511ull)) | (uint64_t)(511 - e);
+}
+
+// The value that lane l ^ d holds (16 <= d), or of the partner in a reduction over 2 d lanes that leaves equal values
+// in the lanes below: xor 1 and 2, then mirrored halves, then a rotation by 8.
+template <int D>
+__device__ __forceinline__ uint32_t partner32(uint32_t v) {
+  if constexpr (D == 1) return dpp_read<kDppXor1>(v);
+  else if constexpr (D == 2) return dpp_read<kDppXor2>(v);
+  else if constexpr (D == 4) return dpp_read<kDppMirror8>(v);
+  else if constexpr (D == 8) return dpp_read<kDppXor8>(v);
+  else return (uint32_t)__shfl_xor((int)v, D);
+}
+template <int D>
+__device__ __forceinline__ uint64_t partner(uint64_t v) {
+  return (uint64_t)partner32<D>((uint32_t)v) | (uint64_t)partner32<D>((uint32_t)(v >> 32)) << 32;
+}
+template <int D>
+__device__ __forceinline__ double partner(double v) {
+  return __builtin_bit_cast(double, partner<D>(__builtin_bit_cast(uint64_t, v)));
+}
+template <int L, int D = 1, typename T, typename F>
+__device__ __forceinline__ T over_lanes(T v, const F& f) {
+  if constexpr (D < L) return over_lanes<L, D * 2>(f(v, partner<D>(v)), f);
+  else return v;
+}
+
+// The lane's experts: e0 .. e0 + n - 1 (n <= V) of the group its lane belongs to.
+template <typename TIn>
+__device__ __forceinline__ double logit_at(const TIn* p) {
+  if constexpr (sizeof(TIn) == 2) return (double)bf16lo(*p);
+  else return (double)*p;
+}
+
+struct RouteArgs {
+  RouteHow how;
+  int lanes_log2;  // of a group
+  int per;         // experts of a group
+  int wide;        // a lane's V logits can be loaded as 16-byte pieces
+};
+
+// Runs f with the number of lanes of a group as a constant.
+template <int L, typename F>
+__device__ __forceinline__ void with_lanes(int log2, const F& f) {
+  switch (log2) {
+    case 0: f(std::integral_constant<int, 1>{}); break;
+    case 1: f(std::integral_constant<int, 2>{}); break;
+    case 2: f(std::integral_constant<int, 4>{}); break;
+    case 3: f(std::integral_constant<int, 8>{}); break;
+    case 4: f(std::integral_constant<int, 16>{}); break;
+    default:
+      if constexpr (L == 64) {
+        if (log2 == 5) f(std::integral_constant<int, 32>{});
+        else f(std::integral_constant<int, 64>{});
+      }
+  }
+}
+
+template <typename TIn, int L, int V>
+__global__ __launch_bounds__(256) void route_kernel(const TIn* __restrict__ x, int64_t T, int64_t ldx, RouteArgs a,
+                                                    const float* __restrict__ bias, int32_t* __restrict__ experts,
+                                                    float* __restrict__ weights) {
+  const int64_t token = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+  if (token >= T) return;  // (all L lanes of a token together; the DPP patterns stay within them)
+  const int lane = threadIdx.x % L;
+  const TIn* xr = x + token * ldx;
+  const RouteHow& how = a.how;
+  const int group = lane >> a.lanes_log2, l = lane & ((1 << a.lanes_log2) - 1);
+  const int first = l * V;  // within the group
+  const int e0 = group * a.per + first;
+  const int n = group < how.groups ? (a.per - first < V ? a.per - first : V) : 0;
+  const double inf = __builtin_inf();
+
+  double c[V];
+  bool loaded = false;
+  if constexpr (V * sizeof(TIn) >= 16) {
+    if (a.wide) {  // (then n is V or not positive)
+      loaded = true;
+      constexpr int P = 16 / sizeof(TIn);
+#pragma unroll
+      for (int j = 0; j < V; j += P) {
+        v4i w = {0, 0, 0, 0};
+        if (n > 0) w = *reinterpret_cast<const v4i*>(xr + e0 + j);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          if constexpr (P == 8) c[j + i] = (double)((i & 1) ? bf16hi((uint32_t)w[i / 2]) : bf16lo((uint32_t)w[i / 2]));
+          else c[j + i] = (double)__int_as_float(w[i]);
+        }
+      }
+    }
+  }
+  if (!loaded) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = j < n ? logit_at(xr + e0 + j) : 0.0;
+  }
+
+  // softmax of all: the largest logit and the sum of the exponentials, where they are needed
+  const bool ordered = bias == nullptr && (how.groups == 1 || how.group_best == 1);  // c has the order of x
+  const bool softmax = how.score == 0;
+  double top = -inf, norm = 0.0;
+  if (softmax && (!ordered || !how.renormalize)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = j < n && c[j] > top ? c[j] : top;
+    top = over_lanes<L>(top, [](double p, double q) { return p > q ? p : q; });
+    const double shift = top == -inf ? 0.0 : top;
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const double e = exp64(c[j] - shift);
+      sum += j < n ? e : 0.0;
+      if (!ordered) c[j] = e;
+    }
+    norm = over_lanes<L>(sum, [](double p, double q) { return p + q; });
+    norm = norm == 0.0 ? 0.0 : 1.0 / norm;  // (every expert switched off: all scores are zero)
+    if (!ordered) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) c[j] *= norm;
+    }
+  } else if (!ordered) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = sigmoid64(c[j]);
+  }
+  if (bias != nullptr) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] += j < n ? (double)bias[e0 + j] : 0.0;
+  }
+
+  bool open = n > 0;
+  if (how.top_groups < how.groups) {
+    double t1 = -inf, t2 = -inf;  // (NaN is below every score)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const double v = j < n && c[j] > -inf ? c[j] : -inf;
+      const double low = v < t1 ? v : t1;
+      t2 = low > t2 ? low : t2;
+      t1 = v > t1 ? v : t1;
+    }
+    with_lanes<L>(a.lanes_log2, [&](auto lanes) {
+      auto step = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if constexpr (D < decltype(lanes)::value) {
+          const double o1 = partner<D>(t1), o2 = partner<D>(t2);
+          const double low = o1 < t1 ? o1 : t1;  // the second best is this or one of the two seconds
+          t1 = o1 > t1 ? o1 : t1;
+          t2 = o2 > t2 ? o2 : t2;
+          t2 = low > t2 ? low : t2;
+        }
+      };
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
+      step(std::integral_constant<int, 4>{});
+      step(std::integral_constant<int, 8>{});
+      if constexpr (L == 64) {
+        step(std::integral_constant<int, 16>{});
+        step(std::integral_constant<int, 32>{});
+      }
+    });
+    double score = how.group_best == 2 ? t1 + t2 : t1;
+    score = score > -inf ? score : -inf;
+    // (the first 43 bits, as for the experts)
+    const uint64_t mine = key_of(score, 0) >> 9;
+    int ahead = 0;
+    for (int g = 0; g < how.groups; ++g) {
+      const int from = g << a.lanes_log2;
+      const uint64_t o = (uint64_t)(uint32_t)__shfl((int)(uint32_t)mine, from, L) |
+                         (uint64_t)(uint32_t)__shfl((int)(uint32_t)(mine >> 32), from, L) << 32;
+      ahead += o > mine || (o == mine && g < group) ? 1 : 0;
+    }
+    open = open && ahead < how.top_groups;
+  }
+
+  uint64_t key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = open && j < n ? key_of(c[j], e0 + j) : 0;
+  int chosen = 0;  // of lane r: expert r
+  for (int r = 0; r < how.k; ++r) {
+    uint64_t best = key[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) best = key[j] > best ? key[j] : best;
+    best = over_lanes<L>(best, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = key[j] == best ? 0 : key[j];
+    if (lane == r) chosen = 511 - (int)(best & 511);
+  }
+
+  const bool live = lane < how.k;
+  const double xc = live ? logit_at(xr + chosen) : -inf;
+  double w;
+  if (!softmax) {
+    w = live ? sigmoid64(xc) : 0.0;
+  } else if (how.renormalize) {  // (the chosen ones against their own largest: the quotients are the same)
+    const double m = over_lanes<L>(xc, [](double p, double q) { return p > q ? p : q; });
+    w = live ? exp64(xc - (m == -inf ? 0.0 : m)) : 0.0;
+  } else {
+    w = live ? exp64(xc - (top == -inf ? 0.0 : top)) * norm : 0.0;
+  }
+  if (how.renormalize) {
+    const double sum = over_lanes<L>(w, [](double p, double q) { return p + q; });
+    w = sum == 0.0 ? 0.0 : w / sum;
+  }
+  if (live) {
+    experts[token * how.k + lane] = chosen;
+    weights[token * how.k + lane] = (float)(how.scale * w);
+  }
+}
+
+// Gradient of the logits.  With d = scale dw of the chosen experts (zero for the others) and, where the weights are
+// normalized, d' = (d - sum d w) / sum s with w = s / sum s:
+//   softmax, normalized: dx = w (d - sum d w) of the chosen;   softmax: dx = s (d - sum d s), all experts;
+//   sigmoid: dx = d s (1 - s) of the chosen (d' for normalized weights).
+// 64 lanes a token; the row is gathered in LDS, so that it leaves whole, zeros and all.
+template <typename TIn>
+__global__ __launch_bounds__(256) void route_backward_kernel(const float* __restrict__ dw, const TIn* __restrict__ x, int64_t T,
+                                                             int64_t ldx, RouteHow how, const int32_t* __restrict__ experts,
+                                                             TIn* __restrict__ dx, int64_t lddx) {
+  __shared__ float rows[4][kMaxRouteExperts];
+  const int wid = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t token = (int64_t)blockIdx.x * 4 + wid;
+  if (token >= T) return;  // (no barrier follows: a wave reads its own row only)
+  float* row = rows[wid];
+  const TIn* xr = x + token * ldx;
+  const int E = how.experts, k = how.k;
+  const double inf = __builtin_inf();
+  const int e = lane < k ? experts[token * k + lane] : -1;
+  const bool live = e >= 0 && e < E;
+  const double xc = live ? logit_at(xr + e) : -inf;
+  double d = live ? how.scale * (double)dw[token * k + lane] : 0.0;
+  auto add = [](double p, double q) { return p + q; };
+  auto most = [](double p, double q) { return p > q ? p : q; };
+  double g;
+  if (how.score == 0 && !how.renormalize) {
+    double top = -inf;
+    for (int i = lane; i < E; i += 64) top = most(logit_at(xr + i), top);
+    top = over_lanes<64>(top, most);
+    top = top == -inf ? 0.0 : top;
+    double sum = 0.0;
+    for (int i = lane; i < E; i += 64) sum += exp64(logit_at(xr + i) - top);
+    sum = over_lanes<64>(sum, add);
+    const double norm = sum == 0.0 ? 0.0 : 1.0 / sum;
+    const double s = live ? exp64(xc - top) * norm : 0.0;
+    const double mean = over_lanes<64>(d * s, add);
+    for (int i = lane; i < E; i += 64) row[i] = (float)(-mean * exp64(logit_at(xr + i) - top) * norm);
+    g = s * (d - mean);
+  } else {
+    for (int i = lane; i < E; i += 64) row[i] = 0.0f;
+    if (how.score == 0) {
+      double m = over_lanes<64>(xc, most);
+      m = m == -inf ? 0.0 : m;
+      double w = live ? exp64(xc - m) : 0.0;
+      const double sum = over_lanes<64>(w, add);
+      w = sum == 0.0 ? 0.0 : w / sum;
+      g = w * (d - over_lanes<64>(d * w, add));
+    } else {
+      const double s = live ? sigmoid64(xc) : 0.0;
+      if (how.renormalize) {
+        const double sum = over_lanes<64>(s, add);
+        const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+        d = (d - over_lanes<64>(d * s, add) * inv) * inv;
+      }
+      g = d * s * (1.0 - s);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (live) row[e] = (float)g;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  TIn* out = dx + token * lddx;
+  for (int i = lane; i < E; i += 64) {
+    if constexpr (sizeof(TIn) == 2) out[i] = (TIn)pack_bf16x2(row[i], 0.0f);
+    else out[i] = row[i];
+  }
+}
+
+static int log2_up(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+template <typename TIn, int L, int V>
+static hipError_t launch_route_as(const void* x, int64_t T, int64_t ldx, const RouteArgs& a, const float* bias,
+                                  int32_t* experts, float* weights, hipStream_t st) {
+  const int64_t blocks = (T + 256 / L - 1) / (256 / L);
+  hipLaunchKernelGGL((route_kernel<TIn, L, V>), dim3((unsigned)blocks), dim3(256), 0, st, (const TIn*)x, T, ldx, a, bias,
+                     experts, weights);
+  return hipGetLastError();
+}
+
+template <typename TIn>
+static hipError_t launch_route_t(const void* x, int64_t T, int64_t ldx, const RouteHow& how, const float* bias,
+                                 int32_t* experts, float* weights, hipStream_t st) {
+  // 16 lanes a token once there are tokens enough to fill the card with them, and where the experts fit its slots.
+  const int glog = log2_up(how.groups), per = how.experts / how.groups;
+  const bool narrow = T > 2048 && how.k <= 16 && glog <= 4 && per <= 16 << (4 - glog);
+  RouteArgs a{how, (narrow ? 4 : 6) - glog, per, 0};
+  const int need = (per + (1 << a.lanes_log2) - 1) >> a.lanes_log2;
+  const int v = 1 << log2_up(need);
+  a.wide = per % v == 0 && ((uintptr_t)x & 15) == 0 && ldx * (int64_t)sizeof(TIn) % 16 == 0 && v * sizeof(TIn) >= 16;
+#define FP8BQ_ROUTE(L, V) \
+  case V: return launch_route_as<TIn, L, V>(x, T, ldx, a, bias, experts, weights, st);
+  if (narrow) {
+    switch (v) { FP8BQ_ROUTE(16, 1) FP8BQ_ROUTE(16, 2) FP8BQ_ROUTE(16, 4) FP8BQ_ROUTE(16, 8) FP8BQ_ROUTE(16, 16) }
+  } else {
+    switch (v) { FP8BQ_ROUTE(64, 1) FP8BQ_ROUTE(64, 2) FP8BQ_ROUTE(64, 4) FP8BQ_ROUTE(64, 8) FP8BQ_ROUTE(64, 16) }
+  }
+#undef FP8BQ_ROUTE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_route(const void* x, int xt, int64_t T, int64_t ldx, const RouteHow& how, const float* bias,
+                        int32_t* experts, float* weights, hipStream_t st) {
+  return xt == 0 ? launch_route_t<uint16_t>(x, T, ldx, how, bias, experts, weights, st)
+                 : launch_route_t<float>(x, T, ldx, how, bias, experts, weights, st);
+}
+
+hipError_t launch_route_backward(const float* dw, const void* x, int xt, int64_t T, int64_t ldx, const RouteHow& how,
+                                 const int32_t* experts, void* dx, int64_t lddx, hipStream_t st) {
+  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
+  if (xt == 0)
+    hipLaunchKernelGGL(route_backward_kernel<uint16_t>, grid, block, 0, st, dw, (const uint16_t*)x, T, ldx, how, experts,
+                       (uint16_t*)dx, lddx);
+  else
+    hipLaunchKernelGGL(route_backward_kernel<float>, grid, block, 0, st, dw, (const float*)x, T, ldx, how, experts,
+                       (float*)dx, lddx);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bq

@@ -661,4 +661,99 @@ int validate_int8_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx
   return check_space(m, ws, ws_bytes, ws_needed);
 }
 
+constexpr int64_t kMaxChoices = 64, kMaxExpertGroups = 64;
+
+// A matrix with any leading dimension and its elements' alignment.
+static int check_loose(const Mat& m) {
+  if (m.p == nullptr) return kErrNull;
+  if ((uintptr_t)m.p % (uintptr_t)m.esize != 0) return kErrAlign;
+  if (m.ld < m.cols) return kErrLd;
+  const int64_t most = kMaxExtentBytes / m.esize;
+  return m.ld > most || (m.rows > 1 && m.rows - 1 > (most - m.cols) / m.ld) ? kErrShape : kOk;
+}
+
+static int check_route(const RouteCheck& g, bool* empty) {
+  *empty = false;
+  if (in_esize(g.xt) == 0) return kErrDtype;
+  if (g.score != 0 && g.score != 1) return kErrValue;
+  if (!(g.scale - g.scale == 0.0)) return kErrValue;  // (NaN, infinities)
+  if (g.T < 0 || g.E < 1 || g.E > kMaxGroupExperts || g.k < 1 || g.k > kMaxChoices || g.k > g.E) return kErrShape;
+  if (g.T >= ((int64_t)1 << 31) / g.k) return kErrShape;
+  if (g.groups < 1 || g.groups > kMaxExpertGroups || g.E % g.groups != 0) return kErrShape;
+  const int64_t per = g.E / g.groups;
+  if (g.top_groups < 1 || g.top_groups > g.groups || g.k > g.top_groups * per) return kErrShape;
+  if (g.group_best < 1 || g.group_best > 2 || g.group_best > per) return kErrShape;
+  if (g.T == 0) *empty = true;
+  return kOk;
+}
+
+int validate_route(const RouteCheck& g, const void* bias, const void* experts, const void* weights, bool* empty) {
+  int st = check_route(g, empty);
+  if (st != kOk || *empty) return st;
+  if (experts == nullptr || weights == nullptr) return kErrNull;
+  const Mat x{g.x, g.T, g.E, g.ldx, in_esize(g.xt)};
+  if ((st = check_loose(x)) != kOk) return st;
+  if (!aligned4(bias) || !aligned4(experts) || !aligned4(weights)) return kErrAlign;
+  const Mat b{bias, bias ? 1 : 0, g.E, g.E, 4}, e{experts, 1, g.T * g.k, g.T * g.k, 4}, w{weights, 1, g.T * g.k, g.T * g.k, 4};
+  if (overlaps(e, x) || overlaps(w, x) || overlaps(e, b) || overlaps(w, b) || overlaps(e, w)) return kErrOverlap;
+  return kOk;
+}
+
+int validate_route_backward(const RouteCheck& g, const void* dweights, const void* experts, const void* dx, int64_t lddx,
+                            bool* empty) {
+  int st = check_route(g, empty);
+  if (st != kOk || *empty) return st;
+  if (dweights == nullptr || experts == nullptr) return kErrNull;
+  const Mat x{g.x, g.T, g.E, g.ldx, in_esize(g.xt)}, d{dx, g.T, g.E, lddx, in_esize(g.xt)};
+  if ((st = check_loose(x)) != kOk || (st = check_loose(d)) != kOk) return st;
+  if (!aligned4(dweights) || !aligned4(experts)) return kErrAlign;
+  const Mat e{experts, 1, g.T * g.k, g.T * g.k, 4}, w{dweights, 1, g.T * g.k, g.T * g.k, 4};
+  return overlaps(d, x) || overlaps(d, e) || overlaps(d, w) ? kErrOverlap : kOk;
+}
+
+int validate_expert_rows(const void* experts, int64_t n, int64_t E, const void* offsets, const void* rows, const void* slots,
+                         const void* ws, size_t ws_bytes, size_t ws_needed) {
+  if (n < 0 || n >= ((int64_t)1 << 31) || E < 1 || E > kMaxGroupExperts) return kErrShape;
+  if (offsets == nullptr || (n > 0 && (experts == nullptr || rows == nullptr || slots == nullptr))) return kErrNull;
+  if (!aligned8(offsets) || !aligned4(experts) || !aligned4(rows) || !aligned4(slots)) return kErrAlign;
+  const Mat m[4] = {{experts, n ? 1 : 0, n, n, 4}, {offsets, 1, E + 1, E + 1, 8}, {rows, n ? 1 : 0, n, n, 4},
+                    {slots, n ? 1 : 0, n, n, 4}};
+  for (int i = 1; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlaps(m[i], m[j])) return kErrOverlap;
+  return check_space(m, ws, ws_bytes, ws_needed);
+}
+
+int validate_rows(const RowsCheck& g, int inputs, int vectors, bool* empty) {
+  *empty = false;
+  if (in_esize(g.out_type) == 0) return kErrDtype;
+  for (int i = 0; i < inputs; ++i)
+    if (in_esize(g.type[i]) == 0) return kErrDtype;
+  if (g.T < 0 || g.H < 0 || g.H % 8 != 0 || g.k < 1 || g.k > kMaxChoices || g.T >= ((int64_t)1 << 31) / g.k) return kErrShape;
+  if (g.T == 0 || g.H == 0) {
+    *empty = true;
+    return kOk;
+  }
+  const int64_t n = g.T * g.k;
+  int st;
+  const Mat out{g.out, g.out_tall ? n : g.T, g.H, g.ldo, in_esize(g.out_type)};
+  Mat in[5];
+  int count = 0;
+  for (int i = 0; i < inputs; ++i) in[count++] = Mat{g.in[i], g.tall[i] ? n : g.T, g.H, g.ld[i], in_esize(g.type[i])};
+  for (int i = 0; i < inputs; ++i)
+    if ((st = check_mat(in[i], true)) != kOk) return st;
+  if ((st = check_mat(out, true)) != kOk) return st;
+  for (int i = 0; i < vectors; ++i) {
+    if (g.vec[i] == nullptr) return kErrNull;
+    if (!aligned4(g.vec[i])) return kErrAlign;
+    in[count++] = Mat{g.vec[i], 1, n, n, 4};
+  }
+  const Mat v{g.vec_out, g.vec_out ? 1 : 0, n, n, 4};
+  if (!aligned4(g.vec_out)) return kErrAlign;
+  if (overlaps(out, v)) return kErrOverlap;
+  for (int i = 0; i < count; ++i)
+    if (overlaps(out, in[i]) || overlaps(v, in[i])) return kErrOverlap;
+  return kOk;
+}
+
 }  // namespace fp8bq

@@ -145,4 +145,35 @@ int validate_int8_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx
                         int64_t ldq, const void* s, const void* ws, size_t ws_bytes, size_t ws_needed, bool* empty);
 int check_workspace(const MxArgs& g, const void* ws, size_t ws_bytes, size_t ws_needed);
 
+// Routing and the experts' rows (include/fp8bq_route.h).
+struct RouteCheck {
+  const void* x;
+  int xt;
+  int64_t T, E, ldx, k;
+  int score;
+  int64_t groups, top_groups, group_best;
+  double scale;
+};
+int validate_route(const RouteCheck& g, const void* bias, const void* experts, const void* weights, bool* empty);
+int validate_route_backward(const RouteCheck& g, const void* dweights, const void* experts, const void* dx, int64_t lddx,
+                            bool* empty);
+int validate_expert_rows(const void* experts, int64_t n, int64_t E, const void* offsets, const void* rows, const void* slots,
+                         const void* ws, size_t ws_bytes, size_t ws_needed);
+// Moves of rows: up to two input matrices of width H, tall ones with T k rows and the others with T, an output matrix,
+// up to three vectors of T k 4-byte entries, and a fourth that is written (may be null).
+struct RowsCheck {
+  int64_t T, k, H;
+  const void* in[2];
+  int type[2];
+  int64_t ld[2];
+  bool tall[2];
+  const void* out;
+  int out_type;
+  int64_t ldo;
+  bool out_tall;
+  const void* vec[3];
+  const void* vec_out;
+};
+int validate_rows(const RowsCheck& g, int inputs, int vectors, bool* empty);
+
 }  // namespace fp8bq
