@@ -44,7 +44,8 @@ Allocating helpers (outputs created with torch on the input's device):
         (accumulate=True: out, an FP32 main-grad buffer, receives out + dW)
 
 The layer grouped by expert is in ``grouped.py``, the layer in MXFP4 in ``mx.py``, the layer in 8-bit integers in
-``int8.py``, routing and the experts' rows in ``route.py``; their names are here too.
+``int8.py``, routing and the experts' rows in ``route.py`` and the orthogonalized update in
+``ortho.py``; their names are here too.
 """
 
 import ctypes
@@ -704,3 +705,7 @@ from .route import (MAX_CHOICES, SCORE_SIGMOID, SCORE_SOFTMAX, combine_rows, com
                     expert_rows, fp8bq_combine_rows, fp8bq_combine_rows_backward, fp8bq_expert_rows,
                     fp8bq_expert_rows_workspace_size, fp8bq_gather_rows, fp8bq_route_experts,
                     fp8bq_route_experts_backward, gather_rows, route_experts, route_experts_backward)
+
+# orthogonalization of updates (include/fp8bq_ortho.h)
+from .ortho import (MUON_COEFFICIENTS, fp8bq_orthogonalize, fp8bq_orthogonalize_workspace_size,  # noqa: E402,F401
+                    orthogonalize)

@@ -14,6 +14,7 @@ U8 = (torch.uint8,)
 I8 = (torch.int8,)
 I32 = (torch.int32,)
 F32 = (torch.float32,)
+BF16 = (torch.bfloat16,)
 I64 = (torch.int64,)
 HI = (torch.bfloat16, torch.float32)
 
@@ -103,6 +104,20 @@ def vector(t, name, n, dtypes, device):
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name}: expected a contiguous vector")
     return t.data_ptr()
+
+
+def batch(t, name, shape, dtypes, device):
+    """(address, matrices, rows, columns, leading dimension, distance of matrices) of a matrix or a batch of them."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.get_device() != device:
+        _refuse(t, name, shape, dtypes, device)
+    B, R, C = shape if len(shape) == 3 else (1, *shape)
+    if t.numel() == 0:
+        return t.data_ptr(), B, R, C, max(C, 1), max(R * C, 1)
+    st = t.stride()
+    if st[-1] != 1 and C > 1:
+        raise ValueError(f"{name}: expected matrices with unit column stride")
+    ld = st[-2] if R > 1 else C
+    return t.data_ptr(), B, R, C, ld, st[0] if B > 1 else (R - 1) * ld + C
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)

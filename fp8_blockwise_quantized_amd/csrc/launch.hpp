@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ortho_plan.hpp"
 #include "plan.hpp"
 
 namespace fp8bq {
@@ -184,6 +185,10 @@ hipError_t launch_combine_rows(const void* y, int yt, int64_t T, int64_t k, int6
 hipError_t launch_combine_rows_backward(const void* dout, int dt, int64_t lddo, const void* y, int yt, int64_t ldy, int64_t T,
                                         int64_t k, int64_t H, const int32_t* rows, const float* weights,
                                         const int32_t* slots, void* dy, int64_t lddy, float* dweights, hipStream_t st);
+
+// Newton-Schulz orthogonalization (include/fp8bq_ortho.h); coef: 3 steps values on the host; ws: p.ws bytes.
+hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, const OrthoPlan& p, int steps, const double* coef,
+                        double eps, void* out, int64_t ldo, int64_t obatch, void* ws, hipStream_t st);
 
 // Byte-matrix transpose: dst[c * ldd + r] = src[r * lds + c] for r < R, c < C (R, C multiples of 128).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t lds, uint8_t* dst, int64_t ldd, int64_t R, int64_t C,

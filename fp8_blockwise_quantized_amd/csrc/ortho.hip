@@ -1,0 +1,489 @@
+// Orthogonalization of an update by Newton-Schulz products, a batch of matrices [R, C] of one size.
+//
+// Mathematics.  With m = min(R, C), n = max(R, C) and X the m x n one of G and its transpose, X <- X / (|X|_F + eps), then
+// in every step A = X X^T, X <- a X + (b A + c A^2) X: each singular value s becomes a s + b s^3 + c s^5, and the singular
+// vectors stay.  Three products a step, A and A^2 symmetric: only their upper triangle of tiles is computed, and a tile
+// is written twice.
+//
+// Rounding.  The products run in 16-bit floats (11 bits) with FP32 accumulation.  Rounding X itself to 11 bits would put
+// noise of all directions into it, and the small singular values' directions are then amplified by a in every step: a
+// gradient of rank 32 in noise came out 2 10^-2 off.  So X is kept as the sum of two halves (22 bits) and the
+// update's product is taken with both.  A, A^2 and b A + c A^2 may be rounded to 11 bits, and X X^T be taken of the
+// first half: an error there is multiplied by X and so stays in X's own directions.  Off by (of the result's norm, five steps)
+// 4 10^-4 for matrices of low rank, 10^-3 for random ones; the result's own BF16 rounding is 1.7 10^-3.  In the last step
+// nothing amplifies any more and the product is taken with the first half alone; in the first, BF16 input fits one half.
+//
+// Scaling.  Halves hold 6 10^-8 .. 65504; X is held as 2^12 X, A and the polynomial as 2^10 A.  The first X is G times a
+// power of two (exact), the rest of the normalization (a factor in 1 .. 2) enters the first step's epilogues.
+//
+// Layout.  X (first half, rows along n) serves A's product, X^T (both halves, side by side, rows along m) the update's:
+// X^T_new = X^T (b A + c A^2) is a product of rows again.  The update writes both: a patch of accumulators is transposed
+// in registers, eight lanes exchanging 8 x 8 values, so that either goes out in 16-byte stores.  Rows are padded with
+// zeros to whole stages of 64 halves.
+//
+// Bound by the matrix pipes (row_gemm.hpp's loop) where the tiles fill the card; a lone matrix's A and A^2 have few tiles and
+// long contractions, which are split, the parts being added up by a second kernel with the same epilogue.
+#include <cmath>
+
+#include "launch.hpp"
+#include "ortho_plan.hpp"
+#include "quant_common.hpp"
+#include "row_gemm.hpp"
+
+namespace fp8bq {
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f;
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2h));
+}
+__device__ __forceinline__ void unpack_f16x2(uint32_t w, float& lo, float& hi) {
+  const v2h v = __builtin_bit_cast(v2h, w);
+  lo = (float)v.x;
+  hi = (float)v.y;
+}
+
+// 8 x 8 values of 16 bits held by eight neighbouring lanes, one row (four pairs) a lane, transposed: first within pairs
+// of lanes, then pairs of values between lanes 2 and 4 apart.
+__device__ __forceinline__ void transpose8(uint32_t (&d)[4], int lane) {
+  const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) d[k] = __builtin_amdgcn_perm(dpp_read<kDppXor1>(d[k]), d[k], sel);
+  const bool b1 = (lane & 2) != 0;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t got = dpp_read<kDppXor2>(b1 ? d[k] : d[k + 1]);
+    d[k] = b1 ? got : d[k];
+    d[k + 1] = b1 ? d[k + 1] : got;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t p = d[k], q = d[k + 2];
+    d[k + 2] = (uint32_t)__builtin_amdgcn_update_dpp((int)q, (int)p, 0x104, 0xF, 0x5, false);  // row_shl:4
+    d[k] = (uint32_t)__builtin_amdgcn_update_dpp((int)p, (int)q, 0x114, 0xF, 0xA, false);      // row_shr:4
+  }
+}
+
+// Sums of squares: parts[batch][block], in 64 bits (gradients may be as small as their squares are not in FP32).
+template <typename TIn>
+__global__ __launch_bounds__(256) void ortho_norm_kernel(const TIn* __restrict__ g, int64_t R, int64_t C, int64_t ldg,
+                                                         int64_t bstride, int wide, double* __restrict__ parts) {
+  __shared__ double red[4];
+  const TIn* gb = g + (int64_t)blockIdx.y * bstride;
+  double sum = 0.0;
+  if (wide) {
+    const int64_t chunks = C / 8, total = R * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      const int64_t r = i / chunks, c = i - r * chunks;
+      float v[8];
+      Load8<TIn>::run(gb + r * ldg + 8 * c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = __builtin_fma((double)v[k], (double)v[k], sum);
+    }
+  } else {
+    const int64_t total = R * C;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      const int64_t r = i / C, c = i - r * C;
+      double v;
+      if constexpr (sizeof(TIn) == 2) v = (double)bf16lo(gb[r * ldg + c]);
+      else v = (double)gb[r * ldg + c];
+      sum = __builtin_fma(v, v, sum);
+    }
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) parts[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// The first X in both layouts, from tiles of 64 x 64 of G; factor[batch].  tall: G is X^T.
+struct OrthoBuffers {
+  uint16_t* x;    // [batch][m][np] first halves
+  uint16_t* xt;   // [batch][n][2 mp] both halves
+  int64_t m, n, mp, np;
+};
+template <typename TIn>
+__global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict__ g, int64_t R, int64_t C, int64_t ldg,
+                                                          int64_t bstride, const double* __restrict__ parts, int nparts,
+                                                          double eps, OrthoBuffers b, int tall, float* __restrict__ factor) {
+  __shared__ uint16_t tile[64][66];
+  __shared__ uint16_t low[64][66];
+  const int t = threadIdx.x, batch = blockIdx.z;
+  double sum = 0.0;  // (every wave alike, in a fixed order)
+  for (int i = t & 63; i < nparts; i += 64) sum += parts[(int64_t)batch * nparts + i];
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+  const double norm = __builtin_sqrt(sum) + eps;
+  const bool finite = norm < __builtin_inf();
+  // norm = fr 2^ex, 1/2 <= fr < 1: X 2^12 = (G 2^(12 - ex)) / fr
+  const int ex = finite ? __builtin_amdgcn_frexp_exp(norm) : 0;
+  if (t == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+    factor[batch] = finite ? (float)(1.0 / __builtin_amdgcn_frexp_mant(norm)) : __builtin_nanf("");
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const TIn* gb = g + (int64_t)batch * bstride;
+  const int c = t & 63;
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const int r = (t >> 6) + 4 * k;
+    float v = 0.0f;
+    if (r0 + r < R && c0 + c < C) {
+      if constexpr (sizeof(TIn) == 2) v = bf16lo(gb[(r0 + r) * ldg + c0 + c]);
+      else v = gb[(r0 + r) * ldg + c0 + c];
+    }
+    v = __builtin_ldexpf(v, 12 - ex);
+    const _Float16 hi = (_Float16)v;
+    tile[r][c] = __builtin_bit_cast(uint16_t, hi);
+    if constexpr (sizeof(TIn) == 4) low[r][c] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)hi));
+  }
+  __syncthreads();
+  // (buffers are padded to whole tiles of 64 along their rows; rows past the matrix are not there)
+  uint16_t* x = b.x + (int64_t)batch * b.m * b.np;
+  uint16_t* xt = b.xt + (int64_t)batch * b.n * 2 * b.mp;
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const int i = (t >> 6) + 4 * k;  // row of the buffer's tile; c its column
+    const int64_t xr = tall ? c0 + i : r0 + i, xc = (tall ? r0 : c0) + c;
+    if (xr < b.m) x[xr * b.np + xc] = tall ? tile[c][i] : tile[i][c];
+    const int64_t tr = tall ? r0 + i : c0 + i, tc = (tall ? c0 : r0) + c;
+    if (tr < b.n) {
+      xt[tr * 2 * b.mp + tc] = tall ? tile[i][c] : tile[c][i];
+      if constexpr (sizeof(TIn) == 4) xt[tr * 2 * b.mp + b.mp + tc] = tall ? low[i][c] : low[c][i];
+    }
+  }
+}
+
+// What is done with a row of patches of a finished tile.
+enum OrthoStep : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2, kOrthoLast = 3, kOrthoLastWide = 4 };
+struct OrthoEnd {
+  float a, b, c;          // the step's coefficients
+  const float* factor;    // of the first step's X (null: 1)
+  uint16_t* sym;          // Gram, polynomial: output [batch][m][mp]
+  const uint16_t* gram;   // polynomial: A
+  const uint16_t* xt;     // update: X^T as it was, with `halves` halves
+  int halves;
+  uint16_t* xt_out;       // update: X^T and X
+  uint16_t* x_out;
+  uint16_t* out;          // last: BF16 result [batch], rows ldo apart
+  int64_t ldo, obatch;
+  int vec;                // 16-byte stores into it are possible
+  int64_t m, n, mp, np;
+};
+
+// Rows [0, rows) x columns [0, width) of 16-bit values: eight columns from col on, as far as they are there (all eight
+// where the buffer is padded: width a multiple of 64).
+__device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, bool vec, const uint32_t (&d)[4]) {
+  if (col >= width) return;
+  if (vec && col + 8 <= width) {
+    *reinterpret_cast<u32x4*>(row + col) = (u32x4){d[0], d[1], d[2], d[3]};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (col + k < width) row[col + k] = (uint16_t)(d[k >> 1] >> (16 * (k & 1)));
+  }
+}
+
+// STEP of one row of patches: v[j][8 q + i] is row m, column n + 32 j + 16 q + i of the product.
+template <int STEP, int NI>
+__device__ __forceinline__ void ortho_row(const OrthoEnd& e, const v16f (&v)[NI], const RowPlace& p, int64_t m) {
+  const float f = e.factor ? e.factor[p.batch] : 1.0f;
+  const int64_t turned = m - (p.lane & 7);         // first of the eight rows that come together, and the lane's
+  const int turn = p.lane & 7;                     // column among the eight after the turn
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t n = p.n + 32 * j + 16 * q;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = v[j][8 * q + i];
+      uint32_t d[4];
+      if constexpr (STEP == kOrthoGram || STEP == kOrthoPoly) {
+        const int64_t size = e.m * e.mp;
+        if constexpr (STEP == kOrthoGram) {
+          const float s = f * f * (kScaleA / (kScaleX * kScaleX));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= s;
+        } else {
+          u32x4 w = {0, 0, 0, 0};
+          if (m < p.mlim && n < e.mp) w = *reinterpret_cast<const u32x4*>(e.gram + p.batch * size + m * e.mp + n);
+          const float s = e.c * (1.0f / kScaleA);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            unpack_f16x2(w[i], lo, hi);
+            y[2 * i] = __builtin_fmaf(e.b, lo, s * y[2 * i]);
+            y[2 * i + 1] = __builtin_fmaf(e.b, hi, s * y[2 * i + 1]);
+          }
+        }
+        if (!p.whole) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
+        uint16_t* o = e.sym + p.batch * size;
+        if (m < p.mlim) put8(o + m * e.mp, n, e.mp, true, d);
+        if (p.mirror) {
+          transpose8(d, p.lane);
+          if (n + turn < p.nlim) put8(o + (n + turn) * e.mp, turned, e.mp, true, d);
+        }
+      } else {
+        u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+        if (m < p.mlim && n < e.mp) {
+          const uint16_t* o = e.xt + (p.batch * e.n + m) * 2 * e.mp + n;
+          hi = *reinterpret_cast<const u32x4*>(o);
+          if (e.halves == 2) lo = *reinterpret_cast<const u32x4*>(o + e.mp);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float h0, h1, l0, l1;
+          unpack_f16x2(hi[i], h0, h1);
+          unpack_f16x2(lo[i], l0, l1);
+          y[2 * i] = f * __builtin_fmaf(e.a, h0 + l0, y[2 * i] * (1.0f / kScaleA));
+          y[2 * i + 1] = f * __builtin_fmaf(e.a, h1 + l1, y[2 * i + 1] * (1.0f / kScaleA));
+        }
+        if (!p.whole) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
+        }
+        if constexpr (STEP == kOrthoUpdate) {
+          uint32_t l[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float h0, h1;
+            d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
+            unpack_f16x2(d[i], h0, h1);
+            l[i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
+          }
+          if (m < p.mlim) {
+            uint16_t* o = e.xt_out + (p.batch * e.n + m) * 2 * e.mp;
+            put8(o, n, e.mp, true, d);
+            put8(o + e.mp, n, e.mp, true, l);
+          }
+          transpose8(d, p.lane);
+          if (n + turn < p.nlim) put8(e.x_out + (p.batch * e.m + n + turn) * e.np, turned, e.np, true, d);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(y[2 * i] * (1.0f / kScaleX), y[2 * i + 1] * (1.0f / kScaleX));
+          uint16_t* o = e.out + p.batch * e.obatch;
+          if constexpr (STEP == kOrthoLast) {
+            if (m < p.mlim) put8(o + m * e.ldo, n, e.m, e.vec != 0, d);
+          } else {
+            transpose8(d, p.lane);
+            if (n + turn < p.nlim) put8(o + (n + turn) * e.ldo, turned, e.n, e.vec != 0, d);
+          }
+        }
+      }
+    }
+}
+
+template <int STEP>
+constexpr int ortho_units() { return STEP == kOrthoGram || STEP == kOrthoPoly ? kUnitsTriangle : kUnitsFull; }
+
+template <int BM, int BN, int WGM, int WGN, int STEP>
+__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWaves)) void ortho_gemm_kernel(
+    RowDesc d, OrthoEnd e, uint32_t tiles_m, uint32_t tiles_n, int batches) {
+  using Tile = RowTile<BM, BN, WGM * WGN>;
+  constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kRing];
+  auto end = [&](const v16f (&acc)[MI][NI], const RowPlace& p) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      ortho_row<STEP, NI>(e, acc[i], p, p.m + 32 * i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  row_gemm_units<kRowsF16, BM, BN, WGM, WGN, ortho_units<STEP>()>(d, tiles_m, tiles_n, 1, batches, nullptr, smem, end);
+}
+
+// Split contractions: a part's sums as the lanes hold them, parts[part][batch][tile][wave][patch][quarter][lane] of four
+// floats; and the kernel that adds them up, one row of a wave's patches to a wave.
+template <int BM, int BN, int WGM, int WGN>
+__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWaves)) void ortho_part_kernel(
+    RowDesc d, v4f* __restrict__ parts, uint32_t tiles, int nsplit, int batches) {
+  using Tile = RowTile<BM, BN, WGM * WGN>;
+  constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kRing];
+  const int64_t T = (int64_t)tiles * (tiles + 1) / 2;
+  auto end = [&](const v16f (&acc)[MI][NI], const RowPlace& p) {
+    v4f* o = parts + (((int64_t)p.split * batches + p.batch) * T + p.tile) * (BM * BN / 4) + p.wave * (MI * NI * 4 * 64) + p.lane;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          o[((i * NI + j) * 4 + r) * 64] = (v4f){acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+  };
+  row_gemm_units<kRowsF16, BM, BN, WGM, WGN, kUnitsTriangle>(d, tiles, tiles, nsplit, batches, nullptr, smem, end);
+}
+template <int BM, int BN, int WGM, int WGN, int STEP>
+__global__ __launch_bounds__(256) void ortho_sum_kernel(OrthoEnd e, const v4f* __restrict__ parts, uint32_t tiles, int nsplit,
+                                                        int batches) {
+  constexpr int NW = WGM * WGN, MI = BM / WGM / 32, NI = BN / WGN / 32;
+  const uint32_t T = tiles * (tiles + 1) / 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (unit >= (int64_t)T * batches * (NW * MI)) return;
+  const int i = (int)(unit % MI), wave = (int)(unit / MI % NW);
+  const int64_t bt = unit / (MI * NW);
+  const uint32_t w = (uint32_t)(bt % T);
+  v16f v[1][NI];
+  const v4f* at = parts + bt * (BM * BN / 4) + ((wave * MI + i) * NI) * (4 * 64) + lane;
+  const int64_t step = (int64_t)T * batches * (BM * BN / 4);
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      v4f s = at[(j * 4 + r) * 64];
+      for (int k = 1; k < nsplit; ++k) s += at[k * step + (j * 4 + r) * 64];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[0][j][4 * r + x] = s[x];
+    }
+  uint32_t tm, tn;
+  row_tile<kUnitsTriangle>(w, tiles, tiles, tm, tn);
+  RowPlace p;
+  p.m0 = (int64_t)tm * BM;
+  p.n0 = (int64_t)tn * BN;
+  p.mlim = p.nlim = e.m;
+  p.m = p.m0 + wave / WGN * (BM / WGM) + (lane & 31);
+  p.n = p.n0 + wave % WGN * (BN / WGN) + 8 * (lane >> 5);
+  p.ccol = 0;
+  p.split = 0;
+  p.batch = (int)(bt / T);
+  p.lane = lane;
+  p.tile = w;
+  p.wave = wave;
+  p.whole = p.m0 + BM <= p.mlim && p.n0 + BN <= p.nlim;
+  p.mirror = tm != tn;
+  ortho_row<STEP, NI>(e, v[0], p, p.m + 32 * i);
+}
+
+template <int BM, int BN, int WGM, int WGN, int STEP>
+static hipError_t launch_product_tile(const RowDesc& d, const OrthoEnd& e, const OrthoProduct& p, int batches, void* parts,
+                                      hipStream_t st) {
+  const dim3 block(WGM * WGN * 64);
+  if constexpr (ortho_units<STEP>() == kUnitsTriangle) {
+    if (p.split > 1) {
+      hipLaunchKernelGGL((ortho_part_kernel<BM, BN, WGM, WGN>), dim3((unsigned)p.grid), block, 0, st, d, (v4f*)parts,
+                         (uint32_t)p.tiles_m, p.split, batches);
+      const hipError_t r = hipGetLastError();
+      if (r != hipSuccess) return r;
+      const int64_t units = p.tiles * batches * (WGM * WGN * (BM / WGM / 32));
+      hipLaunchKernelGGL((ortho_sum_kernel<BM, BN, WGM, WGN, STEP>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, st, e,
+                         (const v4f*)parts, (uint32_t)p.tiles_m, p.split, batches);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((ortho_gemm_kernel<BM, BN, WGM, WGN, STEP>), dim3((unsigned)p.grid), block, 0, st, d, e,
+                     (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, batches);
+  return hipGetLastError();
+}
+template <int STEP>
+static hipError_t launch_product(const RowDesc& d, const OrthoEnd& e, const OrthoProduct& p, int batches, void* parts,
+                                 hipStream_t st) {
+  switch (p.shape) {
+    case k256x256: return launch_product_tile<256, 256, 2, 4, STEP>(d, e, p, batches, parts, st);
+    case k64x64: return launch_product_tile<64, 64, 2, 2, STEP>(d, e, p, batches, parts, st);
+    default: return launch_product_tile<128, 128, 2, 2, STEP>(d, e, p, batches, parts, st);
+  }
+}
+
+#define FP8BQ_TRY(call)                      \
+  do {                                       \
+    const hipError_t err = (call);           \
+    if (err != hipSuccess) return err;       \
+  } while (0)
+
+hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, const OrthoPlan& p, int steps, const double* coef,
+                        double eps, void* out, int64_t ldo, int64_t obatch, void* ws, hipStream_t st) {
+  const bool tall = p.R >= p.C;
+  uint8_t* w = (uint8_t*)ws;
+  double* norms = (double*)(w + p.at_norms);
+  float* factor = (float*)(w + p.at_factor);
+  uint16_t* x = (uint16_t*)(w + p.at_x);
+  uint16_t* xt[2] = {(uint16_t*)(w + p.at_xt[0]), (uint16_t*)(w + p.at_xt[1])};
+  uint16_t* gram = (uint16_t*)(w + p.at_gram);
+  uint16_t* poly = (uint16_t*)(w + p.at_poly);
+  void* parts = w + p.at_parts;
+  const int es = gt == 0 ? 2 : 4, B = (int)p.batch;
+  const int wide = p.C % 8 == 0 && ((uintptr_t)g & 15) == 0 && ldg * es % 16 == 0 && (gbatch * es % 16 == 0 || B == 1);
+
+  const dim3 ngrid((unsigned)p.norm_blocks, (unsigned)B);
+  const dim3 bgrid((unsigned)((p.C + 63) / 64), (unsigned)((p.R + 63) / 64), (unsigned)B);
+  const OrthoBuffers b{x, xt[0], p.m, p.n, p.mp, p.np};
+  if (gt == 0) {
+    hipLaunchKernelGGL(ortho_norm_kernel<uint16_t>, ngrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, wide, norms);
+    FP8BQ_TRY(hipGetLastError());
+    hipLaunchKernelGGL(ortho_begin_kernel<uint16_t>, bgrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, norms,
+                       p.norm_blocks, eps, b, (int)tall, factor);
+  } else {
+    hipLaunchKernelGGL(ortho_norm_kernel<float>, ngrid, dim3(256), 0, st, (const float*)g, p.R, p.C, ldg, gbatch, wide, norms);
+    FP8BQ_TRY(hipGetLastError());
+    hipLaunchKernelGGL(ortho_begin_kernel<float>, bgrid, dim3(256), 0, st, (const float*)g, p.R, p.C, ldg, gbatch, norms,
+                       p.norm_blocks, eps, b, (int)tall, factor);
+  }
+  FP8BQ_TRY(hipGetLastError());
+
+  for (int k = 0; k < steps; ++k) {
+    const bool first = k == 0, last = k == steps - 1;
+    OrthoEnd e{};
+    e.a = (float)coef[3 * k];
+    e.b = (float)coef[3 * k + 1];
+    e.c = (float)coef[3 * k + 2];
+    e.factor = first ? factor : nullptr;
+    e.gram = gram;
+    e.xt = xt[k & 1];
+    e.halves = first && gt == 0 ? 1 : 2;
+    e.xt_out = xt[(k & 1) ^ 1];
+    e.x_out = x;
+    e.out = (uint16_t*)out;
+    e.ldo = ldo;
+    e.obatch = obatch;
+    e.vec = ((uintptr_t)out & 15) == 0 && ldo % 8 == 0 && (obatch % 8 == 0 || B == 1);
+    e.m = p.m;
+    e.n = p.n;
+    e.mp = p.mp;
+    e.np = p.np;
+    RowDesc d{};
+    d.a = d.b = (const uint8_t*)x;  // A = X X^T
+    d.lda = d.ldb = 2 * p.np;
+    d.M = d.N = p.m;
+    d.K = 2 * p.np;
+    d.abatch = d.bbatch = 2 * p.m * p.np;
+    e.sym = gram;
+    FP8BQ_TRY(launch_product<kOrthoGram>(d, e, p.gram, B, parts, st));
+    e.factor = nullptr;
+    d.a = d.b = (const uint8_t*)gram;  // b A + c A A
+    d.lda = d.ldb = 2 * p.mp;
+    d.K = 2 * p.mp;
+    d.abatch = d.bbatch = 2 * p.m * p.mp;
+    e.sym = poly;
+    FP8BQ_TRY(launch_product<kOrthoPoly>(d, e, p.poly, B, parts, st));
+    e.factor = first ? factor : nullptr;
+    const int halves = last ? 1 : e.halves;
+    d.a = (const uint8_t*)xt[k & 1];
+    d.lda = 4 * p.mp;
+    d.b = (const uint8_t*)poly;
+    d.ldb = 2 * p.mp;
+    d.M = p.n;
+    d.N = p.m;
+    d.K = 2 * p.mp * halves;
+    d.wrap = halves == 2 ? (int)(2 * p.mp / 128) : 0;
+    d.abatch = 4 * p.n * p.mp;
+    d.bbatch = 2 * p.m * p.mp;
+    if (!last)
+      FP8BQ_TRY(launch_product<kOrthoUpdate>(d, e, p.update, B, nullptr, st));
+    else if (tall)
+      FP8BQ_TRY(launch_product<kOrthoLast>(d, e, p.update, B, nullptr, st));
+    else
+      FP8BQ_TRY(launch_product<kOrthoLastWide>(d, e, p.update, B, nullptr, st));
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp8bq

@@ -51,6 +51,7 @@ enum RowUnits : int { kUnitsFull = 0, kUnitsTriangle = 1, kUnitsGrouped = 2 };
 
 struct RowUnit : GroupUnit {
   int batch;
+  uint32_t tile;  // number of the tile among its matrix's
 };
 
 // Tile (i, j), i <= j, number w of the upper triangle of t x t tiles, columns of tiles one after the other:
@@ -86,9 +87,26 @@ struct RowPlace {
   int64_t m, n;          // the lane's first row and column
   int64_t ccol;          // output column = column + ccol
   int split, batch, lane;
+  uint32_t tile;
+  int wave;
   bool whole;            // the whole tile exists
   bool mirror;           // (triangle) the tile's transpose is another tile of the result
 };
+
+// Tile number w of a matrix: its row and column of tiles.
+template <int UNITS>
+__device__ __forceinline__ void row_tile(uint32_t w, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+  if constexpr (UNITS == kUnitsTriangle) {
+    triangle_tile(w, tm, tn);
+  } else {
+    const uint32_t group = (uint32_t)kGroupRows * tiles_n;
+    const uint32_t gid = w / group, first = gid * kGroupRows;
+    const uint32_t gsz = (tiles_m - first) < (uint32_t)kGroupRows ? (tiles_m - first) : (uint32_t)kGroupRows;
+    const uint32_t rem = w - gid * group;
+    tm = first + rem % gsz;
+    tn = rem / gsz;
+  }
+}
 
 // smem: ring (and group table).  END: end(acc, place) takes a finished tile.
 template <int KIND, int BM, int BN, int WGM, int WGN, int UNITS, typename END>
@@ -128,6 +146,7 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
           group_unit_of<kGroupRowsMode, BM, BN>(u, gunits, gstarts, grp->experts, (int)d.M, (int)d.N, nkb, lane);
       r.batch = 0;
       r.split = 0;
+      r.tile = 0;
     } else {
       // (opaque here, so that what the divisions by them need is not worked out once and held over the loop)
       uint32_t tiles = T, cols = tiles_n, parts = (uint32_t)nsplit;
@@ -135,16 +154,8 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
       const uint32_t L = xcd_contiguous(u, U);
       const uint32_t z = L / tiles, w = L - z * tiles;
       uint32_t tm, tn;
-      if constexpr (UNITS == kUnitsTriangle) {
-        triangle_tile(w, tm, tn);
-      } else {
-        const uint32_t group = (uint32_t)kGroupRows * cols;
-        const uint32_t gid = w / group, first = gid * kGroupRows;
-        const uint32_t gsz = (tiles_m - first) < (uint32_t)kGroupRows ? (tiles_m - first) : (uint32_t)kGroupRows;
-        const uint32_t rem = w - gid * group;
-        tm = first + rem % gsz;
-        tn = rem / gsz;
-      }
+      row_tile<UNITS>(w, tiles_m, cols, tm, tn);
+      r.tile = (uint32_t)__builtin_amdgcn_readfirstlane((int)w);
       const int ns = (int)parts;
       r.batch = __builtin_amdgcn_readfirstlane((int)(z / parts));
       r.split = (int)z - r.batch * ns;
@@ -324,6 +335,8 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
     p.split = C.split;
     p.batch = C.batch;
     p.lane = el;
+    p.tile = C.tile;
+    p.wave = wid;
     p.whole = (int64_t)C.m0 + BM <= p.mlim && (int64_t)C.n0 + BN <= p.nlim;
     p.mirror = UNITS == kUnitsTriangle && C.m0 != C.n0;
     end(acc, p);

@@ -1,6 +1,8 @@
 // Argument validation (pure host C++).
 #include "validate.hpp"
 
+#include "ortho_plan.hpp"
+
 namespace fp8bq {
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -754,6 +756,41 @@ int validate_rows(const RowsCheck& g, int inputs, int vectors, bool* empty) {
   for (int i = 0; i < count; ++i)
     if (overlaps(out, in[i]) || overlaps(v, in[i])) return kErrOverlap;
   return kOk;
+}
+
+// A batch of matrices as one whose rows are the matrices.
+static Mat batch_mat(const void* p, int64_t B, int64_t R, int64_t C, int64_t ld, int64_t stride, int esize) {
+  const int64_t span = (R - 1) * ld + C;
+  return Mat{p, B, span, B > 1 ? stride : span, esize};
+}
+
+int validate_ortho(const OrthoCheck& c, bool* empty) {
+  *empty = false;
+  if (in_esize(c.gt) == 0) return kErrDtype;
+  if (c.B < 0 || c.R < 0 || c.C < 0 || c.B > kMaxOrthoBatch || c.R > kMaxOrthoSide || c.C > kMaxOrthoSide) return kErrShape;
+  if (c.steps < 1 || c.steps > 64 || !(c.eps > 0.0) || !(c.eps - c.eps == 0.0)) return kErrValue;
+  if (c.coef == nullptr) return kErrNull;
+  for (int i = 0; i < 3 * c.steps; ++i)
+    if (!(c.coef[i] - c.coef[i] == 0.0)) return kErrValue;
+  if (c.B == 0 || c.R == 0 || c.C == 0) {
+    *empty = true;
+    return kOk;
+  }
+  const int64_t most = kMaxExtentBytes / 4;
+  if (c.g == nullptr || c.out == nullptr) return kErrNull;
+  if (c.ldg < c.C || c.ldo < c.C) return kErrLd;
+  if (c.ldg > most / c.R || c.ldo > most / c.R) return kErrShape;
+  const Mat g = batch_mat(c.g, c.B, c.R, c.C, c.ldg, c.gstride, in_esize(c.gt));
+  const Mat o = batch_mat(c.out, c.B, c.R, c.C, c.ldo, c.ostride, 2);
+  int st;
+  if ((st = check_loose(g)) != kOk || (st = check_loose(o)) != kOk) return st;
+  return overlaps(g, o) ? kErrOverlap : kOk;
+}
+
+int check_ortho_workspace(const OrthoCheck& c, const void* ws, size_t ws_bytes, size_t ws_needed) {
+  const Mat m[2] = {batch_mat(c.g, c.B, c.R, c.C, c.ldg, c.gstride, in_esize(c.gt)),
+                    batch_mat(c.out, c.B, c.R, c.C, c.ldo, c.ostride, 2)};
+  return check_space(m, ws, ws_bytes, ws_needed);
 }
 
 }  // namespace fp8bq

@@ -176,4 +176,18 @@ struct RowsCheck {
 };
 int validate_rows(const RowsCheck& g, int inputs, int vectors, bool* empty);
 
+// Orthogonalization (include/fp8bq_ortho.h); the output is BF16.
+struct OrthoCheck {
+  const void* g;
+  int gt;
+  int64_t B, R, C, ldg, gstride;
+  int steps;
+  const double* coef;
+  double eps;
+  const void* out;
+  int64_t ldo, ostride;
+};
+int validate_ortho(const OrthoCheck& c, bool* empty);
+int check_ortho_workspace(const OrthoCheck& c, const void* ws, size_t ws_bytes, size_t ws_needed);
+
 }  // namespace fp8bq
