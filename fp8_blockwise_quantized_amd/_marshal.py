@@ -97,13 +97,18 @@ def space(ws, device):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def flat(t, name, shape, dtypes, device):
+    """Address of a contiguous tensor of the given shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.get_device() != device:
+        _refuse(t, name, shape, dtypes, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def vector(t, name, n, dtypes, device):
     """Address of a contiguous vector of n elements."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != (n,) or t.get_device() != device:
-        _refuse(t, name, (n,), dtypes, device)
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name}: expected a contiguous vector")
-    return t.data_ptr()
+    return flat(t, name, (n,), dtypes, device)
 
 
 def batch(t, name, shape, dtypes, device):

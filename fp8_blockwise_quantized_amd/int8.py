@@ -177,7 +177,7 @@ def quantize_int8(x):
 def quantize_int8_t(x):
     R, C = x.shape
     qt, st = x.new_empty((C, _padded(R)), dtype=torch.int8), x.new_empty(C, dtype=torch.float32)
-    fp8bq_quantize_int8_t(x, qt, st, _space("fp8bq_quantize_int8_t_workspace_size", x, R, C))
+    fp8bq_quantize_int8_t.__wrapped__(x, qt, st, _space("fp8bq_quantize_int8_t_workspace_size", x, R, C))
     return qt, st
 
 
@@ -191,7 +191,7 @@ def gemm_int8(qa, sa, qb, sb, out_dtype=torch.bfloat16, out=None, ws=None, accum
     c = _output(out, M, N, out_dtype, qa)
     if ws is None:
         ws = _space("fp8bq_gemm_int8_workspace_size", qa, M, N, K)
-    fp8bq_gemm_int8(qa, sa, qb, sb, c, ws, accumulate=accumulate)
+    fp8bq_gemm_int8.__wrapped__(qa, sa, qb, sb, c, ws, accumulate=accumulate)
     return c
 
 
@@ -202,7 +202,7 @@ def linear_int8(x, qw, sw, out_dtype=torch.bfloat16, out=None, ws=None):
     y = _output(out, M, N, out_dtype, x)
     if ws is None:
         ws = _space("fp8bq_linear_int8_workspace_size", x, M, N, K)
-    fp8bq_linear_int8(x, qw, sw, y, ws)
+    fp8bq_linear_int8.__wrapped__(x, qw, sw, y, ws)
     return y
 
 
@@ -214,7 +214,7 @@ def grouped_gemm_int8(qa, sa, offsets, qw, sw, out_dtype=torch.bfloat16, out=Non
     y = _output(out, T, N, out_dtype, qa)
     if ws is None:
         ws = _space("fp8bq_grouped_gemm_int8_workspace_size", qa, E, T, N, K)
-    fp8bq_grouped_gemm_int8(qa, sa, offsets, qw, sw, y, ws)
+    fp8bq_grouped_gemm_int8.__wrapped__(qa, sa, offsets, qw, sw, y, ws)
     return y
 
 
@@ -226,5 +226,5 @@ def grouped_linear_int8(x, offsets, qw, sw, out_dtype=torch.bfloat16, out=None, 
     y = _output(out, T, N, out_dtype, x)
     if ws is None:
         ws = _space("fp8bq_grouped_linear_int8_workspace_size", x, E, T, N, K)
-    fp8bq_grouped_linear_int8(x, offsets, qw, sw, y, ws)
+    fp8bq_grouped_linear_int8.__wrapped__(x, offsets, qw, sw, y, ws)
     return y

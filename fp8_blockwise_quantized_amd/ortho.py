@@ -69,5 +69,5 @@ def orthogonalize(g, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None
     if ws is None:
         B, R, C = g.shape if g.dim() == 3 else (1, *g.shape)
         ws = _space("fp8bq_orthogonalize_workspace_size", g, B, R, C)
-    fp8bq_orthogonalize(g, coefficients, eps, out, ws)
+    fp8bq_orthogonalize.__wrapped__(g, coefficients, eps, out, ws)
     return out

@@ -30,8 +30,9 @@ import ctypes
 
 import torch
 
-from . import IN_BF16, IN_F32, OUT_BF16, OUT_F32, _RESTYPES, _SIGS, _c_i64, _c_int, _c_sz, _c_vp, _entry, lib
-from ._marshal import F32, HI, I32, I64, matrix, on_its_device, space, stream, vector
+from . import (Fp8bqError, IN_BF16, IN_F32, OUT_BF16, OUT_F32, _RESTYPES, _SIGS, _c_i64, _c_int, _c_sz, _c_vp, _entry,
+               lib)
+from ._marshal import F32, HI, I32, I64, flat, matrix, on_its_device, space, stream, vector
 from .mx import _space
 
 MAX_CHOICES = 64
@@ -61,58 +62,86 @@ def _in(t):
     return IN_BF16 if t.dtype == torch.bfloat16 else IN_F32
 
 
-def _choices(t, name, T, dtypes, dev):
-    """Address and k of a contiguous [T, k] tensor."""
+def _k_of(t, name):
+    """k of a [T, k] tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 2 or t.shape[0] != T:
-        raise ValueError(f"{name} must have shape [{T}, k], not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return vector(t.view(-1), name, t.numel(), dtypes, dev), t.shape[1]
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have shape [T, k], not {tuple(t.shape)}")
+    return t.shape[1]
 
 
-def _same(t, name, T, k, dtypes, dev):
-    p, n = _choices(t, name, T, dtypes, dev)
-    if n != k:
-        raise ValueError(f"{name} must have shape [{T}, {k}], not {tuple(t.shape)}")
-    return p
+def _call(name, *args):
+    status = getattr(lib(), name)(*args)
+    if status != 0:
+        raise Fp8bqError(status, name)
+
+
+# (what an entry point needs beside its outputs' addresses, so that the helpers need not check what they have made)
+def _route(logits, k, score, bias, groups, top_groups, group_best, renormalize, scale, dev):
+    T, E = logits.shape
+    xp, ldx = matrix(logits, "logits", (T, E), HI, dev)
+    bp = vector(bias, "bias", E, F32, dev) if bias is not None else 0
+    return xp, _in(logits), T, E, ldx, k, score, bp, groups, top_groups, group_best, 1 if renormalize else 0, float(scale)
+
+
+def _route_backward(dweights, logits, score, renormalize, scale, experts, dev):
+    T, E = logits.shape
+    k = _k_of(experts, "experts")
+    dwp = flat(dweights, "dweights", (T, k), F32, dev)
+    xp, ldx = matrix(logits, "logits", (T, E), HI, dev)
+    ep = flat(experts, "experts", (T, k), I32, dev)
+    return dwp, xp, _in(logits), T, E, ldx, k, score, 1 if renormalize else 0, float(scale), ep
+
+
+def _gather(x, slots, k, dev):
+    T, H = x.shape
+    xp, ldx = matrix(x, "x", (T, H), HI, dev)
+    return xp, _in(x), T, H, ldx, vector(slots, "slots", T * k, I32, dev), k
+
+
+def _combine(y, rows, weights, dev):
+    k = _k_of(rows, "rows")
+    T, H = rows.shape[0], y.shape[1]
+    yp, ldy = matrix(y, "y", (T * k, H), HI, dev)
+    rp = flat(rows, "rows", (T, k), I32, dev)
+    return yp, _in(y), T, k, H, ldy, rp, flat(weights, "weights", (T, k), F32, dev) if weights is not None else 0
+
+
+def _combine_backward(dout, y, rows, weights, slots, dev):
+    T, H = dout.shape
+    k = _k_of(rows, "rows")
+    dp, lddo = matrix(dout, "dout", (T, H), HI, dev)
+    yp, ldy = matrix(y, "y", (T * k, H), HI, dev)
+    rp, wp = flat(rows, "rows", (T, k), I32, dev), flat(weights, "weights", (T, k), F32, dev)
+    return dp, _in(dout), lddo, yp, _in(y), ldy, T, k, H, rp, wp, vector(slots, "slots", T * k, I32, dev)
 
 
 @on_its_device
 @_entry
 def fp8bq_route_experts(logits, k, score, bias, groups, top_groups, group_best, renormalize, scale, experts, weights):
-    T, E = logits.shape
     dev = logits.get_device()
-    xp, ldx = matrix(logits, "logits", (T, E), HI, dev)
-    bp = vector(bias, "bias", E, F32, dev) if bias is not None else 0
-    ep, wp = _same(experts, "experts", T, k, I32, dev), _same(weights, "weights", T, k, F32, dev)
-    return (xp, _in(logits), T, E, ldx, k, score, bp, groups, top_groups, group_best, int(bool(renormalize)), float(scale),
-            ep, wp, stream(dev))
+    args = _route(logits, k, score, bias, groups, top_groups, group_best, renormalize, scale, dev)
+    shape = (logits.shape[0], k)
+    return (*args, flat(experts, "experts", shape, I32, dev), flat(weights, "weights", shape, F32, dev), stream(dev))
 
 
 @on_its_device
 @_entry
 def fp8bq_route_experts_backward(dweights, logits, score, renormalize, scale, experts, dlogits):
-    T, E = logits.shape
-    dev = dweights.get_device()
-    dwp, k = _choices(dweights, "dweights", T, F32, dev)
-    xp, ldx = matrix(logits, "logits", (T, E), HI, dev)
-    ep = _same(experts, "experts", T, k, I32, dev)
-    dp, ldd = matrix(dlogits, "dlogits", (T, E), (logits.dtype,), dev)
-    return dwp, xp, _in(logits), T, E, ldx, k, score, int(bool(renormalize)), float(scale), ep, dp, ldd, stream(dev)
+    dev = logits.get_device()
+    args = _route_backward(dweights, logits, score, renormalize, scale, experts, dev)
+    dp, ldd = matrix(dlogits, "dlogits", logits.shape, (logits.dtype,), dev)
+    return (*args, dp, ldd, stream(dev))
 
 
 @on_its_device
 @_entry
 def fp8bq_expert_rows(experts, E, offsets, rows, slots, ws=None):
     dev = experts.get_device()
-    ep, k = _choices(experts, "experts", experts.shape[0], I32, dev)
-    n = experts.numel()
-    if not isinstance(offsets, torch.Tensor):
-        raise TypeError("offsets must be a torch tensor")
-    op = vector(offsets, "offsets", E + 1, I64, dev)
-    rp = _same(rows, "rows", experts.shape[0], k, I32, dev)
+    shape, n = (experts.shape[0], _k_of(experts, "experts")), experts.numel()
+    ep = flat(experts, "experts", shape, I32, dev)
+    op, rp = vector(offsets, "offsets", E + 1, I64, dev), flat(rows, "rows", shape, I32, dev)
     sp = vector(slots, "slots", n, I32, dev)
     wsp, wsb = space(ws, dev)
     return ep, n, E, op, rp, sp, wsp, wsb, stream(dev)
@@ -121,40 +150,28 @@ def fp8bq_expert_rows(experts, E, offsets, rows, slots, ws=None):
 @on_its_device
 @_entry
 def fp8bq_gather_rows(x, slots, k, out):
-    T, H = x.shape
     dev = x.get_device()
-    xp, ldx = matrix(x, "x", (T, H), HI, dev)
-    sp = vector(slots, "slots", T * k, I32, dev)
-    op, ldo = matrix(out, "out", (T * k, H), (x.dtype,), dev)
-    return xp, _in(x), T, H, ldx, sp, k, op, ldo, stream(dev)
+    args = _gather(x, slots, k, dev)
+    op, ldo = matrix(out, "out", (x.shape[0] * k, x.shape[1]), (x.dtype,), dev)
+    return (*args, op, ldo, stream(dev))
 
 
 @on_its_device
 @_entry
 def fp8bq_combine_rows(y, rows, weights, out):
-    T = rows.shape[0]
     dev = y.get_device()
-    rp, k = _choices(rows, "rows", T, I32, dev)
-    H = y.shape[1]
-    yp, ldy = matrix(y, "y", (T * k, H), HI, dev)
-    wp = _same(weights, "weights", T, k, F32, dev) if weights is not None else 0
-    op, ldo = matrix(out, "out", (T, H), HI, dev)
-    return (yp, _in(y), T, k, H, ldy, rp, wp, op, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, ldo, stream(dev))
+    args = _combine(y, rows, weights, dev)
+    op, ldo = matrix(out, "out", (rows.shape[0], y.shape[1]), HI, dev)
+    return (*args, op, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, ldo, stream(dev))
 
 
 @on_its_device
 @_entry
 def fp8bq_combine_rows_backward(dout, y, rows, weights, slots, dy, dweights):
-    T, H = dout.shape
     dev = dout.get_device()
-    dp, lddo = matrix(dout, "dout", (T, H), HI, dev)
-    rp, k = _choices(rows, "rows", T, I32, dev)
-    yp, ldy = matrix(y, "y", (T * k, H), HI, dev)
-    wp = _same(weights, "weights", T, k, F32, dev)
-    sp = vector(slots, "slots", T * k, I32, dev)
-    gp, ldg = matrix(dy, "dy", (T * k, H), (y.dtype,), dev)
-    dwp = _same(dweights, "dweights", T, k, F32, dev)
-    return dp, _in(dout), lddo, yp, _in(y), ldy, T, k, H, rp, wp, sp, gp, ldg, dwp, stream(dev)
+    args = _combine_backward(dout, y, rows, weights, slots, dev)
+    gp, ldg = matrix(dy, "dy", y.shape, (y.dtype,), dev)
+    return (*args, gp, ldg, flat(dweights, "dweights", weights.shape, F32, dev), stream(dev))
 
 
 def _score(score):
@@ -163,42 +180,73 @@ def _score(score):
     return _SCORES[score]
 
 
+@on_its_device
 def route_experts(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_best=1, renormalize=True, scale=1.0):
-    T = logits.shape[0]
-    experts, weights = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.float32)
-    fp8bq_route_experts(logits, k, _score(score), bias, groups, top_groups, group_best, renormalize, scale, experts, weights)
+    dev = logits.get_device()
+    args = _route(logits, k, _score(score), bias, groups, top_groups, group_best, renormalize, scale, dev)
+    at = stream(dev)
+    shape = (logits.shape[0], k)
+    experts, weights = logits.new_empty(shape, dtype=torch.int32), logits.new_empty(shape, dtype=torch.float32)
+    _call("fp8bq_route_experts", *args, experts.data_ptr(), weights.data_ptr(), at)
     return experts, weights
 
 
+@on_its_device
 def route_experts_backward(dweights, logits, experts, score="softmax", renormalize=True, scale=1.0):
+    dev = logits.get_device()
+    args = _route_backward(dweights, logits, _score(score), renormalize, scale, experts, dev)
+    at = stream(dev)
     dlogits = logits.new_empty(logits.shape)
-    fp8bq_route_experts_backward(dweights, logits, _score(score), renormalize, scale, experts, dlogits)
+    _call("fp8bq_route_experts_backward", *args, dlogits.data_ptr(), max(logits.shape[1], 1), at)
     return dlogits
 
 
 @on_its_device
 def expert_rows(experts, E):
-    n = experts.numel()
+    dev = experts.get_device()
+    shape, n = (experts.shape[0], _k_of(experts, "experts")), experts.numel()
+    ep = flat(experts, "experts", shape, I32, dev)
+    at = stream(dev)
     offsets = experts.new_empty(E + 1, dtype=torch.int64)
-    rows, slots = experts.new_empty(experts.shape), experts.new_empty(n)
-    fp8bq_expert_rows(experts, E, offsets, rows, slots, _space("fp8bq_expert_rows_workspace_size", experts, n, E))
+    rows, slots = experts.new_empty(shape), experts.new_empty(n)
+    ws = _space("fp8bq_expert_rows_workspace_size", experts, n, E)
+    wsp, wsb = (0, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _call("fp8bq_expert_rows", ep, n, E, offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), wsp, wsb, at)
     return offsets, rows, slots
 
 
+@on_its_device
 def gather_rows(x, slots, k):
-    out = x.new_empty((x.shape[0] * k, x.shape[1]))
-    fp8bq_gather_rows(x, slots, k, out)
+    dev = x.get_device()
+    args = _gather(x, slots, k, dev)
+    at = stream(dev)
+    T, H = x.shape
+    out = x.new_empty((T * k, H))
+    _call("fp8bq_gather_rows", *args, out.data_ptr(), H, at)
     return out
 
 
+@on_its_device
 def combine_rows(y, rows, weights=None, out_dtype=None):
     """out_dtype: y's, or bfloat16 or float32."""
-    out = y.new_empty((rows.shape[0], y.shape[1]), dtype=out_dtype or y.dtype)
-    fp8bq_combine_rows(y, rows, weights, out)
+    dev = y.get_device()
+    args = _combine(y, rows, weights, dev)
+    if out_dtype is None:
+        out_dtype = y.dtype
+    elif out_dtype not in HI:
+        raise TypeError(f"out_dtype must be bfloat16 or float32, not {out_dtype}")
+    at = stream(dev)
+    H = y.shape[1]
+    out = y.new_empty((rows.shape[0], H), dtype=out_dtype)
+    _call("fp8bq_combine_rows", *args, out.data_ptr(), OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, H, at)
     return out
 
 
+@on_its_device
 def combine_rows_backward(dout, y, rows, weights, slots):
+    dev = dout.get_device()
+    args = _combine_backward(dout, y, rows, weights, slots, dev)
+    at = stream(dev)
     dy, dweights = y.new_empty(y.shape), weights.new_empty(weights.shape)
-    fp8bq_combine_rows_backward(dout, y, rows, weights, slots, dy, dweights)
+    _call("fp8bq_combine_rows_backward", *args, dy.data_ptr(), y.shape[1], dweights.data_ptr(), at)
     return dy, dweights
