@@ -5,63 +5,112 @@
 // (sum of the chosen s).  Without a bias and with groups scored by their best expert the order of c is that of x, and
 // no score is computed for the choice; a normalized softmax then needs the chosen logits only.
 //
-// Near scores: c is computed in 64 bits (about 1e-14, exp64 below) and compared by its first 43 bits and, where those
+// Near scores: c is computed in 64 bits (about 1e-14, exp_all below) and compared by its first 43 bits and, where those
 // are equal, by the index, the lower first.  In 32 bits one token in some ten thousand would swap two experts.  FP64
 // runs at FP32's rate on this card, so what it costs is registers.
 //
 // Bound by instructions: 16384 tokens of 256 experts are 17 MB, 4 us at the copy's rate, and some 100 wave instructions
 // a token for scores and as many for the choice.  A token is shared by 16 lanes (many tokens) or 64 (few, where latency
 // counts).  The lanes are dealt to the groups first, so that a group's score is a reduction over neighbouring lanes; a
-// lane holds V consecutive experts of its group.  A key is the ordered bits of c with the inverted index in place of the
-// last nine, so keys are distinct, one maximum over the lanes names the winner, and it alone clears its slot.
+// lane holds V consecutive experts of its group.  A key is c with the index in place of its last nine bits (key_of), so
+// keys are distinct, one maximum over the lanes names the winner, and the winner alone clears its slot.
 #include "device_common.hpp"
 #include "launch.hpp"
 
 namespace fp8bq {
 
-// e^x in 64 bits for x <= 709 (below -708: 0): 2^n e^r, |r| <= ln 2 / 2, by the Taylor series to r^12 / 12! (the rest is
-// below 2 10^-16).
-__device__ __forceinline__ double exp64(double x) {
-  if (x < -708.0) return 0.0;  // (a NaN goes on)
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  // (ln 2 in two parts, as Cody and Waite do it: the first is its 32 bits behind the point, so n times it is exact)
-  double r = __builtin_fma(n, -0x1.62e42fee00000p-1, x);
-  r = __builtin_fma(n, -0x1.a39ef35793c76p-33, r);
-  double p = 1.0 / 479001600.0;
-  p = __builtin_fma(p, r, 1.0 / 39916800.0);
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
-  p = __builtin_fma(p, r, 1.0 / 362880.0);
-  p = __builtin_fma(p, r, 1.0 / 40320.0);
-  p = __builtin_fma(p, r, 1.0 / 5040.0);
-  p = __builtin_fma(p, r, 1.0 / 720.0);
-  p = __builtin_fma(p, r, 1.0 / 120.0);
-  p = __builtin_fma(p, r, 1.0 / 24.0);
-  p = __builtin_fma(p, r, 1.0 / 6.0);
-  p = __builtin_fma(p, r, 0.5);
-  p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_ldexp(p, (int)n);
-}
-// 1 / v for v >= 1 (infinity: 0): the hardware's estimate and two Newton steps.
-__device__ __forceinline__ double inverse64(double v) {
-  double r = __builtin_amdgcn_rcp(v);
-  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
-  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+// Maximum and minimum of numbers that are no NaN (written out: the compiler quiets NaNs before each of its own).
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
   return r;
 }
-__device__ __forceinline__ double sigmoid64(double x) {
-  // (e^708 is finite, so the steps stay finite; e^-708 and below are zero as weights in FP32)
-  const double t = x < -708.0 ? -708.0 : x;
-  const double s = inverse64(1.0 + exp64(-(t > 708.0 ? 708.0 : t)));
-  return x < -708.0 ? 0.0 : s;
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
 }
 
-// Bits of a double in the order of the doubles (NaN: the lowest of all that are not excluded); the last nine bits hold
-// 511 - e.  Excluded slots have the key 0.
-__device__ __forceinline__ uint64_t key_of(double c, int e) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, c + 0.0);  // (-0 and 0 are equal)
-  const uint64_t o = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
-  return (c != c ? 512ull : (o & ~511ull)) | (uint64_t)(511 - e);
+// e^x in 64 bits of V numbers up to 709, all through one step before the next, so that a step's constant is loaded once;
+// below -708: 0.  2^n e^r, |r| <= ln 2 / 2, by the Taylor series to r^12 / 12! (the rest is below 2 10^-16).
+template <int V>
+__device__ __forceinline__ void exp_all(double (&x)[V]) {
+  double p[V];
+  int n[V];
+  bool low[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    low[j] = x[j] < -708.0;  // (a NaN goes on)
+    const double t = low[j] ? -708.0 : x[j];
+    const double m = __builtin_rint(t * 1.4426950408889634);
+    // (ln 2 in two parts, as Cody and Waite do it: the first is its 32 bits behind the point, so m times it is exact)
+    x[j] = __builtin_fma(m, -0x1.a39ef35793c76p-33, __builtin_fma(m, -0x1.62e42fee00000p-1, t));
+    n[j] = (int)m;
+    p[j] = 1.0 / 479001600.0;
+  }
+  auto step = [&](double c) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[j] = __builtin_fma(p[j], x[j], c);
+  };
+  step(1.0 / 39916800.0);
+  step(1.0 / 3628800.0);
+  step(1.0 / 362880.0);
+  step(1.0 / 40320.0);
+  step(1.0 / 5040.0);
+  step(1.0 / 720.0);
+  step(1.0 / 120.0);
+  step(1.0 / 24.0);
+  step(1.0 / 6.0);
+  step(0.5);
+  step(1.0);
+  step(1.0);
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = low[j] ? 0.0 : __builtin_ldexp(p[j], n[j]);
+}
+__device__ __forceinline__ double exp64(double x) {
+  double v[1] = {x};
+  exp_all(v);
+  return v[0];
+}
+// 1 / (1 + e^-x): the hardware's estimate of the reciprocal and two Newton steps.  (e^708 is finite, so the steps stay
+// finite; below -708 the weight is zero in FP32 many times over.)
+template <int V>
+__device__ __forceinline__ void sigmoid_all(double (&x)[V]) {
+  double e[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) e[j] = x[j] < -708.0 ? 708.0 : -x[j];
+  exp_all(e);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const double v = 1.0 + e[j];
+    double r = __builtin_amdgcn_rcp(v);
+    r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+    r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+    x[j] = x[j] < -708.0 ? 0.0 : r;
+  }
+}
+__device__ __forceinline__ double sigmoid64(double x) {
+  double v[1] = {x};
+  sigmoid_all(v);
+  return v[0];
+}
+
+// c with the index in its last nine bits, so that of equal ones the lower index is the larger number: 511 - e where c is
+// positive, e where it is negative and more bits are a smaller number.  c is kept within 10^308 (infinities; a NaN counts
+// as -infinity); kShut, of a slot that cannot be chosen or was, is below all.
+constexpr double kMostKey = 1e308;
+constexpr uint32_t kShutHigh = 0xFFEFFFFFu;  // the high word of numbers below -1.797 10^308
+__device__ __forceinline__ double shut_key() { return __builtin_bit_cast(double, (uint64_t)kShutHigh << 32); }
+__device__ __forceinline__ double key_of(double c, int e) {
+  c = c > -kMostKey ? c : -kMostKey;
+  c = c < kMostKey ? c + 0.0 : kMostKey;  // (-0 and 0 are equal)
+  const uint64_t b = __builtin_bit_cast(uint64_t, c);
+  const uint32_t low = ((uint32_t)b & ~511u) | (uint32_t)((int64_t)b < 0 ? e : 511 - e);
+  return __builtin_bit_cast(double, (b & 0xFFFFFFFF00000000ull) | low);
+}
+__device__ __forceinline__ int index_of(double key) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, key);
+  return (int64_t)b < 0 ? (int)(b & 511) : 511 - (int)(b & 511);
 }
 
 // The value that lane l ^ d holds (16 <= d), or of the partner in a reduction over 2 d lanes that leaves equal values
@@ -140,10 +189,10 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn* __restrict__ x, i
     if (a.wide) {  // (then n is V or not positive)
       loaded = true;
       constexpr int P = 16 / sizeof(TIn);
+      const TIn* at = xr + (n > 0 ? e0 : 0);
 #pragma unroll
       for (int j = 0; j < V; j += P) {
-        v4i w = {0, 0, 0, 0};
-        if (n > 0) w = *reinterpret_cast<const v4i*>(xr + e0 + j);
+        const v4i w = *reinterpret_cast<const v4i*>(at + j);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           if constexpr (P == 8) c[j + i] = (double)((i & 1) ? bf16hi((uint32_t)w[i / 2]) : bf16lo((uint32_t)w[i / 2]));
@@ -152,9 +201,9 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn* __restrict__ x, i
       }
     }
   }
-  if (!loaded) {
+  if (!loaded) {  // (slots without an expert read another's logit)
 #pragma unroll
-    for (int j = 0; j < V; ++j) c[j] = j < n ? logit_at(xr + e0 + j) : 0.0;
+    for (int j = 0; j < V; ++j) c[j] = logit_at(xr + (j < n ? e0 + j : 0));
   }
 
   // softmax of all: the largest logit and the sum of the exponentials, where they are needed
@@ -164,49 +213,48 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn* __restrict__ x, i
   if (softmax && (!ordered || !how.renormalize)) {
 #pragma unroll
     for (int j = 0; j < V; ++j) top = j < n && c[j] > top ? c[j] : top;
-    top = over_lanes<L>(top, [](double p, double q) { return p > q ? p : q; });
+    top = over_lanes<L>(top, [](double p, double q) { return max64(p, q); });
     const double shift = top == -inf ? 0.0 : top;
+    double e[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = c[j] - shift;
+    exp_all(e);
     double sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const double e = exp64(c[j] - shift);
-      sum += j < n ? e : 0.0;
-      if (!ordered) c[j] = e;
-    }
+    for (int j = 0; j < V; ++j) sum += j < n ? e[j] : 0.0;
     norm = over_lanes<L>(sum, [](double p, double q) { return p + q; });
     norm = norm == 0.0 ? 0.0 : 1.0 / norm;  // (every expert switched off: all scores are zero)
     if (!ordered) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) c[j] *= norm;
+      for (int j = 0; j < V; ++j) c[j] = e[j] * norm;
     }
   } else if (!ordered) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) c[j] = sigmoid64(c[j]);
+    sigmoid_all(c);
   }
   if (bias != nullptr) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) c[j] += j < n ? (double)bias[e0 + j] : 0.0;
+    for (int j = 0; j < V; ++j) c[j] += (double)bias[j < n ? e0 + j : 0];
   }
+  double key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = j < n ? key_of(c[j], e0 + j) : shut_key();
 
-  bool open = n > 0;
   if (how.top_groups < how.groups) {
-    double t1 = -inf, t2 = -inf;  // (NaN is below every score)
+    // (by c itself and not by its key: the sum of two keys has the indexes in it)
+    double t1 = -kMostKey, t2 = -kMostKey;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const double v = j < n && c[j] > -inf ? c[j] : -inf;
-      const double low = v < t1 ? v : t1;
-      t2 = low > t2 ? low : t2;
-      t1 = v > t1 ? v : t1;
+      const double v = j < n && c[j] > -kMostKey ? c[j] : -kMostKey;  // (NaN is below every score)
+      t2 = max64(t2, min64(v, t1));
+      t1 = max64(t1, v);
     }
     with_lanes<L>(a.lanes_log2, [&](auto lanes) {
       auto step = [&](auto d) {
         constexpr int D = decltype(d)::value;
         if constexpr (D < decltype(lanes)::value) {
           const double o1 = partner<D>(t1), o2 = partner<D>(t2);
-          const double low = o1 < t1 ? o1 : t1;  // the second best is this or one of the two seconds
-          t1 = o1 > t1 ? o1 : t1;
-          t2 = o2 > t2 ? o2 : t2;
-          t2 = low > t2 ? low : t2;
+          t2 = max64(max64(t2, o2), min64(t1, o1));  // one of the two seconds, or the smaller of the firsts
+          t1 = max64(t1, o1);
         }
       };
       step(std::integral_constant<int, 1>{});
@@ -218,32 +266,34 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn* __restrict__ x, i
         step(std::integral_constant<int, 32>{});
       }
     });
-    double score = how.group_best == 2 ? t1 + t2 : t1;
-    score = score > -inf ? score : -inf;
-    // (the first 43 bits, as for the experts)
-    const uint64_t mine = key_of(score, 0) >> 9;
+    const double mine = key_of(how.group_best == 2 ? t1 + t2 : t1, group);
     int ahead = 0;
     for (int g = 0; g < how.groups; ++g) {
+      const uint64_t b = __builtin_bit_cast(uint64_t, mine);
       const int from = g << a.lanes_log2;
-      const uint64_t o = (uint64_t)(uint32_t)__shfl((int)(uint32_t)mine, from, L) |
-                         (uint64_t)(uint32_t)__shfl((int)(uint32_t)(mine >> 32), from, L) << 32;
-      ahead += o > mine || (o == mine && g < group) ? 1 : 0;
+      const uint64_t o = (uint64_t)(uint32_t)__shfl((int)(uint32_t)b, from, L) |
+                         (uint64_t)(uint32_t)__shfl((int)(uint32_t)(b >> 32), from, L) << 32;
+      ahead += __builtin_bit_cast(double, o) > mine ? 1 : 0;
     }
-    open = open && ahead < how.top_groups;
+    if (ahead >= how.top_groups) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) key[j] = shut_key();
+    }
   }
 
-  uint64_t key[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) key[j] = open && j < n ? key_of(c[j], e0 + j) : 0;
   int chosen = 0;  // of lane r: expert r
   for (int r = 0; r < how.k; ++r) {
-    uint64_t best = key[0];
+    double best = key[0];
 #pragma unroll
-    for (int j = 1; j < V; ++j) best = key[j] > best ? key[j] : best;
-    best = over_lanes<L>(best, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
+    for (int j = 1; j < V; ++j) best = max64(best, key[j]);
+    best = over_lanes<L>(best, [](double p, double q) { return max64(p, q); });
 #pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = key[j] == best ? 0 : key[j];
-    if (lane == r) chosen = 511 - (int)(best & 511);
+    for (int j = 0; j < V; ++j) {  // (the high word alone makes it one of the shut)
+      const uint64_t b = __builtin_bit_cast(uint64_t, key[j]);
+      const uint32_t high = key[j] == best ? kShutHigh : (uint32_t)(b >> 32);
+      key[j] = __builtin_bit_cast(double, (uint64_t)high << 32 | (uint32_t)b);
+    }
+    if (lane == r) chosen = index_of(best);
   }
 
   const bool live = lane < how.k;
@@ -292,17 +342,32 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
   auto most = [](double p, double q) { return p > q ? p : q; };
   double g;
   if (how.score == 0 && !how.renormalize) {
-    double top = -inf;
-    for (int i = lane; i < E; i += 64) top = most(logit_at(xr + i), top);
+    constexpr int V = kMaxRouteExperts / 64;
+    double v[V], top = -inf, sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = lane + 64 * j;
+      v[j] = -inf;
+      if (64 * j < E) v[j] = i < E ? logit_at(xr + i) : -inf;
+      top = most(v[j], top);
+    }
     top = over_lanes<64>(top, most);
     top = top == -inf ? 0.0 : top;
-    double sum = 0.0;
-    for (int i = lane; i < E; i += 64) sum += exp64(logit_at(xr + i) - top);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (64 * j >= E) break;
+      v[j] = exp64(v[j] - top);
+      sum += v[j];
+    }
     sum = over_lanes<64>(sum, add);
     const double norm = sum == 0.0 ? 0.0 : 1.0 / sum;
     const double s = live ? exp64(xc - top) * norm : 0.0;
     const double mean = over_lanes<64>(d * s, add);
-    for (int i = lane; i < E; i += 64) row[i] = (float)(-mean * exp64(logit_at(xr + i) - top) * norm);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (64 * j >= E) break;
+      row[lane + 64 * j] = (float)(-mean * v[j] * norm);
+    }
     g = s * (d - mean);
   } else {
     for (int i = lane; i < E; i += 64) row[i] = 0.0f;

@@ -38,8 +38,8 @@ typedef enum { FP8BQ_SCORE_SOFTMAX = 0, FP8BQ_SCORE_SIGMOID = 1 } fp8bq_score;
  *   Scores and sums are computed in 64 bits.  c and groups' scores that agree in their first 43 bits count as equal, and
  *   the lower index comes first.  Without a bias and with group_best 1 the logits themselves are compared.
  *   A logit of -infinity has the score zero (a switched-off expert, chosen only when nothing else is left); a row of
- *   nothing else gives weights of zero.  A NaN comes last; with softmax, a NaN or +infinity makes the row's weights NaN
- *   where they depend on it.  The chosen experts are always k different indices.
+ *   nothing else gives weights of zero.  A NaN is chosen like -infinity; with softmax, a NaN or +infinity makes the row's
+ *   weights NaN where they depend on it.  The chosen experts are always k different indices.
  *   bias NULL or [E].  groups divides E, groups <= FP8BQ_MAX_EXPERT_GROUPS, k <= top_groups E / groups,
  *   group_best <= E / groups; scale finite.  (With groups == top_groups every group stays.)
  */
