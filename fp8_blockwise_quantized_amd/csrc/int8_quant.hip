@@ -149,6 +149,7 @@ __global__ __launch_bounds__(256) void int8_colmax_kernel(const TIn* __restrict_
   const int64_t r0 = b.row * rows, r1 = r0 + rows < R ? r0 + rows : R;
   uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < C) {
+#pragma unroll 4
     for (int64_t r = r0 + rr; r < r1; r += 16) {
       float v[8];
       Load8<TIn>::run(x + r * ldx + c, v);
@@ -167,55 +168,56 @@ __global__ __launch_bounds__(256) void int8_colmax_kernel(const TIn* __restrict_
   }
 }
 
-// Second pass: a tile of 128 rows by 128 columns; codes go through LDS and leave transposed, 16 rows to a store.
+// Second pass: a tile of 128 rows by 128 columns; codes go through LDS and leave transposed, 16 rows to a store.  A
+// thread's values are on their way while the maxima of the chunks are joined.
 template <typename TIn>
 __global__ __launch_bounds__(256) void int8_cols_kernel(const TIn* __restrict__ x, int64_t R, int64_t C, int64_t ldx,
                                                         uint32_t ctiles, const uint32_t* __restrict__ part, int chunks,
                                                         uint8_t* __restrict__ qt, int64_t ldqt, float* __restrict__ st) {
-  __shared__ float scale[kColPos];
+  __shared__ float scale[kColPos], inverse[kColPos];
+  __shared__ uint32_t other[kQtCols];
   __shared__ __attribute__((aligned(16))) uint8_t codes[kQtBytes];
   const TileRC b = tile_of_block(ctiles);
   const int t = threadIdx.x;
   const int64_t c0 = b.col * kQtCols;
   const int64_t r0 = b.row * 128;
-  if (t < kQtCols) {
-    uint32_t a = 0;
-    if (c0 + t < C)
-      for (int k = 0; k < chunks; ++k) a = umax(a, part[(int64_t)k * C + c0 + t]);
-    const float sc = int8_scale(a);
-    scale[col_pos(t)] = sc;
-    if (b.row == 0 && c0 + t < C) st[c0 + t] = sc;
-  }
-  __syncthreads();
   // thread: columns 8 cc .. +7 of rows 8 rr .. +7
   const int cc = t & 15, rr = t >> 4;
   const int64_t c = c0 + 8 * cc;
-  uint32_t w[8][2];  // [column][half]: codes of eight rows
+  Raw8<TIn> raw[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i][0] = w[i][1] = 0;
-  float sc[8], rc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    sc[i] = scale[col_pos(8 * cc + i)];
-    rc[i] = 1.0f / sc[i];
+  for (int k = 0; k < 8; ++k) {
+    const int64_t r = r0 + 8 * rr + k;
+    if (r < R && c < C) raw[k].load(x + r * ldx + c); else raw[k].zero();
   }
+  {
+    const int col = t & (kQtCols - 1), half = t >> 7;  // each half of the threads takes every other chunk
+    const int64_t at = c0 + col < C ? c0 + col : C - 1;
+    uint32_t a = 0;
+#pragma unroll 8
+    for (int k = half; k < chunks; k += 2) a = umax(a, part[(int64_t)k * C + at]);
+    if (half) other[col] = a;
+    __syncthreads();
+    if (!half) {
+      const float sc = int8_scale(umax(a, other[col]));
+      scale[col_pos(col)] = sc;
+      inverse[col_pos(col)] = 1.0f / sc;
+      if (b.row == 0 && c0 + col < C) st[c0 + col] = sc;
+    }
+  }
+  __syncthreads();
+  uint32_t w[8][2];  // [column][half]: codes of eight rows
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     float v[4][8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t r = r0 + 8 * rr + 4 * half + k;
-      if (r < R && c < C) {
-        Load8<TIn>::run(x + r * ldx + c, v[k]);
-      } else {
+    for (int k = 0; k < 4; ++k) raw[4 * half + k].get(v[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float sc = scale[col_pos(8 * cc + i)], rc = inverse[col_pos(8 * cc + i)];
+      w[i][half] = int8_pack4(div_by_scale(v[0][i], sc, rc), div_by_scale(v[1][i], sc, rc), div_by_scale(v[2][i], sc, rc),
+                              div_by_scale(v[3][i], sc, rc));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i][half] = int8_pack4(div_by_scale(v[0][i], sc[i], rc[i]), div_by_scale(v[1][i], sc[i], rc[i]),
-                              div_by_scale(v[2][i], sc[i], rc[i]), div_by_scale(v[3][i], sc[i], rc[i]));
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -233,9 +235,9 @@ __global__ __launch_bounds__(256) void int8_cols_kernel(const TIn* __restrict__ 
 
 int int8_col_chunks(int64_t R, int64_t C) {
   const int64_t tiles = (C + kQtCols - 1) / kQtCols, most = (R + 127) / 128;
-  int64_t chunks = (2048 + tiles - 1) / tiles;  // about 2048 workgroups
+  int64_t chunks = (1024 + tiles - 1) / tiles;  // about 1024 workgroups; every tile of the second pass reads all chunks
   chunks = chunks < most ? chunks : most;
-  return (int)(chunks < 1 ? 1 : chunks > 64 ? 64 : chunks);
+  return (int)(chunks < 1 ? 1 : chunks > 32 ? 32 : chunks);
 }
 
 template <typename TIn>

@@ -109,10 +109,30 @@ struct OrthoBuffers {
 template <typename TIn>
 __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict__ g, int64_t R, int64_t C, int64_t ldg,
                                                           int64_t bstride, const double* __restrict__ parts, int nparts,
-                                                          double eps, OrthoBuffers b, int tall, float* __restrict__ factor) {
-  __shared__ uint16_t tile[64][66];
-  __shared__ uint16_t low[64][66];
+                                                          double eps, OrthoBuffers b, int tall, int wide, float* __restrict__ factor) {
+  __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
+  __shared__ __attribute__((aligned(16))) uint16_t low[sizeof(TIn) == 4 ? 64 : 1][72];
   const int t = threadIdx.x, batch = blockIdx.z;
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const TIn* gb = g + (int64_t)batch * bstride;
+  const int row = t >> 3, c = 8 * (t & 7);  // eight columns of rows row and row + 32, on their way while the norm is taken
+  float v[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = r0 + row + 32 * h;
+    if (wide && r < R && c0 + c < C) {
+      Load8<TIn>::run(gb + r * ldg + c0 + c, v[h]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[h][i] = 0.0f;
+        if (r < R && c0 + c + i < C) {
+          if constexpr (sizeof(TIn) == 2) v[h][i] = bf16lo(gb[r * ldg + c0 + c + i]);
+          else v[h][i] = gb[r * ldg + c0 + c + i];
+        }
+      }
+    }
+  }
   double sum = 0.0;  // (every wave alike, in a fixed order)
   for (int i = t & 63; i < nparts; i += 64) sum += parts[(int64_t)batch * nparts + i];
 #pragma unroll
@@ -123,35 +143,51 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
   const int ex = finite ? __builtin_amdgcn_frexp_exp(norm) : 0;
   if (t == 0 && blockIdx.x == 0 && blockIdx.y == 0)
     factor[batch] = finite ? (float)(1.0 / __builtin_amdgcn_frexp_mant(norm)) : __builtin_nanf("");
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  const TIn* gb = g + (int64_t)batch * bstride;
-  const int c = t & 63;
-#pragma unroll 4
-  for (int k = 0; k < 16; ++k) {
-    const int r = (t >> 6) + 4 * k;
-    float v = 0.0f;
-    if (r0 + r < R && c0 + c < C) {
-      if constexpr (sizeof(TIn) == 2) v = bf16lo(gb[(r0 + r) * ldg + c0 + c]);
-      else v = gb[(r0 + r) * ldg + c0 + c];
-    }
-    v = __builtin_ldexpf(v, 12 - ex);
-    const _Float16 hi = (_Float16)v;
-    tile[r][c] = __builtin_bit_cast(uint16_t, hi);
-    if constexpr (sizeof(TIn) == 4) low[r][c] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)hi));
-  }
-  __syncthreads();
   // (buffers are padded to whole tiles of 64 along their rows; rows past the matrix are not there)
   uint16_t* x = b.x + (int64_t)batch * b.m * b.np;
   uint16_t* xt = b.xt + (int64_t)batch * b.n * 2 * b.mp;
-#pragma unroll 4
-  for (int k = 0; k < 16; ++k) {
-    const int i = (t >> 6) + 4 * k;  // row of the buffer's tile; c its column
-    const int64_t xr = tall ? c0 + i : r0 + i, xc = (tall ? r0 : c0) + c;
-    if (xr < b.m) x[xr * b.np + xc] = tall ? tile[c][i] : tile[i][c];
-    const int64_t tr = tall ? r0 + i : c0 + i, tc = (tall ? c0 : r0) + c;
-    if (tr < b.n) {
-      xt[tr * 2 * b.mp + tc] = tall ? tile[i][c] : tile[c][i];
-      if constexpr (sizeof(TIn) == 4) xt[tr * 2 * b.mp + b.mp + tc] = tall ? low[i][c] : low[c][i];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = r0 + row + 32 * h;
+    u32x4 hi, lo = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a0 = __builtin_ldexpf(v[h][2 * i], 12 - ex), a1 = __builtin_ldexpf(v[h][2 * i + 1], 12 - ex);
+      hi[i] = pack_f16x2(a0, a1);
+      if constexpr (sizeof(TIn) == 4) {
+        float h0, h1;
+        unpack_f16x2(hi[i], h0, h1);
+        lo[i] = pack_f16x2(a0 - h0, a1 - h1);
+      }
+    }
+    *reinterpret_cast<u32x4*>(&tile[row + 32 * h][c]) = hi;
+    if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(&low[row + 32 * h][c]) = lo;
+    if (r < R) {
+      if (tall) {
+        *reinterpret_cast<u32x4*>(xt + r * 2 * b.mp + c0 + c) = hi;
+        if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(xt + r * 2 * b.mp + b.mp + c0 + c) = lo;
+      } else {
+        *reinterpret_cast<u32x4*>(x + r * b.np + c0 + c) = hi;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = row + 32 * h;  // column of G; rows c .. c + 7
+    if (c0 + i >= C) continue;
+    u32x4 hi, lo;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) hi[k] = tile[c + 2 * k][i] | (uint32_t)tile[c + 2 * k + 1][i] << 16;
+    if (tall) {
+      *reinterpret_cast<u32x4*>(x + (c0 + i) * b.np + r0 + c) = hi;
+    } else {
+      *reinterpret_cast<u32x4*>(xt + (c0 + i) * 2 * b.mp + r0 + c) = hi;
+      if constexpr (sizeof(TIn) == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lo[k] = low[c + 2 * k][i] | (uint32_t)low[c + 2 * k + 1][i] << 16;
+        *reinterpret_cast<u32x4*>(xt + (c0 + i) * 2 * b.mp + b.mp + r0 + c) = lo;
+      }
     }
   }
 }
@@ -420,12 +456,12 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     hipLaunchKernelGGL(ortho_norm_kernel<uint16_t>, ngrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, wide, norms);
     FP8BQ_TRY(hipGetLastError());
     hipLaunchKernelGGL(ortho_begin_kernel<uint16_t>, bgrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, norms,
-                       p.norm_blocks, eps, b, (int)tall, factor);
+                       p.norm_blocks, eps, b, (int)tall, wide, factor);
   } else {
     hipLaunchKernelGGL(ortho_norm_kernel<float>, ngrid, dim3(256), 0, st, (const float*)g, p.R, p.C, ldg, gbatch, wide, norms);
     FP8BQ_TRY(hipGetLastError());
     hipLaunchKernelGGL(ortho_begin_kernel<float>, bgrid, dim3(256), 0, st, (const float*)g, p.R, p.C, ldg, gbatch, norms,
-                       p.norm_blocks, eps, b, (int)tall, factor);
+                       p.norm_blocks, eps, b, (int)tall, wide, factor);
   }
   FP8BQ_TRY(hipGetLastError());
 
