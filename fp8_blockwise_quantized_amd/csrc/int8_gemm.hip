@@ -19,10 +19,10 @@ struct Int8Out {
 
 // OUT: 0 BF16, 1 FP32, 2 FP32 added to the output, kPartial the sums of a split contraction.
 constexpr int kPartial = 3;
-template <int BM, int BN, int WGM, int WGN, int OUT, bool GROUPED>
-__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWaves)) void int8_gemm_kernel(
+template <int BM, int BN, int WGM, int WGN, int NST, int OUT, bool GROUPED>
+__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN, NST>::kMinWaves)) void int8_gemm_kernel(
     RowDesc d, Int8Out o, uint32_t tiles_m, uint32_t tiles_n, int nsplit, GroupArgs<kGroupRowsMode> grp) {
-  using Tile = RowTile<BM, BN, WGM * WGN>;
+  using Tile = RowTile<BM, BN, WGM * WGN, NST>;
   constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kRing + (GROUPED ? kGroupTableBytes : 0)];
   // (a row of patches at a time: the whole tile in FP32 beside its sums took more registers than there are)
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWav
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  row_gemm_units<kRowsI8, BM, BN, WGM, WGN, GROUPED ? kUnitsGrouped : kUnitsFull>(d, tiles_m, tiles_n, nsplit, 1, &grp,
+  row_gemm_units<kRowsI8, BM, BN, WGM, WGN, NST, GROUPED ? kUnitsGrouped : kUnitsFull>(d, tiles_m, tiles_n, nsplit, 1, &grp,
                                                                                   smem, end);
 }
 
@@ -110,18 +110,18 @@ __global__ __launch_bounds__(256) void int8_reduce_kernel(Int8Out o, int nsplit,
   }
 }
 
-template <int BM, int BN, int WGM, int WGN, int OUT>
+template <int BM, int BN, int WGM, int WGN, int NST, int OUT>
 static hipError_t launch_tile(const RowDesc& r, const Int8Out& o, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)p.grid), block(WGM * WGN * 64);
   const GroupArgs<kGroupRowsMode> none{nullptr, 0, 0};
   if constexpr (OUT < 2) {  // (a grouped product is not added to the output, nor split)
     if (grp.offsets) {
-      hipLaunchKernelGGL((int8_gemm_kernel<BM, BN, WGM, WGN, OUT, true>), grid, block, 0, st, r, o, (uint32_t)p.tiles_m,
+      hipLaunchKernelGGL((int8_gemm_kernel<BM, BN, WGM, WGN, NST, OUT, true>), grid, block, 0, st, r, o, (uint32_t)p.tiles_m,
                          (uint32_t)p.tiles_n, 1, GroupArgs<kGroupRowsMode>{grp.offsets, grp.experts, r.M});
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((int8_gemm_kernel<BM, BN, WGM, WGN, OUT, false>), grid, block, 0, st, r, o, (uint32_t)p.tiles_m,
+  hipLaunchKernelGGL((int8_gemm_kernel<BM, BN, WGM, WGN, NST, OUT, false>), grid, block, 0, st, r, o, (uint32_t)p.tiles_m,
                      (uint32_t)p.tiles_n, p.split_k, none);
   return hipGetLastError();
 }
@@ -138,9 +138,10 @@ static hipError_t launch_out(const Int8Desc& d, const MxGroups& grp, const MxPla
   r.K = d.K;
   const Int8Out o{d.sa, d.sb, d.c, d.ldc, d.past, (d.ldc * (OUT == 0 ? 2 : 4)) % 16 == 0, (int32_t*)ws, (d.N + 3) / 4 * 4};
   switch (p.shape) {
-    case k256x256: return launch_tile<256, 256, 2, 4, OUT>(r, o, grp, p, st);
-    case k64x64: return launch_tile<64, 64, 2, 2, OUT>(r, o, grp, p, st);
-    default: return launch_tile<128, 128, 2, 2, OUT>(r, o, grp, p, st);
+    case k256x256: return launch_tile<256, 256, 2, 4, 2, OUT>(r, o, grp, p, st);
+    case k64x64:
+      return p.deep ? launch_tile<64, 64, 2, 2, 3, OUT>(r, o, grp, p, st) : launch_tile<64, 64, 2, 2, 2, OUT>(r, o, grp, p, st);
+    default: return launch_tile<128, 128, 2, 2, 2, OUT>(r, o, grp, p, st);
   }
 }
 

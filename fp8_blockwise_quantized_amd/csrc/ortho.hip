@@ -320,10 +320,10 @@ __device__ __forceinline__ void ortho_row(const OrthoEnd& e, const v16f (&v)[NI]
 template <int STEP>
 constexpr int ortho_units() { return STEP == kOrthoGram || STEP == kOrthoPoly ? kUnitsTriangle : kUnitsFull; }
 
-template <int BM, int BN, int WGM, int WGN, int STEP>
-__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWaves)) void ortho_gemm_kernel(
+template <int BM, int BN, int WGM, int WGN, int NST, int STEP>
+__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN, NST>::kMinWaves)) void ortho_gemm_kernel(
     RowDesc d, OrthoEnd e, uint32_t tiles_m, uint32_t tiles_n, int batches) {
-  using Tile = RowTile<BM, BN, WGM * WGN>;
+  using Tile = RowTile<BM, BN, WGM * WGN, NST>;
   constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kRing];
   auto end = [&](const v16f (&acc)[MI][NI], const RowPlace& p) {
@@ -333,15 +333,15 @@ __global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWav
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  row_gemm_units<kRowsF16, BM, BN, WGM, WGN, ortho_units<STEP>()>(d, tiles_m, tiles_n, 1, batches, nullptr, smem, end);
+  row_gemm_units<kRowsF16, BM, BN, WGM, WGN, NST, ortho_units<STEP>()>(d, tiles_m, tiles_n, 1, batches, nullptr, smem, end);
 }
 
 // Split contractions: a part's sums as the lanes hold them, parts[part][batch][tile][wave][patch][quarter][lane] of four
 // floats; and the kernel that adds them up, one row of a wave's patches to a wave.
-template <int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWaves)) void ortho_part_kernel(
+template <int BM, int BN, int WGM, int WGN, int NST>
+__global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN, NST>::kMinWaves)) void ortho_part_kernel(
     RowDesc d, v4f* __restrict__ parts, uint32_t tiles, int nsplit, int batches) {
-  using Tile = RowTile<BM, BN, WGM * WGN>;
+  using Tile = RowTile<BM, BN, WGM * WGN, NST>;
   constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kRing];
   const int64_t T = (int64_t)tiles * (tiles + 1) / 2;
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN>::kMinWav
         for (int r = 0; r < 4; ++r)
           o[((i * NI + j) * 4 + r) * 64] = (v4f){acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
   };
-  row_gemm_units<kRowsF16, BM, BN, WGM, WGN, kUnitsTriangle>(d, tiles, tiles, nsplit, batches, nullptr, smem, end);
+  row_gemm_units<kRowsF16, BM, BN, WGM, WGN, NST, kUnitsTriangle>(d, tiles, tiles, nsplit, batches, nullptr, smem, end);
 }
 template <int BM, int BN, int WGM, int WGN, int STEP>
 __global__ __launch_bounds__(256) void ortho_sum_kernel(OrthoEnd e, const v4f* __restrict__ parts, uint32_t tiles, int nsplit,
@@ -374,12 +374,17 @@ __global__ __launch_bounds__(256) void ortho_sum_kernel(OrthoEnd e, const v4f* _
 #pragma unroll
   for (int j = 0; j < NI; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      v4f s = at[(j * 4 + r) * 64];
-      for (int k = 1; k < nsplit; ++k) s += at[k * step + (j * 4 + r) * 64];
+    for (int x = 0; x < 16; ++x) v[0][j][x] = 0.0f;
+#pragma unroll 2
+  for (int k = 0; k < nsplit; ++k, at += step) {  // (in the order of the parts; a part's loads are in flight together)
+    v4f s[NI * 4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) v[0][j][4 * r + x] = s[x];
-    }
+    for (int q = 0; q < NI * 4; ++q) s[q] = at[q * 64];
+#pragma unroll
+    for (int q = 0; q < NI * 4; ++q)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[0][q / 4][4 * (q % 4) + x] += s[q][x];
+  }
   uint32_t tm, tn;
   row_tile<kUnitsTriangle>(w, tiles, tiles, tm, tn);
   RowPlace p;
@@ -399,13 +404,13 @@ __global__ __launch_bounds__(256) void ortho_sum_kernel(OrthoEnd e, const v4f* _
   ortho_row<STEP, NI>(e, v[0], p, p.m + 32 * i);
 }
 
-template <int BM, int BN, int WGM, int WGN, int STEP>
+template <int BM, int BN, int WGM, int WGN, int NST, int STEP>
 static hipError_t launch_product_tile(const RowDesc& d, const OrthoEnd& e, const OrthoProduct& p, int batches, void* parts,
                                       hipStream_t st) {
   const dim3 block(WGM * WGN * 64);
   if constexpr (ortho_units<STEP>() == kUnitsTriangle) {
     if (p.split > 1) {
-      hipLaunchKernelGGL((ortho_part_kernel<BM, BN, WGM, WGN>), dim3((unsigned)p.grid), block, 0, st, d, (v4f*)parts,
+      hipLaunchKernelGGL((ortho_part_kernel<BM, BN, WGM, WGN, NST>), dim3((unsigned)p.grid), block, 0, st, d, (v4f*)parts,
                          (uint32_t)p.tiles_m, p.split, batches);
       const hipError_t r = hipGetLastError();
       if (r != hipSuccess) return r;
@@ -415,7 +420,7 @@ static hipError_t launch_product_tile(const RowDesc& d, const OrthoEnd& e, const
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((ortho_gemm_kernel<BM, BN, WGM, WGN, STEP>), dim3((unsigned)p.grid), block, 0, st, d, e,
+  hipLaunchKernelGGL((ortho_gemm_kernel<BM, BN, WGM, WGN, NST, STEP>), dim3((unsigned)p.grid), block, 0, st, d, e,
                      (uint32_t)p.tiles_m, (uint32_t)p.tiles_n, batches);
   return hipGetLastError();
 }
@@ -423,9 +428,14 @@ template <int STEP>
 static hipError_t launch_product(const RowDesc& d, const OrthoEnd& e, const OrthoProduct& p, int batches, void* parts,
                                  hipStream_t st) {
   switch (p.shape) {
-    case k256x256: return launch_product_tile<256, 256, 2, 4, STEP>(d, e, p, batches, parts, st);
-    case k64x64: return launch_product_tile<64, 64, 2, 2, STEP>(d, e, p, batches, parts, st);
-    default: return launch_product_tile<128, 128, 2, 2, STEP>(d, e, p, batches, parts, st);
+    case k256x256: return launch_product_tile<256, 256, 2, 4, 2, STEP>(d, e, p, batches, parts, st);
+    case k256x192:
+      if constexpr (ortho_units<STEP>() == kUnitsFull) return launch_product_tile<256, 192, 4, 2, 2, STEP>(d, e, p, batches, parts, st);
+      return hipErrorInvalidValue;  // (never planned for a symmetric result)
+    case k64x64:
+      return p.deep ? launch_product_tile<64, 64, 2, 2, 3, STEP>(d, e, p, batches, parts, st)
+                    : launch_product_tile<64, 64, 2, 2, 2, STEP>(d, e, p, batches, parts, st);
+    default: return launch_product_tile<128, 128, 2, 2, 2, STEP>(d, e, p, batches, parts, st);
   }
 }
 

@@ -9,15 +9,17 @@ static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static size_t up256(double n) { return ((size_t)n + 255) & ~(size_t)255; }
 
 // Time of one 128-byte stage for a full round of resident work units, us (as the MXFP4 product's, whose loop it is).
-static double stage_us(int shape) { return shape == k256x256 ? 2.1 : shape == k64x64 ? 0.98 : 1.33; }
+static double stage_us(int shape) {
+  return shape == k256x256 ? 2.1 : shape == k256x192 ? 1.65 : shape == k64x64 ? 0.98 : 1.33;
+}
 constexpr int kMaxOrthoSplit = 16;
 
 // rows x cols outputs (triangle: a symmetric rows x rows result) of nkb stages, for each of the batch.
 static OrthoProduct plan_product(int64_t rows, int64_t cols, int64_t nkb, int64_t batch, bool triangle, int64_t cus) {
   OrthoProduct best;
   double best_us = 0.0;
-  const int shapes[3] = {k256x256, k128x128, k64x64};
-  for (int i = 0; i < 3; ++i) {
+  const int shapes[4] = {k256x256, k128x128, k64x64, k256x192};
+  for (int i = 0; i < (triangle ? 3 : 4); ++i) {  // (a symmetric result has square tiles)
     const int s = shapes[i];
     OrthoProduct p;
     p.shape = s;
@@ -42,6 +44,7 @@ static OrthoProduct plan_product(int64_t rows, int64_t cols, int64_t nkb, int64_
   const int64_t g = slots >= 8 ? slots - slots % 8 : slots;
   const int64_t units = best.tiles * best.split * batch;
   best.grid = units < g ? units : g;
+  best.deep = best.shape == k64x64 && units <= kDeepPerCu * cus;
   return best;
 }
 

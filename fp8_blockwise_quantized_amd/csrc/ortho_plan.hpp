@@ -9,6 +9,7 @@ namespace fp8bq {
 struct OrthoProduct {
   int shape = 0;
   int split = 1;
+  bool deep = false;  // 64 x 64 tiles that are all on the card at once: a ring of three stages
   int64_t tiles_m = 0, tiles_n = 0, tiles = 0;  // tiles: of one matrix (those on and above the diagonal for A and A^2)
   int64_t grid = 0;
 };

@@ -313,6 +313,7 @@ MxPlan plan_int8(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu
     return p;
   }
   plan_tiles(p, E, M, N, cdiv(K, 128), cus);
+  p.deep = p.shape == k64x64 && used * cdiv(p.rows, 64) * p.tiles_n * p.split_k <= kDeepPerCu * cus;
   return p;
 }
 

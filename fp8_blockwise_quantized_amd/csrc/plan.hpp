@@ -20,14 +20,18 @@ enum Op : int { kOpFprop = 0, kOpDgrad = 1, kOpWgrad = 2, kOpDgradWt = 3, kOpTen
 //   k128x128: 4 waves of 64x64, two workgroups per CU;
 //   k128x256 / k256x128: 8 waves of 64x64, one workgroup per CU (tuning shapes, never planned);
 //   k256x256: 8 waves of 128x64, one workgroup per CU;
-//   k64x64: 4 waves of 16x64, four workgroups per CU (few output rows: 4x the tiles of 128x128).
-enum TileShape : int { k128x128 = 0, k128x256 = 1, k256x128 = 2, k256x256 = 3, k64x64 = 4 };
+//   k64x64: 4 waves of 16x64, four workgroups per CU (few output rows: 4x the tiles of 128x128);
+//   k256x192: 8 waves of 64x96, one workgroup per CU (orthogonalization only).
+enum TileShape : int { k128x128 = 0, k128x256 = 1, k256x128 = 2, k256x256 = 3, k64x64 = 4, k256x192 = 5 };
 inline int tile_rows(int shape) {
-  return shape == k64x64 ? 64 : (shape == k256x128 || shape == k256x256) ? 256 : 128;
+  return shape == k64x64 ? 64 : (shape == k256x128 || shape == k256x256 || shape == k256x192) ? 256 : 128;
 }
 inline int tile_cols(int shape) {
-  return shape == k64x64 ? 64 : (shape == k128x256 || shape == k256x256) ? 256 : 128;
+  return shape == k64x64 ? 64 : shape == k256x192 ? 192 : (shape == k128x256 || shape == k256x256) ? 256 : 128;
 }
+// 64 x 64 tiles have a ring of three stages up to that many of them to a compute unit (three fit; us with two stages and
+// three: 256 tiles of 2048 bytes' contraction 10.1 / 8.2, 528 tiles of 4096 25 / 29).
+constexpr int kDeepPerCu = 2;
 inline int blocks_per_cu(int shape) { return shape == k64x64 ? 4 : shape == k128x128 ? 2 : 1; }
 constexpr int kMaxSplit = 8;
 
@@ -145,6 +149,7 @@ struct MxPlan {
   bool skinny = true;  // few rows: the streaming kernel; else LDS tiles of the shape below
   int64_t rows = 0;    // rows one product is expected to have
   int shape = k128x128;
+  bool deep = false;   // 8-bit integers, 64 x 64 tiles that are all on the card at once: a ring of three stages
   int split_k = 1;     // skinny: waves of a workgroup that split the contraction; else as in GemmPlan
   int64_t tiles_m = 0, tiles_n = 0;
   int64_t grid = 0;
