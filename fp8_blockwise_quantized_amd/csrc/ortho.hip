@@ -7,19 +7,20 @@
 //
 // Rounding.  The products run in 16-bit floats (11 bits) with FP32 accumulation.  Rounding X itself to 11 bits would put
 // noise of all directions into it, and the small singular values' directions are then amplified by a in every step: a
-// gradient of rank 32 in noise came out 2 10^-2 off.  So X is kept as the sum of two halves (22 bits) and the
-// update's product is taken with both.  A, A^2 and b A + c A^2 may be rounded to 11 bits, and X X^T be taken of the
-// first half: an error there is multiplied by X and so stays in X's own directions.  Off by (of the result's norm, five steps)
-// 4 10^-4 for matrices of low rank, 10^-3 for random ones; the result's own BF16 rounding is 1.7 10^-3.  In the last step
-// nothing amplifies any more and the product is taken with the first half alone; in the first, BF16 input fits one half.
+// gradient of rank 32 in noise came out 2 10^-2 off.  So X is kept as the sum of two halves (22 bits), and a X is taken of
+// both.  The products take the first half alone, and A and the polynomial P = b A + c A^2 are rounded to 11 bits: an error
+// of A or P is multiplied by X and stays among X's rows, and P times the second half is what P, whose columns are X's own
+// directions, makes of noise: neither reaches the directions in which X is small.  Off by (of the result's norm, five
+// steps) 5 10^-4 for matrices of low rank, 1.6 10^-3 for random ones (with products of both halves 4 10^-4 and 1.3 10^-3,
+// at twice the work); the result's own BF16 rounding is 1.7 10^-3.
 //
 // Scaling.  Halves hold 6 10^-8 .. 65504; X is held as 2^12 X, A and the polynomial as 2^10 A.  The first X is G times a
 // power of two (exact), the rest of the normalization (a factor in 1 .. 2) enters the first step's epilogues.
 //
-// Layout.  X (first half, rows along n) serves A's product, X^T (both halves, side by side, rows along m) the update's:
-// X^T_new = X^T (b A + c A^2) is a product of rows again.  The update writes both: a patch of accumulators is transposed
-// in registers, eight lanes exchanging 8 x 8 values, so that either goes out in 16-byte stores.  Rows are padded with
-// zeros to whole stages of 64 halves.
+// Layout.  X (first half, rows along n) serves A's product, X^T (rows along m) the update's: X^T_new = X^T P is a product
+// of rows again.  The update writes both: a patch of accumulators is transposed in registers, eight lanes exchanging
+// 8 x 8 values, so that either goes out in 16-byte stores.  The second half lies beside X^T and is replaced where it is
+// read.  Rows are padded with zeros to whole stages of 64 halves.
 //
 // Bound by the matrix pipes (row_gemm.hpp's loop) where the tiles fill the card; a lone matrix's A and A^2 have few tiles and
 // long contractions, which are split, the parts being added up by a second kernel with the same epilogue.
@@ -103,7 +104,8 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(const TIn* __restrict__
 // The first X in both layouts, from tiles of 64 x 64 of G; factor[batch].  tall: G is X^T.
 struct OrthoBuffers {
   uint16_t* x;    // [batch][m][np] first halves
-  uint16_t* xt;   // [batch][n][2 mp] both halves
+  uint16_t* xt;   // [batch][n][mp] first halves
+  uint16_t* low;  // [batch][n][mp] second halves (FP32 input; BF16 fits the first)
   int64_t m, n, mp, np;
 };
 template <typename TIn>
@@ -145,7 +147,8 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
     factor[batch] = finite ? (float)(1.0 / __builtin_amdgcn_frexp_mant(norm)) : __builtin_nanf("");
   // (buffers are padded to whole tiles of 64 along their rows; rows past the matrix are not there)
   uint16_t* x = b.x + (int64_t)batch * b.m * b.np;
-  uint16_t* xt = b.xt + (int64_t)batch * b.n * 2 * b.mp;
+  uint16_t* xt = b.xt + (int64_t)batch * b.n * b.mp;
+  uint16_t* xl = b.low + (int64_t)batch * b.n * b.mp;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t r = r0 + row + 32 * h;
@@ -164,8 +167,8 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
     if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(&low[row + 32 * h][c]) = lo;
     if (r < R) {
       if (tall) {
-        *reinterpret_cast<u32x4*>(xt + r * 2 * b.mp + c0 + c) = hi;
-        if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(xt + r * 2 * b.mp + b.mp + c0 + c) = lo;
+        *reinterpret_cast<u32x4*>(xt + r * b.mp + c0 + c) = hi;
+        if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(xl + r * b.mp + c0 + c) = lo;
       } else {
         *reinterpret_cast<u32x4*>(x + r * b.np + c0 + c) = hi;
       }
@@ -182,11 +185,11 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
     if (tall) {
       *reinterpret_cast<u32x4*>(x + (c0 + i) * b.np + r0 + c) = hi;
     } else {
-      *reinterpret_cast<u32x4*>(xt + (c0 + i) * 2 * b.mp + r0 + c) = hi;
+      *reinterpret_cast<u32x4*>(xt + (c0 + i) * b.mp + r0 + c) = hi;
       if constexpr (sizeof(TIn) == 4) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) lo[k] = low[c + 2 * k][i] | (uint32_t)low[c + 2 * k + 1][i] << 16;
-        *reinterpret_cast<u32x4*>(xt + (c0 + i) * 2 * b.mp + b.mp + r0 + c) = lo;
+        *reinterpret_cast<u32x4*>(xl + (c0 + i) * b.mp + r0 + c) = lo;
       }
     }
   }
@@ -199,8 +202,9 @@ struct OrthoEnd {
   const float* factor;    // of the first step's X (null: 1)
   uint16_t* sym;          // Gram, polynomial: output [batch][m][mp]
   const uint16_t* gram;   // polynomial: A
-  const uint16_t* xt;     // update: X^T as it was, with `halves` halves
-  int halves;
+  const uint16_t* xt;     // update: X^T as it was, and its second half (replaced; not read where it is not there)
+  uint16_t* low;
+  int has_low;
   uint16_t* xt_out;       // update: X^T and X
   uint16_t* x_out;
   uint16_t* out;          // last: BF16 result [batch], rows ldo apart
@@ -270,9 +274,9 @@ __device__ __forceinline__ void ortho_row(const OrthoEnd& e, const v16f (&v)[NI]
       } else {
         u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
         if (m < p.mlim && n < e.mp) {
-          const uint16_t* o = e.xt + (p.batch * e.n + m) * 2 * e.mp + n;
-          hi = *reinterpret_cast<const u32x4*>(o);
-          if (e.halves == 2) lo = *reinterpret_cast<const u32x4*>(o + e.mp);
+          const int64_t at = (p.batch * e.n + m) * e.mp + n;
+          hi = *reinterpret_cast<const u32x4*>(e.xt + at);
+          if (e.has_low) lo = *reinterpret_cast<const u32x4*>(e.low + at);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -296,9 +300,9 @@ __device__ __forceinline__ void ortho_row(const OrthoEnd& e, const v16f (&v)[NI]
             l[i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
           }
           if (m < p.mlim) {
-            uint16_t* o = e.xt_out + (p.batch * e.n + m) * 2 * e.mp;
-            put8(o, n, e.mp, true, d);
-            put8(o + e.mp, n, e.mp, true, l);
+            const int64_t at = (p.batch * e.n + m) * e.mp;
+            put8(e.xt_out + at, n, e.mp, true, d);
+            put8(e.low + at, n, e.mp, true, l);
           }
           transpose8(d, p.lane);
           if (n + turn < p.nlim) put8(e.x_out + (p.batch * e.m + n + turn) * e.np, turned, e.np, true, d);
@@ -453,6 +457,7 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
   float* factor = (float*)(w + p.at_factor);
   uint16_t* x = (uint16_t*)(w + p.at_x);
   uint16_t* xt[2] = {(uint16_t*)(w + p.at_xt[0]), (uint16_t*)(w + p.at_xt[1])};
+  uint16_t* low = (uint16_t*)(w + p.at_low);
   uint16_t* gram = (uint16_t*)(w + p.at_gram);
   uint16_t* poly = (uint16_t*)(w + p.at_poly);
   void* parts = w + p.at_parts;
@@ -461,7 +466,7 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
 
   const dim3 ngrid((unsigned)p.norm_blocks, (unsigned)B);
   const dim3 bgrid((unsigned)((p.C + 63) / 64), (unsigned)((p.R + 63) / 64), (unsigned)B);
-  const OrthoBuffers b{x, xt[0], p.m, p.n, p.mp, p.np};
+  const OrthoBuffers b{x, xt[0], low, p.m, p.n, p.mp, p.np};
   if (gt == 0) {
     hipLaunchKernelGGL(ortho_norm_kernel<uint16_t>, ngrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, wide, norms);
     FP8BQ_TRY(hipGetLastError());
@@ -484,7 +489,8 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     e.factor = first ? factor : nullptr;
     e.gram = gram;
     e.xt = xt[k & 1];
-    e.halves = first && gt == 0 ? 1 : 2;
+    e.low = low;
+    e.has_low = !(first && gt == 0);
     e.xt_out = xt[(k & 1) ^ 1];
     e.x_out = x;
     e.out = (uint16_t*)out;
@@ -504,24 +510,18 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     e.sym = gram;
     FP8BQ_TRY(launch_product<kOrthoGram>(d, e, p.gram, B, parts, st));
     e.factor = nullptr;
-    d.a = d.b = (const uint8_t*)gram;  // b A + c A A
+    d.a = d.b = (const uint8_t*)gram;  // P
     d.lda = d.ldb = 2 * p.mp;
     d.K = 2 * p.mp;
     d.abatch = d.bbatch = 2 * p.m * p.mp;
     e.sym = poly;
     FP8BQ_TRY(launch_product<kOrthoPoly>(d, e, p.poly, B, parts, st));
     e.factor = first ? factor : nullptr;
-    const int halves = last ? 1 : e.halves;
-    d.a = (const uint8_t*)xt[k & 1];
-    d.lda = 4 * p.mp;
+    d.a = (const uint8_t*)xt[k & 1];  // X^T P
+    d.lda = 2 * p.mp;
     d.b = (const uint8_t*)poly;
-    d.ldb = 2 * p.mp;
     d.M = p.n;
-    d.N = p.m;
-    d.K = 2 * p.mp * halves;
-    d.wrap = halves == 2 ? (int)(2 * p.mp / 128) : 0;
-    d.abatch = 4 * p.n * p.mp;
-    d.bbatch = 2 * p.m * p.mp;
+    d.abatch = 2 * p.n * p.mp;
     if (!last)
       FP8BQ_TRY(launch_product<kOrthoUpdate>(d, e, p.update, B, nullptr, st));
     else if (tall)

@@ -64,7 +64,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t R, int64_t C, int cu_count, bool* fi
   if (!*fits) return p;
   p.gram = plan_product(p.m, p.m, p.np / 64, batch, true, cus);
   p.poly = plan_product(p.m, p.m, p.mp / 64, batch, true, cus);
-  p.update = plan_product(p.n, p.m, 2 * p.mp / 64, batch, false, cus);
+  p.update = plan_product(p.n, p.m, p.mp / 64, batch, false, cus);
   const int64_t blocks = cdiv(R * C, 16384), most = cdiv(2048, batch);
   p.norm_blocks = (int)(blocks < most ? blocks : most);
   size_t at = 0;
@@ -77,8 +77,9 @@ OrthoPlan plan_ortho(int64_t batch, int64_t R, int64_t C, int cu_count, bool* fi
   p.at_norms = take(b * p.norm_blocks * 8.0);
   p.at_factor = take(b * 4.0);
   p.at_x = take(b * m * np * 2.0);
-  p.at_xt[0] = take(b * n * mp * 4.0);
-  p.at_xt[1] = take(b * n * mp * 4.0);
+  p.at_xt[0] = take(b * n * mp * 2.0);
+  p.at_xt[1] = take(b * n * mp * 2.0);
+  p.at_low = take(b * n * mp * 2.0);
   p.at_gram = take(b * m * mp * 2.0);
   p.at_poly = take(b * m * mp * 2.0);
   auto parts = [&](const OrthoProduct& q) {

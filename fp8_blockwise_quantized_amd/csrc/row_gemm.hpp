@@ -25,7 +25,6 @@ struct RowDesc {
   int64_t ldb;
   int64_t M, N;
   int64_t K;          // contraction bytes, a multiple of 16
-  int wrap;           // stages after which B's columns begin again (0: never)
   int64_t abatch, bbatch;  // bytes between the matrices of a batch
 };
 
@@ -187,7 +186,7 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
     const int mleft = u.mend - 1 - u.m0, nleft = u.nend - 1 - u.n0;
     const uint32_t lda = (uint32_t)d.lda, ldb = (uint32_t)d.ldb;
     abytes = (uint32_t)(mleft < BM - 1 ? mleft : BM - 1) * lda + (uint32_t)d.K;
-    bbytes = (uint32_t)(nleft < BN - 1 ? nleft : BN - 1) * ldb + (d.wrap ? (uint32_t)d.wrap * 128u : (uint32_t)d.K);
+    bbytes = (uint32_t)(nleft < BN - 1 ? nleft : BN - 1) * ldb + (uint32_t)d.K;
     int el = lane;  // (worked out anew for each unit, as the place in the output)
     asm volatile("" : "+v"(el));
 #pragma unroll
@@ -222,8 +221,7 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
     if (i < AL) {
       dma16(rsrc_of(abase + (int64_t)lkb * 128, abytes - (uint32_t)(lkb * 128)), aoff[i], stg + (wid + NW * i) * 1024);
     } else {
-      const int kb = d.wrap && lkb >= d.wrap ? lkb - d.wrap : lkb;
-      dma16(rsrc_of(bbase + (int64_t)kb * 128, bbytes - (uint32_t)(kb * 128)), boff[i - AL],
+      dma16(rsrc_of(bbase + (int64_t)lkb * 128, bbytes - (uint32_t)(lkb * 128)), boff[i - AL],
             stg + Tile::kB + (wid + NW * (i - AL)) * 1024);
     }
   };

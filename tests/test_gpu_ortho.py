@@ -1,7 +1,7 @@
 """Orthogonalized updates against Newton-Schulz steps in float64.
 
-What the kernels round is stated in their header: X to two halves (22 bits), A and the polynomial to 11 bits, the result to
-BF16 (2^-8).  The same scheme in float64 (emulated below) says how far that takes the result; the kernels round at the same
+What the kernels round is stated in their header: X to two halves (22 bits), of which the products take the first, A and the
+polynomial to 11 bits, the result to BF16 (2^-8).  The same scheme in float64 (emulated below) says how far that takes the result; the kernels round at the same
 places, at other values in the last bit, so they are held to twice the emulation's distance from the exact steps, and each
 element to twelve times its root mean square (a tail of a million roundings).  An error dP of the polynomial moves element
 (i, j) of X by sum_k dP[i, k] X[k, j], which grows with the size of X's column j, so the mean is also taken along each
@@ -37,19 +37,19 @@ def half(t, scale):
     return (t * scale).to(torch.float16).to(F64) / scale
 
 
-def steps_of(g, coefficients, eps=1e-7, emulate=False, bf16_in=False):
+def steps_of(g, coefficients, eps=1e-7, emulate=False):
     out = []
     for x in g.to(F64):
         turned = x.shape[0] > x.shape[1]
         x = x.t() if turned else x
         x = x / (x.square().sum().sqrt() + eps)
-        for i, (a, b, c) in enumerate(coefficients):
+        for a, b, c in coefficients:
             if emulate:
                 hi = half(x, 4096.0)
                 lo = half(x - hi, 4096.0)
                 A = half(hi @ hi.t(), 1024.0)
                 P = half(b * A + c * (A @ A), 1024.0)
-                x = a * (hi + lo) + P @ (hi if i == len(coefficients) - 1 else hi + lo)
+                x = a * (hi + lo) + P @ hi
             else:
                 A = x @ x.t()
                 x = a * x + (b * A + c * (A @ A)) @ x
