@@ -139,6 +139,7 @@ static hipError_t launch_out(const Int8Desc& d, const MxGroups& grp, const MxPla
   const Int8Out o{d.sa, d.sb, d.c, d.ldc, d.past, (d.ldc * (OUT == 0 ? 2 : 4)) % 16 == 0, (int32_t*)ws, (d.N + 3) / 4 * 4};
   switch (p.shape) {
     case k256x256: return launch_tile<256, 256, 2, 4, 2, OUT>(r, o, grp, p, st);
+    case k256x192: return launch_tile<256, 192, 4, 2, 2, OUT>(r, o, grp, p, st);
     case k64x64:
       return p.deep ? launch_tile<64, 64, 2, 2, 3, OUT>(r, o, grp, p, st) : launch_tile<64, 64, 2, 2, 2, OUT>(r, o, grp, p, st);
     default: return launch_tile<128, 128, 2, 2, 2, OUT>(r, o, grp, p, st);

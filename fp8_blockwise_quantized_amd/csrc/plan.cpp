@@ -235,14 +235,18 @@ GemmPlan plan_grouped(int op, int64_t E, int64_t T, int64_t N, int64_t K, int cu
 
 // Time of one 256-long stage for one full round of resident MXFP4 work units, in microseconds, measured on
 // MI355X (8192 x 8192 x 8192 with each tile: 275, 340 and 500 us).
-static double mx_stage_us(int shape) { return shape == k256x256 ? 2.1 : shape == k64x64 ? 0.98 : 1.33; }
+static double mx_stage_us(int shape) {
+  return shape == k256x256 ? 2.1 : shape == k256x192 ? 1.65 : shape == k64x64 ? 0.98 : 1.33;
+}
 
-// Shape, split and grid of the LDS-tiled kernels: nkb stages of 128 contraction bytes, expected rows p.rows.
-static void plan_tiles(MxPlan& p, int64_t E, int64_t M, int64_t N, int64_t nkb, int64_t cus) {
+// Shape, split and grid of the LDS-tiled kernels: nkb stages of 128 contraction bytes, expected rows p.rows; of the first
+// `count` shapes below.  256 x 192 tiles fill the last round where 256 x 256 ones leave it half empty (8 bits, us with 256 x 256 and
+// so: 4099 x 5632 x 2048 63 / 58, 8192 x 2560 x 2048 60 / 53, 3000 x 8000 x 4096 106 / 98).
+static void plan_tiles(MxPlan& p, int64_t E, int64_t M, int64_t N, int64_t nkb, int64_t cus, int count) {
   const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
-  const int shapes[3] = {k256x256, k128x128, k64x64};
+  const int shapes[4] = {k256x256, k128x128, k64x64, k256x192};
   double best = 0.0;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < count; ++i) {
     const int s = shapes[i];
     const int64_t slots = cus * blocks_per_cu(s);
     const double tiles = (double)used * (double)cdiv(p.rows, tile_rows(s)) * (double)cdiv(N, tile_cols(s));
@@ -291,7 +295,7 @@ MxPlan plan_mx(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu_c
     p.grid = units < 16 * cus ? units : 16 * cus;
     return p;
   }
-  plan_tiles(p, E, M, N, cdiv(K, 256), cus);
+  plan_tiles(p, E, M, N, cdiv(K, 256), cus, 3);
   return p;
 }
 
@@ -312,7 +316,7 @@ MxPlan plan_int8(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu
     p.grid = units < 16 * cus ? units : 16 * cus;
     return p;
   }
-  plan_tiles(p, E, M, N, cdiv(K, 128), cus);
+  plan_tiles(p, E, M, N, cdiv(K, 128), cus, 4);
   p.deep = p.shape == k64x64 && used * cdiv(p.rows, 64) * p.tiles_n * p.split_k <= kDeepPerCu * cus;
   return p;
 }

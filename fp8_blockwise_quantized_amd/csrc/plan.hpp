@@ -21,7 +21,7 @@ enum Op : int { kOpFprop = 0, kOpDgrad = 1, kOpWgrad = 2, kOpDgradWt = 3, kOpTen
 //   k128x256 / k256x128: 8 waves of 64x64, one workgroup per CU (tuning shapes, never planned);
 //   k256x256: 8 waves of 128x64, one workgroup per CU;
 //   k64x64: 4 waves of 16x64, four workgroups per CU (few output rows: 4x the tiles of 128x128);
-//   k256x192: 8 waves of 64x96, one workgroup per CU (orthogonalization only).
+//   k256x192: 8 waves of 64x96, one workgroup per CU (8-bit integers and orthogonalization only).
 enum TileShape : int { k128x128 = 0, k128x256 = 1, k256x128 = 2, k256x256 = 3, k64x64 = 4, k256x192 = 5 };
 inline int tile_rows(int shape) {
   return shape == k64x64 ? 64 : (shape == k256x128 || shape == k256x256 || shape == k256x192) ? 256 : 128;
