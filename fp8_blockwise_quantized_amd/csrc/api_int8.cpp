@@ -102,7 +102,7 @@ int fp8bq_quantize_int8(const void* x, fp8bq_in xt, int64_t R, int64_t C, int64_
 }
 
 size_t fp8bq_quantize_int8_t_workspace_size(int64_t R, int64_t C) {
-  return R < 1 || C < 1 || R >= ((int64_t)1 << 31) || C >= ((int64_t)1 << 31)
+  return R < 1 || C < 1 || R >= ((int64_t)1 << 30) || C >= ((int64_t)1 << 30)
              ? 0
              : (size_t)int8_col_chunks(R, C) * (size_t)C * sizeof(float);
 }

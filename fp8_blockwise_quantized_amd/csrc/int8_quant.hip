@@ -130,12 +130,24 @@ static hipError_t launch_rows(const void* x, int64_t R, int64_t C, int64_t ldx, 
   return hipGetLastError();
 }
 
+template <typename TIn>
+static hipError_t launch_rows_any(const void* x, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
+                                  hipStream_t st) {
+  // Few rows: four waves share one, so that its loads are in flight together.
+  if (R <= 2048) return launch_rows<TIn, 4>(x, R, C, ldx, q, ldq, s, st);
+  // (at 64 threads a row, the threads of one launch stay below 2^32)
+  constexpr int64_t kMost = (int64_t)1 << 24;
+  for (int64_t r = 0; r < R; r += kMost) {
+    const int64_t n = R - r < kMost ? R - r : kMost;
+    const hipError_t e = launch_rows<TIn, 1>((const TIn*)x + r * ldx, n, C, ldx, q + r * ldq, ldq, s + r, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_int8_rows(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
                             hipStream_t st) {
-  // Few rows: four waves share one, so that its loads are in flight together.
-  if (R <= 2048)
-    return xt == 0 ? launch_rows<uint16_t, 4>(x, R, C, ldx, q, ldq, s, st) : launch_rows<float, 4>(x, R, C, ldx, q, ldq, s, st);
-  return xt == 0 ? launch_rows<uint16_t, 1>(x, R, C, ldx, q, ldq, s, st) : launch_rows<float, 1>(x, R, C, ldx, q, ldq, s, st);
+  return xt == 0 ? launch_rows_any<uint16_t>(x, R, C, ldx, q, ldq, s, st) : launch_rows_any<float>(x, R, C, ldx, q, ldq, s, st);
 }
 
 // Columns, first pass: maxima of 128 columns over a chunk of `rows` rows, part[chunk][C].

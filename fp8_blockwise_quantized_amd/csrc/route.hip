@@ -436,22 +436,36 @@ static hipError_t launch_route_t(const void* x, int64_t T, int64_t ldx, const Ro
   return hipErrorInvalidValue;
 }
 
+// Tokens of one launch: at 64 threads each, its threads stay below 2^32.
+constexpr int64_t kLaunchTokens = (int64_t)1 << 24;
+
 hipError_t launch_route(const void* x, int xt, int64_t T, int64_t ldx, const RouteHow& how, const float* bias,
                         int32_t* experts, float* weights, hipStream_t st) {
-  return xt == 0 ? launch_route_t<uint16_t>(x, T, ldx, how, bias, experts, weights, st)
-                 : launch_route_t<float>(x, T, ldx, how, bias, experts, weights, st);
+  for (int64_t t = 0; t < T; t += kLaunchTokens) {
+    const int64_t n = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+    const hipError_t e =
+        xt == 0 ? launch_route_t<uint16_t>((const uint16_t*)x + t * ldx, n, ldx, how, bias, experts + t * how.k, weights + t * how.k, st)
+                : launch_route_t<float>((const float*)x + t * ldx, n, ldx, how, bias, experts + t * how.k, weights + t * how.k, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_route_backward(const float* dw, const void* x, int xt, int64_t T, int64_t ldx, const RouteHow& how,
                                  const int32_t* experts, void* dx, int64_t lddx, hipStream_t st) {
-  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
-  if (xt == 0)
-    hipLaunchKernelGGL(route_backward_kernel<uint16_t>, grid, block, 0, st, dw, (const uint16_t*)x, T, ldx, how, experts,
-                       (uint16_t*)dx, lddx);
-  else
-    hipLaunchKernelGGL(route_backward_kernel<float>, grid, block, 0, st, dw, (const float*)x, T, ldx, how, experts,
-                       (float*)dx, lddx);
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kLaunchTokens) {
+    const int64_t n = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+    const dim3 grid((unsigned)((n + 3) / 4)), block(256);
+    if (xt == 0)
+      hipLaunchKernelGGL(route_backward_kernel<uint16_t>, grid, block, 0, st, dw + t * how.k, (const uint16_t*)x + t * ldx, n, ldx,
+                         how, experts + t * how.k, (uint16_t*)dx + t * lddx, lddx);
+    else
+      hipLaunchKernelGGL(route_backward_kernel<float>, grid, block, 0, st, dw + t * how.k, (const float*)x + t * ldx, n, ldx, how,
+                         experts + t * how.k, (float*)dx + t * lddx, lddx);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp8bq

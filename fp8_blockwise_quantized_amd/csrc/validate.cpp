@@ -651,8 +651,8 @@ int validate_int8_quant(const void* x, int xt, int64_t R, int64_t C, int64_t ldx
     *empty = true;
     return kOk;
   }
-  const int64_t kMost = (int64_t)1 << 31;
-  if (R >= kMost || C >= kMost || (R / 128 + 1) * (C / 128 + 1) >= kMost) return kErrShape;  // tiles of one launch
+  const int64_t kMost = (int64_t)1 << 30;
+  if (R >= kMost || C >= kMost || (columns && (R / 128 + 1) * (C / 128 + 1) >= ((int64_t)1 << 24))) return kErrShape;  // of one launch
   const Mat mx{x, R, C, ldx, in_esize(xt)};
   const Mat mq = columns ? Mat{q, C, (R + 15) / 16 * 16, ldq, 1} : Mat{q, R, C, ldq, 1};
   const int64_t n = columns ? C : R;

@@ -69,7 +69,7 @@ def test_empty_calls_succeed():
 def test_quantizer_refusals():
     for f in (rows, cols):
         assert f(xt=2) == f(xt=-1) == DTYPE
-        assert f(R=-1) == f(C=-16) == f(C=K + 4) == f(R=1 << 31) == SHAPE
+        assert f(R=-1) == f(C=-16) == f(C=K + 4) == f(R=1 << 30) == f(C=1 << 30) == f(R=1 << 31) == SHAPE
         assert f(x=NUL) == f(q=NUL) == f(s=NUL) == NULL
         assert f(x=P(0, 8)) == f(q=P(1, 4)) == f(s=P(2, 4)) == ALIGN
         assert f(ldx=K - 8) == f(ldx=K + 1) == f(ldq=K - 16) == f(ldq=313) == LD
