@@ -114,35 +114,30 @@ __global__ __launch_bounds__(kQRowThreads) void int8_rows_kernel(const TIn* __re
   }
 }
 
-template <typename TIn, int WPR>
+template <typename TIn, int WPR, int CH>
 static hipError_t launch_rows(const void* x, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
                               hipStream_t st) {
   constexpr int RPB = kQRowThreads / 64 / WPR;
-  const dim3 grid((unsigned)((R + RPB - 1) / RPB)), block(kQRowThreads);
-  const int64_t chunks = (C + 512 * WPR - 1) / (512 * WPR);
-  const TIn* xp = reinterpret_cast<const TIn*>(x);
-  if (chunks <= 4)
-    hipLaunchKernelGGL((int8_rows_kernel<TIn, WPR, 4>), grid, block, 0, st, xp, R, C, ldx, q, ldq, s);
-  else if (chunks <= 12)
-    hipLaunchKernelGGL((int8_rows_kernel<TIn, WPR, 12>), grid, block, 0, st, xp, R, C, ldx, q, ldq, s);
-  else
-    hipLaunchKernelGGL((int8_rows_kernel<TIn, WPR, 0>), grid, block, 0, st, xp, R, C, ldx, q, ldq, s);
-  return hipGetLastError();
-}
-
-template <typename TIn>
-static hipError_t launch_rows_any(const void* x, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
-                                  hipStream_t st) {
-  // Few rows: four waves share one, so that its loads are in flight together.
-  if (R <= 2048) return launch_rows<TIn, 4>(x, R, C, ldx, q, ldq, s, st);
-  // (at 64 threads a row, the threads of one launch stay below 2^32)
-  constexpr int64_t kMost = (int64_t)1 << 24;
+  constexpr int64_t kMost = (int64_t)1 << 22;  // rows of a launch: its threads stay below 2^32
   for (int64_t r = 0; r < R; r += kMost) {
     const int64_t n = R - r < kMost ? R - r : kMost;
-    const hipError_t e = launch_rows<TIn, 1>((const TIn*)x + r * ldx, n, C, ldx, q + r * ldq, ldq, s + r, st);
+    hipLaunchKernelGGL((int8_rows_kernel<TIn, WPR, CH>), dim3((unsigned)((n + RPB - 1) / RPB)), dim3(kQRowThreads), 0, st,
+                       (const TIn*)x + r * ldx, n, C, ldx, q + r * ldq, ldq, s + r);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// A wave holds rows of up to 2048 elements, four waves longer ones (us with one wave and four: 16384 x 512 6.3 / 14, x 2048
+// 17 / 19, x 4096 34 / 30, x 11264 162 / 103; 512 x 2048 2.9 / 2.9, x 5632 4.7 / 3.4).
+template <typename TIn>
+static hipError_t launch_rows_any(const void* x, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
+                                  hipStream_t st) {
+  if (C <= 4 * 512) return launch_rows<TIn, 1, 4>(x, R, C, ldx, q, ldq, s, st);
+  if (C <= 4 * 2048) return launch_rows<TIn, 4, 4>(x, R, C, ldx, q, ldq, s, st);
+  if (C <= 12 * 2048) return launch_rows<TIn, 4, 12>(x, R, C, ldx, q, ldq, s, st);
+  return launch_rows<TIn, 4, 0>(x, R, C, ldx, q, ldq, s, st);
 }
 
 hipError_t launch_int8_rows(const void* x, int xt, int64_t R, int64_t C, int64_t ldx, uint8_t* q, int64_t ldq, float* s,

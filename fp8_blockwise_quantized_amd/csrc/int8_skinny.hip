@@ -5,8 +5,14 @@
 // C row l % 16 and columns 4 (l / 16) .. +3.  A wave owns 16 columns and reads 128 bytes of each of its B rows at a
 // time; the waves that share them split the contraction and join their integer sums in LDS.
 //
-// A in BF16 or FP32: the workgroup quantizes its rows itself, into LDS (the scale needs the whole row, so all its
-// threads look for the maxima first), while its first weights are on their way; no launch, no workspace.
+// A in BF16 or FP32, few values of it and one product: the workgroup quantizes the rows itself, into LDS (the scale needs
+// the whole row, so all its threads look for the maxima first), while its first weights are on their way.  That is spared
+// a launch, and costs every workgroup about 0.3 us for 4096 values.
+//
+// Measured (us, weights in the caches; an empty launch takes 2): one row, 2048 x 2048 from codes 3.9, from BF16 5.1;
+// 11264 x 2048 6.4 and 7.8 (3.6 and 3.0 TB/s); 16 rows, 2048 x 2048 4.5.  Codes and scales are asked for with the weights,
+// ahead of the products (behind them one row of 11264 x 2048 took 7.6), and registers are kept for three workgroups a
+// compute unit (from BF16 9.2 with two).
 #include "group_table.hpp"
 #include "int8_common.hpp"
 #include "launch.hpp"
@@ -41,14 +47,13 @@ __device__ __forceinline__ void int8_store4(void* c, int64_t ldc, int64_t m, int
 // operand read fall on different banks.
 __host__ __device__ inline int64_t skinny_row_bytes(int64_t K) { return (K + 127) / 128 * 128 + 16; }
 
-// Codes and scales of rows m0 .. m0 + rows - 1 (zeros from mend on), all threads of the workgroup.
+// Codes and scales of the first `rows` rows (zeros from M on), all threads of the workgroup.
 template <typename TA>
-__device__ __forceinline__ void quantize_rows(const Int8Desc& d, int64_t m0, int64_t mend, int rows, uint8_t* qx,
-                                              float* rs, uint32_t* amax) {
+__device__ __forceinline__ void quantize_rows(const Int8Desc& d, int rows, uint8_t* qx, float* rs, uint32_t* amax) {
   const int t = threadIdx.x, tpr = kSkinnyThreads / rows, row = t / tpr, c0 = 8 * (t % tpr);
-  const int64_t rb = skinny_row_bytes(d.K), m = m0 + row;
-  const bool live = m < mend;
-  const TA* x = reinterpret_cast<const TA*>(d.a) + (live ? m : m0) * d.lda;
+  const int64_t rb = skinny_row_bytes(d.K);
+  const bool live = row < d.M;
+  const TA* x = reinterpret_cast<const TA*>(d.a) + (live ? row : 0) * d.lda;
   if (t < 16) amax[t] = 0;
   __syncthreads();
   uint32_t a = 0;
@@ -77,7 +82,7 @@ __device__ __forceinline__ void quantize_rows(const Int8Desc& d, int64_t m0, int
 
 // ks: waves that split the contraction (a power of two up to 8); rows: of A in LDS (unused with codes).
 template <typename TA, int OUT, bool GROUPED>
-__global__ __launch_bounds__(kSkinnyThreads, 4) void int8_skinny_kernel(Int8Desc d, MxGroups grp, int ks, int rows) {
+__global__ __launch_bounds__(kSkinnyThreads, 6) void int8_skinny_kernel(Int8Desc d, MxGroups grp, int ks, int rows) {
   extern __shared__ __attribute__((aligned(16))) uint8_t qx[];
   __shared__ int part[kSkinnyWaves][4][64];
   __shared__ float rs[16];
@@ -102,7 +107,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void int8_skinny_kernel(Int8Desc
     total = tiles_n * (uint32_t)((d.M + 15) / 16);
   }
 
-  int64_t held = -1;  // first of the rows in LDS (changed behind a barrier that ends all reads of the ones before)
+  bool held = false;  // the rows' codes are in LDS
   for (uint32_t u = blockIdx.x; u < total; u += gridDim.x) {
     int64_t m0 = 0, mend = d.M, nbase = 0;
     uint32_t w = u;
@@ -120,13 +125,25 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void int8_skinny_kernel(Int8Desc
     auto bload = [&](int64_t k) { return *reinterpret_cast<const v4i*>(brow + (k < d.K ? k : d.K - 16)); };
     const int64_t k0 = (int64_t)phase * 128 + 16 * g, step = (int64_t)ks * 128;
     v4i b[2] = {bload(k0), bload(k0 + 64)};
-    if constexpr (FUSED) {
-      if (held != m0) {
-        quantize_rows<TA>(d, m0, mend, rows, qx, rs, amax);
-        held = m0;
-      }
-    }
     const bool mine = m < mend;
+    const uint8_t* arow = reinterpret_cast<const uint8_t*>(d.a) + (mine ? m : mend - 1) * d.lda;  // (codes)
+    auto aload = [&](int64_t k) { return *reinterpret_cast<const v4i*>(arow + (k < d.K ? k : d.K - 16)); };
+    v4i ca[2];
+    float sa = 0.0f, sb[4];
+    if constexpr (!FUSED) {
+      ca[0] = aload(k0);
+      ca[1] = aload(k0 + 64);
+      sa = d.sa[mine ? m : mend - 1];
+    }
+    if constexpr (FUSED) {
+      if (!held) quantize_rows<TA>(d, rows, qx, rs, amax);
+      held = true;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {  // (here, so that the end does not wait for them)
+      const int64_t n = nt + 4 * g + r;
+      sb[r] = d.sb[nbase + (n < d.N ? n : d.N - 1)];
+    }
     v4i acc = {0, 0, 0, 0};
     for (int64_t k = k0; k - 16 * g < d.K; k += step) {
       const v4i b0 = b[0], b1 = b[1];
@@ -140,7 +157,8 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void int8_skinny_kernel(Int8Desc
         if constexpr (FUSED) {
           if (r16 < rows) a[h] = *reinterpret_cast<const v4i*>(qx + r16 * rb + at);  // (zeros from K on)
         } else {
-          if (mine && at < d.K) a[h] = *reinterpret_cast<const v4i*>(reinterpret_cast<const uint8_t*>(d.a) + m * d.lda + at);
+          if (at < d.K) a[h] = ca[h];
+          ca[h] = aload(at + step);
         }
       }
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0, a[0], acc, 0, 0, 0);
@@ -158,13 +176,10 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void int8_skinny_kernel(Int8Desc
       __syncthreads();
     }
     if (phase == 0 && mine && nt < d.N) {
-      const float sa = FUSED ? rs[r16] : d.sa[m];
+      if constexpr (FUSED) sa = rs[r16];
       v4f y;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t n = nt + 4 * g + r;
-        y[r] = (float)acc[r] * sa * d.sb[nbase + (n < d.N ? n : d.N - 1)];
-      }
+      for (int r = 0; r < 4; ++r) y[r] = (float)acc[r] * sa * sb[r];
       int8_store4<OUT>(d.c, d.ldc, m, nt + 4 * g, d.N, y);
     }
   }
@@ -175,8 +190,7 @@ static hipError_t launch_one(const Int8Desc& d, const MxGroups& grp, const MxPla
   int rows = 1;
   size_t lds = 0;
   if constexpr (!std::is_same_v<TA, uint8_t>) {
-    const int64_t most = GROUPED || d.M > 16 ? 16 : d.M;
-    while (rows < most) rows *= 2;
+    while (rows < d.M) rows *= 2;
     lds = (size_t)rows * (size_t)skinny_row_bytes(d.K);
   }
   hipLaunchKernelGGL((int8_skinny_kernel<TA, OUT, GROUPED>), dim3((unsigned)p.grid), dim3(kSkinnyThreads), lds, st, d, grp,
@@ -186,8 +200,8 @@ static hipError_t launch_one(const Int8Desc& d, const MxGroups& grp, const MxPla
 
 template <typename TA>
 static hipError_t launch_out(const Int8Desc& d, const MxGroups& grp, const MxPlan& p, hipStream_t st) {
-  if (grp.offsets) return d.out_t == 0 ? launch_one<TA, 0, true>(d, grp, p, st) : launch_one<TA, 1, true>(d, grp, p, st);
-  if constexpr (std::is_same_v<TA, uint8_t>) {  // (only the dense product of codes is added to the output)
+  if constexpr (std::is_same_v<TA, uint8_t>) {  // (what is quantized here is dense and not added to the output)
+    if (grp.offsets) return d.out_t == 0 ? launch_one<TA, 0, true>(d, grp, p, st) : launch_one<TA, 1, true>(d, grp, p, st);
     if (d.out_t == 2) return launch_one<TA, 2, false>(d, grp, p, st);
   }
   return d.out_t == 0 ? launch_one<TA, 0, false>(d, grp, p, st) : launch_one<TA, 1, false>(d, grp, p, st);

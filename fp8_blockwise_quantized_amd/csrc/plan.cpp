@@ -240,8 +240,8 @@ static double mx_stage_us(int shape) {
 }
 
 // Shape, split and grid of the LDS-tiled kernels: nkb stages of 128 contraction bytes, expected rows p.rows; of the first
-// `count` shapes below.  256 x 192 tiles fill the last round where 256 x 256 ones leave it half empty (8 bits, us with 256 x 256 and
-// so: 4099 x 5632 x 2048 63 / 58, 8192 x 2560 x 2048 60 / 53, 3000 x 8000 x 4096 106 / 98).
+// `count` shapes below.  256 x 192 tiles fill the last round where 256 x 256 ones leave it half empty (8 bits, us with
+// 256 x 256 and so: 4099 x 5632 x 2048 63 / 58, 8192 x 2560 x 2048 60 / 53, 3000 x 8000 x 4096 106 / 98).
 static void plan_tiles(MxPlan& p, int64_t E, int64_t M, int64_t N, int64_t nkb, int64_t cus, int count) {
   const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
   const int shapes[4] = {k256x256, k128x128, k64x64, k256x192};
@@ -304,14 +304,19 @@ MxPlan plan_int8(bool linear, int64_t E, int64_t M, int64_t N, int64_t K, int cu
   const int64_t cus = cu_count > 0 ? cu_count : 256;
   const int64_t used = E == 0 ? 1 : (M < E ? (M > 0 ? M : 1) : E);
   p.rows = cdiv(M, used);
-  const int64_t tiles = used * cdiv(N, 16);
-  p.skinny = M <= 16 && tiles <= 1536;
+  // Few rows on few weights: the kernel without LDS staging.  From codes (us; the tiled kernel second): one row, N = 11264
+  // and K = 2048 6.4 / 7.9, 22528 x 2048 9.8 / 10.7, 45056 x 2048 16.9 / 16.1; 16 rows, 2048 x 2048 4.6 / 7.7, 2048 x 3952
+  // 5.2 / 8.1, 11264 x 2048 8.3 / 7.9, 2048 x 11264 12.1 / 10.1.
+  p.skinny = M <= 16 && used * N * K <= (p.rows <= 4 ? 48000000 : 20000000);
   if (p.skinny) {
-    int64_t rows = 1;  // that a workgroup keeps in LDS when it quantizes them itself
-    while (rows < (E == 0 ? M : 16)) rows *= 2;
-    p.fused = linear && rows * (K + 144) <= 65536;
+    // A workgroup quantizes the rows itself while that costs less than the quantizer's launch (us, so and with a launch): one
+    // row, 2048 x 2048 5.1 / 6.0, 11264 x 2048 7.8 / 8.5, 2048 x 11264 9.7 / 12.2; 2048 x 2048, 8 rows 6.5 / 6.6, 16 rows
+    // 8.2 / 6.9; 8 rows of 8 experts, 1408 x 2048 each, 16.2 / 9.9.
+    p.fused = linear && E == 0 && M * K <= 12288;
+    // Waves that share 16 columns: eight, or as many as there are stages, or what leaves four workgroups a compute unit (one
+    // row, 22528 x 2048 with eight and four 11.1 / 9.8; 11264 x 2048 6.4 / 7.5).
     p.split_k = 8;
-    while (p.split_k > 1 && p.split_k > cdiv(K, 128)) p.split_k /= 2;
+    while (p.split_k > 1 && (p.split_k > cdiv(K, 128) || used * cdiv(N, 8 / p.split_k * 16) > 4 * cus)) p.split_k /= 2;
     const int64_t units = used * cdiv(N, 8 / p.split_k * 16);
     p.grid = units < 16 * cus ? units : 16 * cus;
     return p;

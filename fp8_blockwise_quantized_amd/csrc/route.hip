@@ -10,8 +10,9 @@
 // runs at FP32's rate on this card, so what it costs is registers.
 //
 // Bound by instructions: 16384 tokens of 256 experts are 17 MB, 4 us at the copy's rate, and some 100 wave instructions
-// a token for scores and as many for the choice.  A token is shared by 16 lanes (many tokens) or 64 (few, where latency
-// counts).  The lanes are dealt to the groups first, so that a group's score is a reduction over neighbouring lanes; a
+// a token for scores and as many for the choice (8 of 256 sigmoid scores with a bias, in 8 groups of which 4 stay, 17.2 us; 8 of
+// 256 softmax scores 9.0; 2 of 96 in BF16 at 8192 tokens 5.0; a call of few tokens 3 to 6, a launch's 2 and one pass of
+// dependent steps).  A token is shared by 16 lanes (many tokens) or 64 (few, where latency counts).  The lanes are dealt to the groups first, so that a group's score is a reduction over neighbouring lanes; a
 // lane holds V consecutive experts of its group.  A key is c with the index in place of its last nine bits (key_of), so
 // keys are distinct, one maximum over the lanes names the winner, and the winner alone clears its slot.
 #include "device_common.hpp"
@@ -418,9 +419,13 @@ static hipError_t launch_route_as(const void* x, int64_t T, int64_t ldx, const R
 template <typename TIn>
 static hipError_t launch_route_t(const void* x, int64_t T, int64_t ldx, const RouteHow& how, const float* bias,
                                  int32_t* experts, float* weights, hipStream_t st) {
-  // 16 lanes a token once there are tokens enough to fill the card with them, and where the experts fit its slots.
+  // 16 lanes a token where a lane has four experts at most, or once the tokens fill the card, and where the experts fit its
+  // 16 slots (us with 16 lanes and 64: 64 experts, 64 tokens 3.3 / 3.9, 16384 tokens 4.7 / 10.6; 96 experts, 2048 tokens
+  // 4.2 / 3.8, 8192 tokens 5.0 / 6.4; 256 sigmoid scores in 8 groups, 64 tokens 9.3 / 5.6, 4096 9.7 / 8.5, 8192 12.0 / 13.4,
+  // 16384 17.2 / 22.3).
   const int glog = log2_up(how.groups), per = how.experts / how.groups;
-  const bool narrow = T > 2048 && how.k <= 16 && glog <= 4 && per <= 16 << (4 - glog);
+  const bool fits = how.k <= 16 && glog <= 4 && per <= 16 << (4 - glog);
+  const bool narrow = fits && (T > 4096 || per <= 4 << (4 - glog));
   RouteArgs a{how, (narrow ? 4 : 6) - glog, per, 0};
   const int need = (per + (1 << a.lanes_log2) - 1) >> a.lanes_log2;
   const int v = 1 << log2_up(need);

@@ -116,9 +116,9 @@ def test_grouped_products(counts, N, K):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(1, 70, 65392), (16, 70, 3952), (9, 70, 3968)])
-def test_rows_that_fill_the_local_memory(M, N, K):
-    """The most that a workgroup quantizes for itself (64 KB of codes), and one step more."""
+@pytest.mark.parametrize("M,N,K", [(1, 70, 12288), (1, 70, 12304), (3, 70, 4096), (1, 70, 65392), (16, 70, 3952)])
+def test_rows_quantized_in_the_product(M, N, K):
+    """The longest rows that a workgroup quantizes for itself, and longer ones."""
     say("int8 skinny", M, N, K)
     _, _, w, sw = operands(M, 2 * N, K)
     x = torch.randn(M, K, device="cuda")
