@@ -1,9 +1,11 @@
 // Quantizers of the 8-bit linear layer: rows (a scale for each token) and columns, transposed (a scale for each channel
 // over all the tokens: the operands of the products that contract over the tokens).  The rule is in int8_common.hpp.
 //
-// Bound by memory.  Rows: a row's values stay in registers between the maximum and the codes, so x is read once.
-// Columns: the maximum of a column needs all rows, so x is read twice, by column blocks of 128; the first pass
-// leaves the maxima of each chunk of rows, the second joins them.
+// Bound by memory.  Rows: a row's values stay in registers between the maximum and the codes, so x is read once (16384 x
+// 2048 BF16 17 us, 5.9 TB/s; 16384 x 11264 102 us, 5.4).  Columns: the maximum of a column needs all rows, so x is
+// read twice, by column blocks of 128; the first pass leaves the maxima of each chunk of rows, the second joins them
+// (4099 x 5632 BF16 9 + 14 us, of which 11 are the 69 MB at the copy's rate that one read of x and the codes need; the second
+// read comes from the caches).
 #include "int8_common.hpp"
 #include "launch.hpp"
 

@@ -22,8 +22,13 @@
 // 8 x 8 values, so that either goes out in 16-byte stores.  The second half lies beside X^T and is replaced where it is
 // read.  Rows are padded with zeros to whole stages of 64 halves.
 //
-// Bound by the matrix pipes (row_gemm.hpp's loop) where the tiles fill the card; a lone matrix's A and A^2 have few tiles and
-// long contractions, which are split, the parts being added up by a second kernel with the same epilogue.
+// Bound by row_gemm.hpp's loop where the tiles fill the card (matrix pipes busy 61% of the cycles, the bare instruction
+// 1.68 PFLOP/s); a lone matrix's A and A^2 have few tiles and long contractions, which are split, the parts being
+// added up by a second kernel with the same epilogue.  Measured, five steps (us): 32 of 1408 x 2048 4120 (a step: A 190,
+// P 155, update 450, 0.58 to 0.68 PFLOP/s of what is computed; before them norm 39 and first X 90, 4.1 TB/s), 11264 x 2048
+// FP32 1226 (57 + 14, 24, 150; 22 and 54; unsplit 1283 with BF16), 8 of 512 x 384 110 (17 launches that wait for each other,
+// 5 to 10 each).  The update's tile shape hardly matters (11264 x 2048 with 256 x 192, 128 x 128, 64 x 64 and 256 x 256:
+// 1198, 1195, 1362, 1302; 32 of 1408 x 2048: 4328, 4194, 4985, 4108).
 #include <cmath>
 
 #include "launch.hpp"

@@ -5,7 +5,11 @@
 // Layout.  As the MXFP4 product: a stage holds 128 contraction bytes of the tile's rows of A and B and arrives by
 // direct global->LDS loads into a ring of two stages (three in 64 x 64 tiles that are all on the card at once, where a
 // stage is shorter than memory's answer takes: 64 x 2048 x 2048 in 8 bits 9.8 -> 7.9 us, 512 x 2048 x 2048 10.2 -> 8.3),
-// whose loads go out between the last MFMAs of the stage that held the slot; 16-byte chunks are XOR-swizzled by row; workgroups are persistent and the ring runs on across tiles.
+// whose loads go out between the last MFMAs of the stage that held the slot; 16-byte chunks are XOR-swizzled by row (no
+// bank conflicts); workgroups are persistent and the ring runs on across tiles.
+// Tried on the 256 x 256 tile and not better: four waves of 128 x 128 with their sums in accumulation registers, rings of
+// four and eight shorter stages, LDS reads spread between the MFMAs, staggered workgroups, not waiting for a tile's stores;
+// touching the lines of a stage ahead of its loads cost 10%.
 // A contraction that ends inside a stage: chunks past its end get an offset past the buffer's end, which reads zeros.
 #pragma once
 

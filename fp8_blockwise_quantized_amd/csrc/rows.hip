@@ -3,6 +3,11 @@
 //
 // All of it moves bytes; nothing here has arithmetic to speak of.  Every sum runs in a fixed order (a token's choices
 // in theirs, a dot product over the threads in theirs), so results do not change from call to call.
+//
+// Measured, 16384 tokens of 2048 BF16 values with two choices each on 64 experts (us): sort 5 + 9, gather 41 (201 MB, 4.9 TB/s),
+// combine 40 to 48 (as much), its backward 55 (328 MB, 6.0 TB/s; a streaming copy does 6.1).  Five tokens with six
+// choices: 2.8, 2.7 and 4.0, a launch and its latency.  A workgroup takes a token (or a row of the output), so that its
+// choices' rows are read and summed in registers and written once.
 #include "group_table.hpp"
 #include "launch.hpp"
 #include "quant_common.hpp"
