@@ -231,99 +231,130 @@ __device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, 
   }
 }
 
-// STEP of one row of patches: v[j][8 q + i] is row m, column n + 32 j + 16 q + i of the product.
-template <int STEP, int NI>
-__device__ __forceinline__ void ortho_row(const OrthoEnd& e, const v16f (&v)[NI], const RowPlace& p, int64_t m) {
-  const float f = e.factor ? e.factor[p.batch] : 1.0f;
+// What a patch's end reads: A (polynomial), or X^T as it was and its second half (update).
+struct OrthoOld {
+  u32x4 hi[2], lo[2];
+};
+template <int STEP>
+__device__ __forceinline__ void ortho_load(const OrthoEnd& e, const RowPlace& p, int64_t m, int64_t n0, OrthoOld& o) {
+  if constexpr (STEP == kOrthoGram) return;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int64_t n = n0 + 16 * q;
+    o.hi[q] = o.lo[q] = (u32x4){0, 0, 0, 0};
+    if (m < p.mlim && n < e.mp) {
+      if constexpr (STEP == kOrthoPoly) {
+        o.hi[q] = *reinterpret_cast<const u32x4*>(e.gram + (p.batch * e.m + m) * e.mp + n);
+      } else {
+        const int64_t at = (p.batch * e.n + m) * e.mp + n;
+        o.hi[q] = *reinterpret_cast<const u32x4*>(e.xt + at);
+        if (e.has_low) o.lo[q] = *reinterpret_cast<const u32x4*>(e.low + at);
+      }
+    }
+  }
+}
+
+// STEP of one patch: v[8 q + i] is row m, column n0 + 16 q + i of the product.
+template <int STEP>
+__device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, const RowPlace& p, int64_t m, int64_t n0, float f,
+                                            const OrthoOld& old) {
   const int64_t turned = m - (p.lane & 7);         // first of the eight rows that come together, and the lane's
   const int turn = p.lane & 7;                     // column among the eight after the turn
 #pragma unroll
-  for (int j = 0; j < NI; ++j)
+  for (int q = 0; q < 2; ++q) {
+    const int64_t n = n0 + 16 * q;
+    float y[8];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int64_t n = p.n + 32 * j + 16 * q;
-      float y[8];
+    for (int i = 0; i < 8; ++i) y[i] = v[8 * q + i];
+    uint32_t d[4];
+    if constexpr (STEP == kOrthoGram || STEP == kOrthoPoly) {
+      const int64_t size = e.m * e.mp;
+      if constexpr (STEP == kOrthoGram) {
+        const float s = f * f * (kScaleA / (kScaleX * kScaleX));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = v[j][8 * q + i];
-      uint32_t d[4];
-      if constexpr (STEP == kOrthoGram || STEP == kOrthoPoly) {
-        const int64_t size = e.m * e.mp;
-        if constexpr (STEP == kOrthoGram) {
-          const float s = f * f * (kScaleA / (kScaleX * kScaleX));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] *= s;
-        } else {
-          u32x4 w = {0, 0, 0, 0};
-          if (m < p.mlim && n < e.mp) w = *reinterpret_cast<const u32x4*>(e.gram + p.batch * size + m * e.mp + n);
-          const float s = e.c * (1.0f / kScaleA);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            unpack_f16x2(w[i], lo, hi);
-            y[2 * i] = __builtin_fmaf(e.b, lo, s * y[2 * i]);
-            y[2 * i + 1] = __builtin_fmaf(e.b, hi, s * y[2 * i + 1]);
-          }
-        }
-        if (!p.whole) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
-        uint16_t* o = e.sym + p.batch * size;
-        if (m < p.mlim) put8(o + m * e.mp, n, e.mp, true, d);
-        if (p.mirror) {
-          transpose8(d, p.lane);
-          if (n + turn < p.nlim) put8(o + (n + turn) * e.mp, turned, e.mp, true, d);
-        }
+        for (int i = 0; i < 8; ++i) y[i] *= s;
       } else {
-        u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-        if (m < p.mlim && n < e.mp) {
-          const int64_t at = (p.batch * e.n + m) * e.mp + n;
-          hi = *reinterpret_cast<const u32x4*>(e.xt + at);
-          if (e.has_low) lo = *reinterpret_cast<const u32x4*>(e.low + at);
-        }
+        const float s = e.c * (1.0f / kScaleA);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float h0, h1, l0, l1;
-          unpack_f16x2(hi[i], h0, h1);
-          unpack_f16x2(lo[i], l0, l1);
-          y[2 * i] = f * __builtin_fmaf(e.a, h0 + l0, y[2 * i] * (1.0f / kScaleA));
-          y[2 * i + 1] = f * __builtin_fmaf(e.a, h1 + l1, y[2 * i + 1] * (1.0f / kScaleA));
+          float lo, hi;
+          unpack_f16x2(old.hi[q][i], lo, hi);
+          y[2 * i] = __builtin_fmaf(e.b, lo, s * y[2 * i]);
+          y[2 * i + 1] = __builtin_fmaf(e.b, hi, s * y[2 * i + 1]);
         }
-        if (!p.whole) {
+      }
+      if (!p.whole) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
+        for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
+      uint16_t* o = e.sym + p.batch * size;
+      if (m < p.mlim) put8(o + m * e.mp, n, e.mp, true, d);
+      if (p.mirror) {
+        transpose8(d, p.lane);
+        if (n + turn < p.nlim) put8(o + (n + turn) * e.mp, turned, e.mp, true, d);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float h0, h1, l0, l1;
+        unpack_f16x2(old.hi[q][i], h0, h1);
+        unpack_f16x2(old.lo[q][i], l0, l1);
+        y[2 * i] = f * __builtin_fmaf(e.a, h0 + l0, y[2 * i] * (1.0f / kScaleA));
+        y[2 * i + 1] = f * __builtin_fmaf(e.a, h1 + l1, y[2 * i + 1] * (1.0f / kScaleA));
+      }
+      if (!p.whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
+      }
+      if constexpr (STEP == kOrthoUpdate) {
+        uint32_t l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float h0, h1;
+          d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
+          unpack_f16x2(d[i], h0, h1);
+          l[i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
         }
-        if constexpr (STEP == kOrthoUpdate) {
-          uint32_t l[4];
+        if (m < p.mlim) {
+          const int64_t at = (p.batch * e.n + m) * e.mp;
+          put8(e.xt_out + at, n, e.mp, true, d);
+          put8(e.low + at, n, e.mp, true, l);
+        }
+        transpose8(d, p.lane);
+        if (n + turn < p.nlim) put8(e.x_out + (p.batch * e.m + n + turn) * e.np, turned, e.np, true, d);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float h0, h1;
-            d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
-            unpack_f16x2(d[i], h0, h1);
-            l[i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
-          }
-          if (m < p.mlim) {
-            const int64_t at = (p.batch * e.n + m) * e.mp;
-            put8(e.xt_out + at, n, e.mp, true, d);
-            put8(e.low + at, n, e.mp, true, l);
-          }
-          transpose8(d, p.lane);
-          if (n + turn < p.nlim) put8(e.x_out + (p.batch * e.m + n + turn) * e.np, turned, e.np, true, d);
+        for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(y[2 * i] * (1.0f / kScaleX), y[2 * i + 1] * (1.0f / kScaleX));
+        uint16_t* o = e.out + p.batch * e.obatch;
+        if constexpr (STEP == kOrthoLast) {
+          if (m < p.mlim) put8(o + m * e.ldo, n, e.m, e.vec != 0, d);
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(y[2 * i] * (1.0f / kScaleX), y[2 * i + 1] * (1.0f / kScaleX));
-          uint16_t* o = e.out + p.batch * e.obatch;
-          if constexpr (STEP == kOrthoLast) {
-            if (m < p.mlim) put8(o + m * e.ldo, n, e.m, e.vec != 0, d);
-          } else {
-            transpose8(d, p.lane);
-            if (n + turn < p.nlim) put8(o + (n + turn) * e.ldo, turned, e.n, e.vec != 0, d);
-          }
+          transpose8(d, p.lane);
+          if (n + turn < p.nlim) put8(o + (n + turn) * e.ldo, turned, e.n, e.vec != 0, d);
         }
       }
     }
+  }
+}
+
+// MI x NI patches; what a patch reads is asked for two patches ahead.
+template <int STEP, int MI, int NI>
+__device__ __forceinline__ void ortho_patches(const OrthoEnd& e, const v16f (&v)[MI][NI], const RowPlace& p) {
+  constexpr int P = MI * NI, kAhead = 2;
+  const float f = e.factor ? e.factor[p.batch] : 1.0f;
+  OrthoOld old[kAhead + 1];
+#pragma unroll
+  for (int u = 0; u < (P < kAhead ? P : kAhead); ++u) ortho_load<STEP>(e, p, p.m + 32 * (u / NI), p.n + 32 * (u % NI), old[u]);
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    const int w = u + kAhead;
+    if (w < P) ortho_load<STEP>(e, p, p.m + 32 * (w / NI), p.n + 32 * (w % NI), old[w % (kAhead + 1)]);
+    __builtin_amdgcn_sched_barrier(0);
+    ortho_patch<STEP>(e, v[u / NI][u % NI], p, p.m + 32 * (u / NI), p.n + 32 * (u % NI), f, old[u % (kAhead + 1)]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 template <int STEP>
@@ -336,11 +367,7 @@ __global__ __launch_bounds__(WGM* WGN * 64, (RowTile<BM, BN, WGM * WGN, NST>::kM
   constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kRing];
   auto end = [&](const v16f (&acc)[MI][NI], const RowPlace& p) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      ortho_row<STEP, NI>(e, acc[i], p, p.m + 32 * i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    ortho_patches<STEP, MI, NI>(e, acc, p);
   };
   row_gemm_units<kRowsF16, BM, BN, WGM, WGN, NST, ortho_units<STEP>()>(d, tiles_m, tiles_n, 1, batches, nullptr, smem, end);
 }
@@ -410,7 +437,8 @@ __global__ __launch_bounds__(256) void ortho_sum_kernel(OrthoEnd e, const v4f* _
   p.wave = wave;
   p.whole = p.m0 + BM <= p.mlim && p.n0 + BN <= p.nlim;
   p.mirror = tm != tn;
-  ortho_row<STEP, NI>(e, v[0], p, p.m + 32 * i);
+  p.m += 32 * i;
+  ortho_patches<STEP, 1, NI>(e, v, p);
 }
 
 template <int BM, int BN, int WGM, int WGN, int NST, int STEP>
