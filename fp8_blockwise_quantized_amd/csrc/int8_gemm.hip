@@ -5,8 +5,8 @@
 //
 // Measured: 8192 x 8192 x 8192 2.44 POP/s (the library's plain 8-bit product without scales 2.35), 16384 x 11264 x 2048 331 us
 // (2.28), 4099 x 5632 x 2048 56 us (1.69), 64 experts of 2816 x 2048 with 768 rows 66 us (the weights' 369 MB at 5.6
-// TB/s).  Bound by the matrix pipes at the clock that the power allows (busy 73% of the cycles; the bare instruction runs
-// at 3.45 POP/s on such data), and with short contractions by the output: without its stores 2048 long ones take 23% less,
+// TB/s).  Bound by the matrix pipes at the clock that the power allows (busy 73% of the cycles for 8192 x 8192 x 8192,
+// 58% for 16384 x 11264 x 2048; the bare instruction runs at 3.45 POP/s on such data), and with short contractions by the output: without its stores 2048 long ones take 23% less,
 // 8192 long ones 11%; without the loads 13 to 15% less.
 #include "int8_common.hpp"
 #include "row_gemm.hpp"

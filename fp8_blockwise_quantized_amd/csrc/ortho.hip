@@ -22,13 +22,15 @@
 // 8 x 8 values, so that either goes out in 16-byte stores.  The second half lies beside X^T and is replaced where it is
 // read.  Rows are padded with zeros to whole stages of 64 halves.
 //
-// Bound by row_gemm.hpp's loop where the tiles fill the card (matrix pipes busy 61% of the cycles, the bare instruction
-// 1.68 PFLOP/s); a lone matrix's A and A^2 have few tiles and long contractions, which are split, the parts being
-// added up by a second kernel with the same epilogue.  Measured, five steps (us): 32 of 1408 x 2048 4120 (a step: A 190,
-// P 155, update 450, 0.58 to 0.68 PFLOP/s of what is computed; before them norm 39 and first X 90, 4.1 TB/s), 11264 x 2048
-// FP32 1226 (57 + 14, 24, 150; 22 and 54; unsplit 1283 with BF16), 8 of 512 x 384 110 (17 launches that wait for each other,
-// 5 to 10 each).  The update's tile shape hardly matters (11264 x 2048 with 256 x 192, 128 x 128, 64 x 64 and 256 x 256:
-// 1198, 1195, 1362, 1302; 32 of 1408 x 2048: 4328, 4194, 4985, 4108).
+// Bound, where the tiles fill the card, by row_gemm.hpp's loop (matrix pipes busy in A 57% and in P 50% of the cycles) and in
+// the update by its epilogue, 10 bytes an element read and written (busy 28%; 32 of 1408 x 2048 take 15% less without what
+// the epilogues read, 28% without what they write as well).  A lone matrix's A and A^2 have few tiles and long contractions, which
+// are split, the parts being added up by a second kernel with the same epilogue.  Measured, five steps (us): 32 of 1408 x
+// 2048 4060 (a step: A 190, P 150, update 440, 0.58 to 0.68 PFLOP/s of what is computed; before them norm 39 and first X 90,
+// 6.1 TB/s), 11264 x 2048 FP32 1200 (57 + 14, 24, 145; 22 and 54; A and A^2 unsplit 80 more), 8 of 512 x 384 110 (17
+// launches that wait for each other, 5 to 10 each).  The update's tile shape hardly matters (11264 x 2048 with 256 x 192, 128 x
+// 128, 64 x 64 and 256 x 256: 1198, 1195, 1362, 1302; 32 of 1408 x 2048: 4328, 4194, 4985, 4108), nor do staggered starts
+// (4097 for 4086, 1203 for 1172); stores of the second half past the caches cost 3%.
 #include <cmath>
 
 #include "launch.hpp"
