@@ -56,7 +56,7 @@ __device__ __forceinline__ void unpack_f16x2(uint32_t w, float& lo, float& hi) {
 
 // 8 x 8 values of 16 bits held by eight neighbouring lanes, one row (four pairs) a lane, transposed: first within pairs
 // of lanes, then pairs of values between lanes 2 and 4 apart.
-__device__ __forceinline__ void transpose8(uint32_t (&d)[4], int lane) {
+__device__ __forceinline__ void transpose8(u32x4& d, int lane) {
   const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) d[k] = __builtin_amdgcn_perm(dpp_read<kDppXor1>(d[k]), d[k], sel);
@@ -222,10 +222,10 @@ struct OrthoEnd {
 
 // Rows [0, rows) x columns [0, width) of 16-bit values: eight columns from col on, as far as they are there (all eight
 // where the buffer is padded: width a multiple of 64).
-__device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, bool vec, const uint32_t (&d)[4]) {
+__device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, bool vec, const u32x4& d) {
   if (col >= width) return;
   if (vec && col + 8 <= width) {
-    *reinterpret_cast<u32x4*>(row + col) = (u32x4){d[0], d[1], d[2], d[3]};
+    *reinterpret_cast<u32x4*>(row + col) = d;
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -233,69 +233,94 @@ __device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, 
   }
 }
 
-// What a patch's end reads: A (polynomial), or X^T as it was and its second half (update).
+// A lane's two 16-byte chunks of a patch row (columns 0 .. 7 and 16 .. 23 of its half): lanes l and l + 16 swap one, so that an
+// access takes 64 contiguous bytes of 16 rows and not 32 of 32 rows.  The swap undoes itself: it stands behind loads and
+// ahead of stores, and chunk q then lies at row m - (l & 16) + 16 q, column n0 + (l & 16).
+__device__ __forceinline__ void swap_chunks(u32x4 (&d)[2]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const auto p = __builtin_amdgcn_permlane16_swap(d[0][k], d[1][k], false, false);
+    d[0][k] = p[0];
+    d[1][k] = p[1];
+  }
+}
+__device__ __forceinline__ int64_t swapped_at(int64_t m, int64_t n0, int64_t ld, int lane) {
+  return (m - (lane & 16)) * ld + n0 + (lane & 16);
+}
+
+// What a patch's end reads: A (polynomial), or X^T as it was and its second half (update).  Whole tiles: as loaded, chunks
+// still swapped.
 struct OrthoOld {
   u32x4 hi[2], lo[2];
 };
 template <int STEP>
 __device__ __forceinline__ void ortho_load(const OrthoEnd& e, const RowPlace& p, int64_t m, int64_t n0, OrthoOld& o) {
   if constexpr (STEP == kOrthoGram) return;
+  const int64_t rows = STEP == kOrthoPoly ? e.m : e.n;
+  const uint16_t* from = STEP == kOrthoPoly ? e.gram : e.xt;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int64_t n = n0 + 16 * q;
     o.hi[q] = o.lo[q] = (u32x4){0, 0, 0, 0};
-    if (m < p.mlim && n < e.mp) {
-      if constexpr (STEP == kOrthoPoly) {
-        o.hi[q] = *reinterpret_cast<const u32x4*>(e.gram + (p.batch * e.m + m) * e.mp + n);
-      } else {
-        const int64_t at = (p.batch * e.n + m) * e.mp + n;
-        o.hi[q] = *reinterpret_cast<const u32x4*>(e.xt + at);
-        if (e.has_low) o.lo[q] = *reinterpret_cast<const u32x4*>(e.low + at);
-      }
-    }
+    if (!p.whole && (m >= p.mlim || n0 + 16 * q >= e.mp)) continue;
+    const int64_t at = p.batch * rows * e.mp + (p.whole ? swapped_at(m, n0, e.mp, p.lane) + 16 * q * e.mp : m * e.mp + n0 + 16 * q);
+    o.hi[q] = *reinterpret_cast<const u32x4*>(from + at);
+    if (STEP != kOrthoPoly && e.has_low) o.lo[q] = *reinterpret_cast<const u32x4*>(e.low + at);
+  }
+}
+
+// Both chunks of a row of a matrix (rows ld apart) of which `width` columns are there.
+__device__ __forceinline__ void put_chunks(uint16_t* o, int64_t ld, int64_t width, bool vec, const RowPlace& p, int64_t m,
+                                           int64_t n0, const u32x4 (&d)[2]) {
+  if (p.whole && vec) {
+    u32x4 w[2] = {d[0], d[1]};
+    swap_chunks(w);
+    uint16_t* at = o + swapped_at(m, n0, ld, p.lane);
+    *reinterpret_cast<u32x4*>(at) = w[0];
+    *reinterpret_cast<u32x4*>(at + 16 * ld) = w[1];
+  } else if (m < p.mlim) {
+    put8(o + m * ld, n0, width, vec, d[0]);
+    put8(o + m * ld, n0 + 16, width, vec, d[1]);
+  }
+}
+// Their transposes: eight rows of the patch in a row of a matrix whose rows are the patch's columns.
+__device__ __forceinline__ void put_turned(uint16_t* o, int64_t ld, int64_t width, bool vec, const RowPlace& p, int64_t m,
+                                           int64_t n0, const u32x4 (&d)[2]) {
+  const int turn = p.lane & 7;  // the lane's column among the eight after the turn
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    u32x4 w = d[q];
+    transpose8(w, p.lane);
+    const int64_t n = n0 + 16 * q + turn;
+    if (n < p.nlim) put8(o + n * ld, m - turn, width, vec, w);
   }
 }
 
 // STEP of one patch: v[8 q + i] is row m, column n0 + 16 q + i of the product.
 template <int STEP>
 __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, const RowPlace& p, int64_t m, int64_t n0, float f,
-                                            const OrthoOld& old) {
-  const int64_t turned = m - (p.lane & 7);         // first of the eight rows that come together, and the lane's
-  const int turn = p.lane & 7;                     // column among the eight after the turn
+                                            OrthoOld& old) {
+  if (STEP != kOrthoGram && p.whole) {
+    swap_chunks(old.hi);
+    if (STEP != kOrthoPoly && e.has_low) swap_chunks(old.lo);
+  }
+  u32x4 d[2], l[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int64_t n = n0 + 16 * q;
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = v[8 * q + i];
-    uint32_t d[4];
-    if constexpr (STEP == kOrthoGram || STEP == kOrthoPoly) {
-      const int64_t size = e.m * e.mp;
-      if constexpr (STEP == kOrthoGram) {
-        const float s = f * f * (kScaleA / (kScaleX * kScaleX));
+    if constexpr (STEP == kOrthoGram) {
+      const float s = f * f * (kScaleA / (kScaleX * kScaleX));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= s;
-      } else {
-        const float s = e.c * (1.0f / kScaleA);
+      for (int i = 0; i < 8; ++i) y[i] *= s;
+    } else if constexpr (STEP == kOrthoPoly) {
+      const float s = e.c * (1.0f / kScaleA);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float lo, hi;
-          unpack_f16x2(old.hi[q][i], lo, hi);
-          y[2 * i] = __builtin_fmaf(e.b, lo, s * y[2 * i]);
-          y[2 * i + 1] = __builtin_fmaf(e.b, hi, s * y[2 * i + 1]);
-        }
-      }
-      if (!p.whole) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
-      uint16_t* o = e.sym + p.batch * size;
-      if (m < p.mlim) put8(o + m * e.mp, n, e.mp, true, d);
-      if (p.mirror) {
-        transpose8(d, p.lane);
-        if (n + turn < p.nlim) put8(o + (n + turn) * e.mp, turned, e.mp, true, d);
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack_f16x2(old.hi[q][i], lo, hi);
+        y[2 * i] = __builtin_fmaf(e.b, lo, s * y[2 * i]);
+        y[2 * i + 1] = __builtin_fmaf(e.b, hi, s * y[2 * i + 1]);
       }
     } else {
 #pragma unroll
@@ -306,38 +331,38 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
         y[2 * i] = f * __builtin_fmaf(e.a, h0 + l0, y[2 * i] * (1.0f / kScaleA));
         y[2 * i + 1] = f * __builtin_fmaf(e.a, h1 + l1, y[2 * i + 1] * (1.0f / kScaleA));
       }
-      if (!p.whole) {
+    }
+    if (!p.whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n + i < p.nlim ? y[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) y[i] = m < p.mlim && n0 + 16 * q + i < p.nlim ? y[i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (STEP == kOrthoLast || STEP == kOrthoLastWide) {
+        d[q][i] = pack_bf16x2(y[2 * i] * (1.0f / kScaleX), y[2 * i + 1] * (1.0f / kScaleX));
+      } else {
+        d[q][i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
       }
       if constexpr (STEP == kOrthoUpdate) {
-        uint32_t l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float h0, h1;
-          d[i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
-          unpack_f16x2(d[i], h0, h1);
-          l[i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
-        }
-        if (m < p.mlim) {
-          const int64_t at = (p.batch * e.n + m) * e.mp;
-          put8(e.xt_out + at, n, e.mp, true, d);
-          put8(e.low + at, n, e.mp, true, l);
-        }
-        transpose8(d, p.lane);
-        if (n + turn < p.nlim) put8(e.x_out + (p.batch * e.m + n + turn) * e.np, turned, e.np, true, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(y[2 * i] * (1.0f / kScaleX), y[2 * i + 1] * (1.0f / kScaleX));
-        uint16_t* o = e.out + p.batch * e.obatch;
-        if constexpr (STEP == kOrthoLast) {
-          if (m < p.mlim) put8(o + m * e.ldo, n, e.m, e.vec != 0, d);
-        } else {
-          transpose8(d, p.lane);
-          if (n + turn < p.nlim) put8(o + (n + turn) * e.ldo, turned, e.n, e.vec != 0, d);
-        }
+        float h0, h1;
+        unpack_f16x2(d[q][i], h0, h1);
+        l[q][i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
       }
     }
+  }
+  if constexpr (STEP == kOrthoGram || STEP == kOrthoPoly) {
+    uint16_t* o = e.sym + p.batch * e.m * e.mp;
+    put_chunks(o, e.mp, e.mp, true, p, m, n0, d);
+    if (p.mirror) put_turned(o, e.mp, e.mp, true, p, m, n0, d);
+  } else if constexpr (STEP == kOrthoUpdate) {
+    const int64_t at = p.batch * e.n * e.mp;
+    put_chunks(e.xt_out + at, e.mp, e.mp, true, p, m, n0, d);
+    put_chunks(e.low + at, e.mp, e.mp, true, p, m, n0, l);
+    put_turned(e.x_out + p.batch * e.m * e.np, e.np, e.np, true, p, m, n0, d);
+  } else {
+    uint16_t* o = e.out + p.batch * e.obatch;
+    if constexpr (STEP == kOrthoLast) put_chunks(o, e.ldo, e.m, e.vec != 0, p, m, n0, d);
+    else put_turned(o, e.ldo, e.n, e.vec != 0, p, m, n0, d);
   }
 }
 
