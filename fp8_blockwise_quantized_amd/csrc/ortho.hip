@@ -26,8 +26,8 @@
 // the update by its epilogue, 10 bytes an element read and written (busy 28%; 32 of 1408 x 2048 take 15% less without what
 // the epilogues read, 28% without what they write as well).  A lone matrix's A and A^2 have few tiles and long contractions, which
 // are split, the parts being added up by a second kernel with the same epilogue.  Measured, five steps (us): 32 of 1408 x
-// 2048 4060 (a step: A 190, P 150, update 440, 0.58 to 0.68 PFLOP/s of what is computed; before them norm 39 and first X 90,
-// 6.1 TB/s), 11264 x 2048 FP32 1200 (57 + 14, 24, 145; 22 and 54; A and A^2 unsplit 80 more), 8 of 512 x 384 110 (17
+// 2048 4030 (a step: A 190, P 150, update 440, 0.58 to 0.68 PFLOP/s of what is computed; before them norm 39 and first X 90,
+// 6.1 TB/s), 11264 x 2048 FP32 1184 (57 + 14, 24, 140; 22 and 54; A and A^2 unsplit 80 more), 8 of 512 x 384 111 (17
 // launches that wait for each other, 5 to 10 each).  The update's tile shape hardly matters (11264 x 2048 with 256 x 192, 128 x
 // 128, 64 x 64 and 256 x 256: 1198, 1195, 1362, 1302; 32 of 1408 x 2048: 4328, 4194, 4985, 4108), nor do staggered starts
 // (4097 for 4086, 1203 for 1172); stores of the second half past the caches cost 3%.
@@ -234,7 +234,7 @@ __device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, 
 }
 
 // A lane's two 16-byte chunks of a patch row (columns 0 .. 7 and 16 .. 23 of its half): lanes l and l + 16 swap one, so that an
-// access takes 64 contiguous bytes of 16 rows and not 32 of 32 rows.  The swap undoes itself: it stands behind loads and
+// access takes 64 contiguous bytes of 16 rows and not 32 of 32 rows (11264 x 2048 1179 -> 1161 us).  The swap undoes itself: it stands behind loads and
 // ahead of stores, and chunk q then lies at row m - (l & 16) + 16 q, column n0 + (l & 16).
 __device__ __forceinline__ void swap_chunks(u32x4 (&d)[2]) {
 #pragma unroll
@@ -366,7 +366,8 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
   }
 }
 
-// MI x NI patches; what a patch reads is asked for two patches ahead.
+// MI x NI patches; what a patch reads is asked for two patches ahead (11264 x 2048 1222 -> 1190 us, 16 of 1024 x 1024
+// 751 -> 702).
 template <int STEP, int MI, int NI>
 __device__ __forceinline__ void ortho_patches(const OrthoEnd& e, const v16f (&v)[MI][NI], const RowPlace& p) {
   constexpr int P = MI * NI, kAhead = 2;
