@@ -5,32 +5,27 @@
 // vectors stay.  Three products a step, A and A^2 symmetric: only their upper triangle of tiles is computed, and a tile
 // is written twice.
 //
-// Rounding.  The products run in 16-bit floats (11 bits) with FP32 accumulation.  Rounding X itself to 11 bits would put
-// noise of all directions into it, and the small singular values' directions are then amplified by a in every step: a
-// gradient of rank 32 in noise came out 2 10^-2 off.  So X is kept as the sum of two halves (22 bits), and a X is taken of
-// both.  The products take the first half alone, and A and the polynomial P = b A + c A^2 are rounded to 11 bits: an error
-// of A or P is multiplied by X and stays among X's rows, and P times the second half is what P, whose columns are X's own
-// directions, makes of noise: neither reaches the directions in which X is small.  Off by (of the result's norm, five
-// steps) 5 10^-4 for matrices of low rank, 1.6 10^-3 for random ones (with products of both halves 4 10^-4 and 1.3 10^-3,
-// at twice the work); the result's own BF16 rounding is 1.7 10^-3.
+// Rounding.  A step amplifies what it is given: an error of X in directions where X is small by a, one of A by up to b + 2 c A.
+// With A and P held in 11 bits and products of 11-bit operands the result was off by 3 10^-4 (low rank) to 7 10^-3 of its norm
+// (few rows, equal singular values), where its own rounding to BF16 is 1.7 10^-3; every one of these roundings alone is worth
+// 2 10^-4 to 6 10^-3.  So X, A and P are each the sum of two 16-bit floats (22 bits), and a product of two such sums takes
+// three of the four products (first halves; first by second; second by first), with FP32 accumulation: off by 5 10^-6 or less for
+// random, low-rank and orthogonal matrices, as FP32 products are, at three times the matrix instructions.  A BF16 input fits
+// the first half, so the first step has one term in A and two in the update.
 //
 // Scaling.  Halves hold 6 10^-8 .. 65504; X is held as 2^12 X, A and the polynomial as 2^10 A.  The first X is G times a
 // power of two (exact), the rest of the normalization (a factor in 1 .. 2) enters the first step's epilogues.
 //
-// Layout.  X (first half, rows along n) serves A's product, X^T (rows along m) the update's: X^T_new = X^T P is a product
+// Layout.  X (rows along n) serves A's product, X^T (rows along m) the update's: X^T_new = X^T P is a product
 // of rows again.  The update writes both: a patch of accumulators is transposed in registers, eight lanes exchanging
-// 8 x 8 values, so that either goes out in 16-byte stores.  The second half lies beside X^T and is replaced where it is
-// read.  Rows are padded with zeros to whole stages of 64 halves.
+// 8 x 8 values, so that either goes out in 16-byte stores.  Second halves lie beside the first ones, in matrices of their own.
+// Rows are padded with zeros to whole stages of 64 halves.
 //
-// Bound, where the tiles fill the card, by row_gemm.hpp's loop (matrix pipes busy in A 57% and in P 50% of the cycles) and in
-// the update by its epilogue, 10 bytes an element read and written (busy 28%; 32 of 1408 x 2048 take 15% less without what
-// the epilogues read, 28% without what they write as well).  A lone matrix's A and A^2 have few tiles and long contractions, which
-// are split, the parts being added up by a second kernel with the same epilogue.  Measured, five steps (us): 32 of 1408 x
-// 2048 4030 (a step: A 190, P 150, update 440, 0.58 to 0.68 PFLOP/s of what is computed; before them norm 39 and first X 90,
-// 6.1 TB/s), 11264 x 2048 FP32 1184 (57 + 14, 24, 140; 22 and 54; A and A^2 unsplit 80 more), 8 of 512 x 384 111 (17
-// launches that wait for each other, 5 to 10 each).  The update's tile shape hardly matters (11264 x 2048 with 256 x 192, 128 x
-// 128, 64 x 64 and 256 x 256: 1198, 1195, 1362, 1302; 32 of 1408 x 2048: 4328, 4194, 4985, 4108), nor do staggered starts
-// (4097 for 4086, 1203 for 1172); stores of the second half past the caches cost 3%.
+// Bound, where the tiles fill the card, by row_gemm.hpp's loop and in the update by its epilogue as well, 12 bytes an element
+// read and written.  A lone matrix's A and A^2 have few tiles and long contractions, which are split, the parts being added
+// up by a second kernel with the same epilogue.  Measured, five steps (us): 32 of 1408 x 2048 8900 (a step: A 524, P 407,
+// update 967, 0.8 to 1.03 PFLOP/s of what is computed; before them norm 39 and first X 90, 6.1 TB/s), 11264 x 2048 FP32 2630
+// (142 + 18, 35 + 15, 322; 24 and 59), 8 of 512 x 384 191 (17 launches that wait for each other, 6 to 16 each).
 #include <cmath>
 
 #include "launch.hpp"
@@ -110,9 +105,8 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(const TIn* __restrict__
 
 // The first X in both layouts, from tiles of 64 x 64 of G; factor[batch].  tall: G is X^T.
 struct OrthoBuffers {
-  uint16_t* x;    // [batch][m][np] first halves
-  uint16_t* xt;   // [batch][n][mp] first halves
-  uint16_t* low;  // [batch][n][mp] second halves (FP32 input; BF16 fits the first)
+  uint16_t *x, *x_low;    // [batch][m][np] first and second halves (second: FP32 input; BF16 fits the first)
+  uint16_t *xt, *xt_low;  // [batch][n][mp]
   int64_t m, n, mp, np;
 };
 template <typename TIn>
@@ -153,9 +147,13 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
   if (t == 0 && blockIdx.x == 0 && blockIdx.y == 0)
     factor[batch] = finite ? (float)(1.0 / __builtin_amdgcn_frexp_mant(norm)) : __builtin_nanf("");
   // (buffers are padded to whole tiles of 64 along their rows; rows past the matrix are not there)
-  uint16_t* x = b.x + (int64_t)batch * b.m * b.np;
-  uint16_t* xt = b.xt + (int64_t)batch * b.n * b.mp;
-  uint16_t* xl = b.low + (int64_t)batch * b.n * b.mp;
+  // straight: rows of G; turned: its columns
+  const int64_t of_x = (int64_t)batch * b.m * b.np, of_xt = (int64_t)batch * b.n * b.mp;
+  uint16_t* straight = tall ? b.xt + of_xt : b.x + of_x;
+  uint16_t* straight_low = tall ? b.xt_low + of_xt : b.x_low + of_x;
+  uint16_t* turned = tall ? b.x + of_x : b.xt + of_xt;
+  uint16_t* turned_low = tall ? b.x_low + of_x : b.xt_low + of_xt;
+  const int64_t lds = tall ? b.mp : b.np, ldt = tall ? b.np : b.mp;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t r = r0 + row + 32 * h;
@@ -173,12 +171,8 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
     *reinterpret_cast<u32x4*>(&tile[row + 32 * h][c]) = hi;
     if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(&low[row + 32 * h][c]) = lo;
     if (r < R) {
-      if (tall) {
-        *reinterpret_cast<u32x4*>(xt + r * b.mp + c0 + c) = hi;
-        if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(xl + r * b.mp + c0 + c) = lo;
-      } else {
-        *reinterpret_cast<u32x4*>(x + r * b.np + c0 + c) = hi;
-      }
+      *reinterpret_cast<u32x4*>(straight + r * lds + c0 + c) = hi;
+      if constexpr (sizeof(TIn) == 4) *reinterpret_cast<u32x4*>(straight_low + r * lds + c0 + c) = lo;
     }
   }
   __syncthreads();
@@ -189,15 +183,11 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
     u32x4 hi, lo;
 #pragma unroll
     for (int k = 0; k < 4; ++k) hi[k] = tile[c + 2 * k][i] | (uint32_t)tile[c + 2 * k + 1][i] << 16;
-    if (tall) {
-      *reinterpret_cast<u32x4*>(x + (c0 + i) * b.np + r0 + c) = hi;
-    } else {
-      *reinterpret_cast<u32x4*>(xt + (c0 + i) * b.mp + r0 + c) = hi;
-      if constexpr (sizeof(TIn) == 4) {
+    *reinterpret_cast<u32x4*>(turned + (c0 + i) * ldt + r0 + c) = hi;
+    if constexpr (sizeof(TIn) == 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) lo[k] = low[c + 2 * k][i] | (uint32_t)low[c + 2 * k + 1][i] << 16;
-        *reinterpret_cast<u32x4*>(xl + (c0 + i) * b.mp + r0 + c) = lo;
-      }
+      for (int k = 0; k < 4; ++k) lo[k] = low[c + 2 * k][i] | (uint32_t)low[c + 2 * k + 1][i] << 16;
+      *reinterpret_cast<u32x4*>(turned_low + (c0 + i) * ldt + r0 + c) = lo;
     }
   }
 }
@@ -207,13 +197,9 @@ enum OrthoStep : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2, kOrthoL
 struct OrthoEnd {
   float a, b, c;          // the step's coefficients
   const float* factor;    // of the first step's X (null: 1)
-  uint16_t* sym;          // Gram, polynomial: output [batch][m][mp]
-  const uint16_t* gram;   // polynomial: A
-  const uint16_t* xt;     // update: X^T as it was, and its second half (replaced; not read where it is not there)
-  uint16_t* low;
-  int has_low;
-  uint16_t* xt_out;       // update: X^T and X
-  uint16_t* x_out;
+  const uint16_t *old, *old_low;  // polynomial: A; update: X^T as it was (second halves null: zeros)
+  uint16_t *to, *to_low;          // Gram, polynomial: [batch][m][mp]; update: X^T
+  uint16_t *x, *x_low;            // update: X
   uint16_t* out;          // last: BF16 result [batch], rows ldo apart
   int64_t ldo, obatch;
   int vec;                // 16-byte stores into it are possible
@@ -234,7 +220,7 @@ __device__ __forceinline__ void put8(uint16_t* row, int64_t col, int64_t width, 
 }
 
 // A lane's two 16-byte chunks of a patch row (columns 0 .. 7 and 16 .. 23 of its half): lanes l and l + 16 swap one, so that an
-// access takes 64 contiguous bytes of 16 rows and not 32 of 32 rows (11264 x 2048 1179 -> 1161 us).  The swap undoes itself: it stands behind loads and
+// access takes 64 contiguous bytes of 16 rows and not 32 of 32 rows (2% of 11264 x 2048 with one term).  The swap undoes itself: it stands behind loads and
 // ahead of stores, and chunk q then lies at row m - (l & 16) + 16 q, column n0 + (l & 16).
 __device__ __forceinline__ void swap_chunks(u32x4 (&d)[2]) {
 #pragma unroll
@@ -257,14 +243,13 @@ template <int STEP>
 __device__ __forceinline__ void ortho_load(const OrthoEnd& e, const RowPlace& p, int64_t m, int64_t n0, OrthoOld& o) {
   if constexpr (STEP == kOrthoGram) return;
   const int64_t rows = STEP == kOrthoPoly ? e.m : e.n;
-  const uint16_t* from = STEP == kOrthoPoly ? e.gram : e.xt;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     o.hi[q] = o.lo[q] = (u32x4){0, 0, 0, 0};
     if (!p.whole && (m >= p.mlim || n0 + 16 * q >= e.mp)) continue;
     const int64_t at = p.batch * rows * e.mp + (p.whole ? swapped_at(m, n0, e.mp, p.lane) + 16 * q * e.mp : m * e.mp + n0 + 16 * q);
-    o.hi[q] = *reinterpret_cast<const u32x4*>(from + at);
-    if (STEP != kOrthoPoly && e.has_low) o.lo[q] = *reinterpret_cast<const u32x4*>(e.low + at);
+    o.hi[q] = *reinterpret_cast<const u32x4*>(e.old + at);
+    if (e.old_low) o.lo[q] = *reinterpret_cast<const u32x4*>(e.old_low + at);
   }
 }
 
@@ -301,7 +286,7 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
                                             OrthoOld& old) {
   if (STEP != kOrthoGram && p.whole) {
     swap_chunks(old.hi);
-    if (STEP != kOrthoPoly && e.has_low) swap_chunks(old.lo);
+    if (e.old_low) swap_chunks(old.lo);
   }
   u32x4 d[2], l[2];
 #pragma unroll
@@ -317,10 +302,11 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
       const float s = e.c * (1.0f / kScaleA);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        unpack_f16x2(old.hi[q][i], lo, hi);
-        y[2 * i] = __builtin_fmaf(e.b, lo, s * y[2 * i]);
-        y[2 * i + 1] = __builtin_fmaf(e.b, hi, s * y[2 * i + 1]);
+        float h0, h1, l0, l1;
+        unpack_f16x2(old.hi[q][i], h0, h1);
+        unpack_f16x2(old.lo[q][i], l0, l1);
+        y[2 * i] = __builtin_fmaf(e.b, h0 + l0, s * y[2 * i]);
+        y[2 * i + 1] = __builtin_fmaf(e.b, h1 + l1, s * y[2 * i + 1]);
       }
     } else {
 #pragma unroll
@@ -342,8 +328,6 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
         d[q][i] = pack_bf16x2(y[2 * i] * (1.0f / kScaleX), y[2 * i + 1] * (1.0f / kScaleX));
       } else {
         d[q][i] = pack_f16x2(y[2 * i], y[2 * i + 1]);
-      }
-      if constexpr (STEP == kOrthoUpdate) {
         float h0, h1;
         unpack_f16x2(d[q][i], h0, h1);
         l[q][i] = pack_f16x2(y[2 * i] - h0, y[2 * i + 1] - h1);
@@ -351,14 +335,19 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
     }
   }
   if constexpr (STEP == kOrthoGram || STEP == kOrthoPoly) {
-    uint16_t* o = e.sym + p.batch * e.m * e.mp;
-    put_chunks(o, e.mp, e.mp, true, p, m, n0, d);
-    if (p.mirror) put_turned(o, e.mp, e.mp, true, p, m, n0, d);
+    const int64_t at = p.batch * e.m * e.mp;
+    put_chunks(e.to + at, e.mp, e.mp, true, p, m, n0, d);
+    put_chunks(e.to_low + at, e.mp, e.mp, true, p, m, n0, l);
+    if (p.mirror) {
+      put_turned(e.to + at, e.mp, e.mp, true, p, m, n0, d);
+      put_turned(e.to_low + at, e.mp, e.mp, true, p, m, n0, l);
+    }
   } else if constexpr (STEP == kOrthoUpdate) {
-    const int64_t at = p.batch * e.n * e.mp;
-    put_chunks(e.xt_out + at, e.mp, e.mp, true, p, m, n0, d);
-    put_chunks(e.low + at, e.mp, e.mp, true, p, m, n0, l);
-    put_turned(e.x_out + p.batch * e.m * e.np, e.np, e.np, true, p, m, n0, d);
+    const int64_t at = p.batch * e.n * e.mp, of_x = p.batch * e.m * e.np;
+    put_chunks(e.to + at, e.mp, e.mp, true, p, m, n0, d);
+    put_chunks(e.to_low + at, e.mp, e.mp, true, p, m, n0, l);
+    put_turned(e.x + of_x, e.np, e.np, true, p, m, n0, d);
+    put_turned(e.x_low + of_x, e.np, e.np, true, p, m, n0, l);
   } else {
     uint16_t* o = e.out + p.batch * e.obatch;
     if constexpr (STEP == kOrthoLast) put_chunks(o, e.ldo, e.m, e.vec != 0, p, m, n0, d);
@@ -366,8 +355,8 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
   }
 }
 
-// MI x NI patches; what a patch reads is asked for two patches ahead (11264 x 2048 1222 -> 1190 us, 16 of 1024 x 1024
-// 751 -> 702).
+// MI x NI patches; what a patch reads is asked for two patches ahead (with one term 11264 x 2048 1222 -> 1190 us, 16 of
+// 1024 x 1024 751 -> 702).
 template <int STEP, int MI, int NI>
 __device__ __forceinline__ void ortho_patches(const OrthoEnd& e, const v16f (&v)[MI][NI], const RowPlace& p) {
   constexpr int P = MI * NI, kAhead = 2;
@@ -516,18 +505,20 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
   uint8_t* w = (uint8_t*)ws;
   double* norms = (double*)(w + p.at_norms);
   float* factor = (float*)(w + p.at_factor);
+  const int es = gt == 0 ? 2 : 4, B = (int)p.batch;
+  // (of X^T, A and the polynomial the second halves lie behind the first ones of all matrices)
+  const int64_t to_low_xt = p.batch * p.n * p.mp, to_low_sym = p.batch * p.m * p.mp;
   uint16_t* x = (uint16_t*)(w + p.at_x);
+  uint16_t* x_low = (uint16_t*)(w + p.at_low);
   uint16_t* xt[2] = {(uint16_t*)(w + p.at_xt[0]), (uint16_t*)(w + p.at_xt[1])};
-  uint16_t* low = (uint16_t*)(w + p.at_low);
   uint16_t* gram = (uint16_t*)(w + p.at_gram);
   uint16_t* poly = (uint16_t*)(w + p.at_poly);
   void* parts = w + p.at_parts;
-  const int es = gt == 0 ? 2 : 4, B = (int)p.batch;
   const int wide = p.C % 8 == 0 && ((uintptr_t)g & 15) == 0 && ldg * es % 16 == 0 && (gbatch * es % 16 == 0 || B == 1);
 
   const dim3 ngrid((unsigned)p.norm_blocks, (unsigned)B);
   const dim3 bgrid((unsigned)((p.C + 63) / 64), (unsigned)((p.R + 63) / 64), (unsigned)B);
-  const OrthoBuffers b{x, xt[0], low, p.m, p.n, p.mp, p.np};
+  const OrthoBuffers b{x, x_low, xt[0], xt[0] + to_low_xt, p.m, p.n, p.mp, p.np};
   if (gt == 0) {
     hipLaunchKernelGGL(ortho_norm_kernel<uint16_t>, ngrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, wide, norms);
     FP8BQ_TRY(hipGetLastError());
@@ -548,12 +539,9 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     e.b = (float)coef[3 * k + 1];
     e.c = (float)coef[3 * k + 2];
     e.factor = first ? factor : nullptr;
-    e.gram = gram;
-    e.xt = xt[k & 1];
-    e.low = low;
-    e.has_low = !(first && gt == 0);
-    e.xt_out = xt[(k & 1) ^ 1];
-    e.x_out = x;
+    const bool low = !(first && gt == 0);  // X has second halves
+    e.x = x;
+    e.x_low = x_low;
     e.out = (uint16_t*)out;
     e.ldo = ldo;
     e.obatch = obatch;
@@ -568,14 +556,22 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     d.M = d.N = p.m;
     d.K = 2 * p.np;
     d.abatch = d.bbatch = 2 * p.m * p.np;
-    e.sym = gram;
+    d.alow = d.blow = 2 * (x_low - x);
+    d.terms = low ? 3 : 1;
+    e.to = gram;
+    e.to_low = gram + to_low_sym;
     FP8BQ_TRY(launch_product<kOrthoGram>(d, e, p.gram, B, parts, st));
     e.factor = nullptr;
     d.a = d.b = (const uint8_t*)gram;  // P
     d.lda = d.ldb = 2 * p.mp;
     d.K = 2 * p.mp;
     d.abatch = d.bbatch = 2 * p.m * p.mp;
-    e.sym = poly;
+    d.alow = d.blow = 2 * to_low_sym;
+    d.terms = 3;
+    e.old = gram;
+    e.old_low = gram + to_low_sym;
+    e.to = poly;
+    e.to_low = poly + to_low_sym;
     FP8BQ_TRY(launch_product<kOrthoPoly>(d, e, p.poly, B, parts, st));
     e.factor = first ? factor : nullptr;
     d.a = (const uint8_t*)xt[k & 1];  // X^T P
@@ -583,6 +579,12 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     d.b = (const uint8_t*)poly;
     d.M = p.n;
     d.abatch = 2 * p.n * p.mp;
+    d.alow = 2 * to_low_xt;
+    d.terms = low ? 3 : 2;
+    e.old = xt[k & 1];
+    e.old_low = low ? xt[k & 1] + to_low_xt : nullptr;
+    e.to = xt[(k & 1) ^ 1];
+    e.to_low = e.to + to_low_xt;
     if (!last)
       FP8BQ_TRY(launch_product<kOrthoUpdate>(d, e, p.update, B, nullptr, st));
     else if (tall)

@@ -18,7 +18,8 @@ struct OrthoPlan {
   int64_t batch, R, C, m, n, mp, np;  // m, n: the shorter and the longer side; mp, np: padded to whole stages
   OrthoProduct gram, poly, update;
   int norm_blocks;                    // of a matrix
-  size_t at_norms, at_factor, at_x, at_xt[2], at_low, at_gram, at_poly, at_parts;  // byte offsets in the workspace
+  // byte offsets in the workspace: first halves of X and, at at_low, its second ones; X^T, A and the polynomial hold both
+  size_t at_norms, at_factor, at_x, at_xt[2], at_low, at_gram, at_poly, at_parts;
   size_t ws;
 };
 

@@ -30,6 +30,10 @@ struct RowDesc {
   int64_t M, N;
   int64_t K;          // contraction bytes, a multiple of 16
   int64_t abatch, bbatch;  // bytes between the matrices of a batch
+  // Halves: an operand of 22 bits is a sum of two matrices, low bytes apart.  Of (a + al)(b + bl) the first `terms` of
+  // a b, a bl and al b are taken, one stage after the other (al bl is 2^-22 of the whole).
+  int64_t alow, blow;
+  int terms;
 };
 
 enum RowKind : int { kRowsI8 = 0, kRowsF16 = 1 };
@@ -132,7 +136,8 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
   const int lane = t & 63;
   const int wid = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wid / WGN, wn = wid % WGN;
-  const int nkb = (int)((d.K + 127) / 128);  // stages of the contraction
+  const int terms = KIND == kRowsF16 ? d.terms : 1;
+  const int nkb = (int)((d.K + 127) / 128) * terms;  // stages of the contraction
   const int tail = (int)(d.K % 128);         // bytes of a last stage that is not whole
   const uint32_t G = gridDim.x;
   const uint32_t T = UNITS == kUnitsTriangle ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
@@ -178,12 +183,17 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
   uint32_t lu = blockIdx.x;
   RowUnit L = unit_at(lu);
   int lkb = L.kb0;
+  int lk = 0, lt = 0;  // halves: the stage's place along the rows, and its term
   bool lmore = true;
   const uint8_t* abase = nullptr;
   const uint8_t* bbase = nullptr;
   uint32_t abytes = 0, bbytes = 0;
   uint32_t aoff[AL], boff[BL];
   auto set_sources = [&](const RowUnit& u) {
+    if constexpr (KIND == kRowsF16) {
+      lk = lkb / terms;
+      lt = lkb - lk * terms;
+    }
     abase = d.a + (int64_t)u.batch * d.abatch + (int64_t)u.m0 * d.lda;
     bbase = d.b + (int64_t)u.batch * d.bbatch + (int64_t)u.n0 * d.ldb;
     // (32-bit throughout: a tile's rows lie within 2^31 bytes)
@@ -222,11 +232,13 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
     }
   };
   auto issue_load = [&](int i, uint8_t* stg) {
+    const int at = (KIND == kRowsF16 ? lk : lkb) * 128;
     if (i < AL) {
-      dma16(rsrc_of(abase + (int64_t)lkb * 128, abytes - (uint32_t)(lkb * 128)), aoff[i], stg + (wid + NW * i) * 1024);
+      const int64_t low = KIND == kRowsF16 && lt == 2 ? d.alow : 0;
+      dma16(rsrc_of(abase + low + at, abytes - (uint32_t)at), aoff[i], stg + (wid + NW * i) * 1024);
     } else {
-      dma16(rsrc_of(bbase + (int64_t)lkb * 128, bbytes - (uint32_t)(lkb * 128)), boff[i - AL],
-            stg + Tile::kB + (wid + NW * (i - AL)) * 1024);
+      const int64_t low = KIND == kRowsF16 && lt == 1 ? d.blow : 0;
+      dma16(rsrc_of(bbase + low + at, bbytes - (uint32_t)at), boff[i - AL], stg + Tile::kB + (wid + NW * (i - AL)) * 1024);
     }
   };
   auto advance = [&]() {
@@ -241,6 +253,11 @@ __device__ __forceinline__ void row_gemm_units(const RowDesc& d, uint32_t tiles_
         lkb = L.kb1 - 1;  // (loaded again into a slot that is never read)
         lmore = false;
         return;
+      }
+    } else if constexpr (KIND == kRowsF16) {
+      if (++lt == terms) {
+        lt = 0;
+        ++lk;
       }
     }
     cut_sources();

@@ -6,9 +6,9 @@
  *   A = X X^T,   X <- a X + (b A + c A^2) X     (R <= C; otherwise with X^T X from the right),
  * which takes each singular value s to a s + b s^3 + c s^5 and keeps the singular vectors.  The result is X in BF16.
  *
- * Accuracy.  X is held in 22 bits, its products take 11 of them and A and the polynomial are held in 11, sums in FP32: the
- * result is off by 1.6 10^-3 of its norm or less besides its own rounding to BF16, for matrices of full and of low rank
- * alike (five steps of 3.4445, -4.7750, 2.0315).
+ * Accuracy.  X, A and the polynomial are held in 22 bits, and their products taken of these, sums in FP32: the result is off
+ * by 2^-14 of its norm or less besides its own rounding to BF16, for matrices of full and of low rank, of equal singular
+ * values and of a few rows alike (up to ten steps of 3.4445, -4.7750, 2.0315).
  * Singular values have to stay below 12 and the polynomial b A + c A^2 below 60 on the way (16-bit floats hold no more);
  * past that the result is not finite.  A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN in all of
  * its places and leaves the others of the batch alone.
@@ -32,8 +32,8 @@ extern "C" {
  *   coefficients  HOST memory, 3 steps doubles: a, b, c of each step (read during the call); finite.
  *   1 <= steps <= FP8BQ_MAX_ORTHO_STEPS;  eps > 0, finite.
  *   out  [B] matrices [R, C], BF16 (ldo, ostride).
- *   ws   at least fp8bq_orthogonalize_workspace_size(B, R, C) bytes (8 to 12 an element, and the partial sums of a split
- *        contraction where few matrices leave the card idle).
+ *   ws   at least fp8bq_orthogonalize_workspace_size(B, R, C) bytes (at most 20 an element of the matrices with both sides
+ *        rounded up to 64, and the partial sums of a split contraction where few matrices leave the card idle).
  *   B <= 4096; R, C <= 2^20.
  */
 size_t fp8bq_orthogonalize_workspace_size(int64_t B, int64_t R, int64_t C);

@@ -1,0 +1,90 @@
+"""The accuracy that the orthogonalization's header states, against Newton-Schulz steps in float64.
+
+A result y is the exact w plus an error e, rounded to BF16, so |y - w| <= |e| + half the step of BF16 at w (where w and w + e
+lie on two sides of a power of two, y is that power at most that far).  What |y - w| has beyond that half step is held to
+2^-14 of the norm of w.  Where that comes from: every operand is held in 22 bits and sums in FP32; the same scheme on the CPU
+is off by 5 10^-7 with exact sums and by up to 2.3 10^-6 (five steps) and 5 10^-6 (ten) with FP32 ones on the matrices
+below, and a factor of twelve is left for the order of the sums."""
+
+import pytest
+import torch
+
+import fp8_blockwise_quantized_amd as fq
+from parity import say
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+MUON = (3.4445, -4.7750, 2.0315)
+
+
+def exact(g, coefficients, eps=1e-7):
+    out = []
+    for x in g.to(F64):
+        turned = x.shape[0] > x.shape[1]
+        x = x.t() if turned else x
+        x = x / (x.square().sum().sqrt() + eps)
+        for a, b, c in coefficients:
+            A = x @ x.t()
+            x = a * x + (b * A + c * (A @ A)) @ x
+        out.append(x.t() if turned else x)
+    return torch.stack(out)
+
+
+def hold(got, g, coefficients=(MUON,) * 5, eps=1e-7, bound=2.0 ** -14):
+    torch.cuda.synchronize()
+    for y, w in zip(got.to(F64), exact(g, coefficients, eps)):
+        half_step = torch.ldexp(torch.ones_like(w), torch.frexp(w).exponent - 9)  # w = f 2^e, 1/2 <= f < 1: steps of 2^(e - 8)
+        beyond = ((y - w).abs() - half_step).clamp(min=0.0)
+        off = float(beyond.norm()) / float(w.norm())
+        print("off by", off, flush=True)
+        assert off <= bound
+
+
+def normal(*shape, seed=1):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def orthogonal_rows(m, n):
+    """Equal singular values."""
+    return torch.linalg.qr(normal(n, m, seed=m).to(F64))[0].t().to(F32).unsqueeze(0)
+
+
+def low_rank(m, n, r):
+    u = normal(1, m, r, seed=2) / torch.arange(1, r + 1, device="cuda").sqrt()
+    v = normal(1, n, r, seed=3)
+    return (u.unsqueeze(2) * v.unsqueeze(1)).sum(3) + 0.2 * normal(1, m, n, seed=4)
+
+
+MATRICES = {
+    "random": [normal, (1, 256, 2048), (1, 64, 1024), (1, 32, 1024), (3, 32, 32), (2, 64, 64), (4, 64, 256), (5, 8, 8), (7, 2, 3),
+               (1, 512, 384), (1, 1000, 700), (1, 300, 5000), (2, 1408, 1100)],
+    "equal": [orthogonal_rows, (400, 1024), (4, 1024), (130, 130), (1, 33)],
+    "low": [low_rank, (512, 384, 32), (700, 2050, 7), (96, 96, 1)],
+}
+CASES = [(kind, shape) for kind, (_, *shapes) in MATRICES.items() for shape in shapes]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind,shape", CASES, ids=[f"{k}-{'x'.join(map(str, s))}" for k, s in CASES])
+def test_five_steps(kind, shape, dtype):
+    say("ortho accuracy", kind, shape, dtype)
+    g = MATRICES[kind][0](*shape).to(dtype)
+    hold(fq.orthogonalize(g), g)
+    turned = g.transpose(1, 2).contiguous()
+    hold(fq.orthogonalize(turned), turned)
+
+
+@pytest.mark.parametrize("shape", [(512, 384), (40, 100)])
+def test_identity(shape):
+    say("ortho accuracy identity", shape)
+    g = torch.eye(*shape, device="cuda").unsqueeze(0)
+    hold(fq.orthogonalize(g), g)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 10])
+def test_other_numbers_of_steps(steps):
+    say("ortho accuracy steps", steps)
+    for dtype in (F32, BF16):
+        g = normal(1, 256, 1024, seed=5).to(dtype)
+        hold(fq.orthogonalize(g, steps=steps), g, (MUON,) * steps)
