@@ -13,7 +13,8 @@
 // random, low-rank and orthogonal matrices, as FP32 products are, at three times the matrix instructions.  A BF16 input fits
 // the first half, so the first step has one term in A and two in the update.
 //
-// Scaling.  Halves hold 6 10^-8 .. 65504; X is held as 2^12 X, A and the polynomial as 2^10 A.  The first X is G times a
+// Scaling.  Halves hold 6 10^-8 .. 65504; X is held as 2^12 X, A and the polynomial as 2^8 A: an entry of A may be the
+// square of a singular value, so that singular values up to 15.99 fit both.  The first X is G times a
 // power of two (exact), the rest of the normalization (a factor in 1 .. 2) enters the first step's epilogues.
 //
 // Layout.  X (rows along n) serves A's product, X^T (rows along m) the update's: X^T_new = X^T P is a product
@@ -37,7 +38,7 @@ namespace fp8bq {
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
-constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f;
+constexpr float kScaleX = 4096.0f, kScaleA = 256.0f;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const f32x2_t v = {lo, hi};

@@ -88,3 +88,23 @@ def test_other_numbers_of_steps(steps):
     for dtype in (F32, BF16):
         g = normal(1, 256, 1024, seed=5).to(dtype)
         hold(fq.orthogonalize(g, steps=steps), g, (MUON,) * steps)
+
+
+STRONG = [((10.0, 0.0, 0.0), (0.1, 0.0, 0.0)),                     # the singular value goes to 10 and back to 1
+          ((15.0, 0.0, 0.0), (0.05, 0.0, 0.0), (1.5, -0.5, 0.0)),
+          ((14.0, 0.0, 0.0), (0.25, 0.9, 0.001)),                  # a polynomial of 215 at 14
+          ((0.5, -16.25, 0.0), (0.06, 0.0, 0.0))]                  # and one below zero, the value at -15.75
+
+
+@pytest.mark.parametrize("coefficients", STRONG)
+@pytest.mark.parametrize("shape", [(1, 1), (1, 40), (40, 1), (50, 70), (300, 128)])
+def test_up_to_the_stated_limits(shape, coefficients):
+    """Singular values up to 15 and polynomials up to 215, where one row has all of the norm, so that a single entry of A is
+    the largest singular value's square and one of X may be that value."""
+    say("ortho limits", shape, coefficients)
+    g = torch.zeros(1, *shape, device="cuda")
+    g[0, shape[0] // 2] = normal(shape[1], seed=7)
+    hold(fq.orthogonalize(g, steps=len(coefficients), coefficients=list(coefficients)), g, coefficients)
+    g = torch.zeros(1, *shape, device="cuda")
+    g[0, shape[0] // 2, shape[1] // 3] = 3.0
+    hold(fq.orthogonalize(g, steps=len(coefficients), coefficients=list(coefficients)), g, coefficients)
