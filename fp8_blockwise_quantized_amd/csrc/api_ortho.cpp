@@ -9,6 +9,8 @@
 
 using namespace fp8bq;
 
+static_assert(FP8BQ_MAX_ORTHO_STEPS == kMaxOrthoSteps, "steps of a call");
+
 static int cus_or_default() {
   int cus = 0;
   return current_device(&cus) == kOk && cus > 0 ? cus : 256;

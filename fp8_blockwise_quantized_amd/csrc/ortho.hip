@@ -14,8 +14,10 @@
 // the first half, so the first step has one term in A and two in the update.
 //
 // Scaling.  Halves hold 6 10^-8 .. 65504; X is held as 2^12 X, A and the polynomial as 2^8 A: an entry of A may be the
-// square of a singular value, so that singular values up to 15.99 fit both.  The first X is G times a
-// power of two (exact), the rest of the normalization (a factor in 1 .. 2) enters the first step's epilogues.
+// square of a singular value, so that singular values up to 15.99 fit both.  What is held is X / u, where the unit u of
+// each matrix and step is known from |G|, eps and the coefficients alone (ortho_factors): the first X is G times the power
+// of two that brings its own norm to 1/2 .. 1 (exact), and while X can be at most S < 1, it is held in units of the power of
+// two above S.  So a G far below eps, whose X is tiny, keeps its bits; from S = 1 on the unit is one.
 //
 // Layout.  X (rows along n) serves A's product, X^T (rows along m) the update's: X^T_new = X^T P is a product
 // of rows again.  The update writes both: a patch of accumulators is transposed in registers, eight lanes exchanging
@@ -104,7 +106,30 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(const TIn* __restrict__
   if (threadIdx.x == 0) parts[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// The first X in both layouts, from tiles of 64 x 64 of G; factor[batch].  tall: G is X^T.
+// The coefficients' magnitudes, from which the units are found.
+struct OrthoSteps {
+  int steps;
+  float a[kMaxOrthoSteps], b[kMaxOrthoSteps], c[kMaxOrthoSteps];
+};
+// What a matrix's epilogues multiply with: of step k factor[2 k] for A (u_k^2) and factor[2 k + 1] for the update (u_k / u_k+1;
+// in the last step u_k, as the result is in units of one).  norm = |G|; u_0 = 2^ex / (norm + eps).
+__device__ __forceinline__ void ortho_factors(const OrthoSteps& s, double norm, int ex, double eps, float* factor) {
+  double u = norm > 0.0 ? __builtin_ldexp(1.0, ex) / (norm + eps) : 1.0;
+  double most = norm / (norm + eps);  // no singular value of X is larger (nor its norm)
+  for (int k = 0; k < s.steps; ++k) {
+    const double q = most * most;
+    most *= (double)s.a[k] + q * ((double)s.b[k] + q * (double)s.c[k]);
+    most = most < 16.0 ? most : 16.0;
+    const double above = __builtin_ldexp(1.0, __builtin_amdgcn_frexp_exp(most));
+    // (2^-120: quotients of units stay finite, and a smaller result is zero in BF16)
+    const double next = k == s.steps - 1 || !(most > 0.0) || above > 1.0 ? 1.0 : above < 0x1p-120 ? 0x1p-120 : above;
+    factor[2 * k] = (float)(u * u);
+    factor[2 * k + 1] = (float)(u / next);
+    u = next;
+  }
+}
+
+// The first X in both layouts, from tiles of 64 x 64 of G, and the factors.  tall: G is X^T.
 struct OrthoBuffers {
   uint16_t *x, *x_low;    // [batch][m][np] first and second halves (second: FP32 input; BF16 fits the first)
   uint16_t *xt, *xt_low;  // [batch][n][mp]
@@ -113,7 +138,8 @@ struct OrthoBuffers {
 template <typename TIn>
 __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict__ g, int64_t R, int64_t C, int64_t ldg,
                                                           int64_t bstride, const double* __restrict__ parts, int nparts,
-                                                          double eps, OrthoBuffers b, int tall, int wide, float* __restrict__ factor) {
+                                                          double eps, OrthoBuffers b, int tall, int wide, OrthoSteps steps,
+                                                          float* __restrict__ factor) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
   __shared__ __attribute__((aligned(16))) uint16_t low[sizeof(TIn) == 4 ? 64 : 1][72];
   const int t = threadIdx.x, batch = blockIdx.z;
@@ -141,12 +167,18 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
   for (int i = t & 63; i < nparts; i += 64) sum += parts[(int64_t)batch * nparts + i];
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
-  const double norm = __builtin_sqrt(sum) + eps;
+  const double norm = __builtin_sqrt(sum);
   const bool finite = norm < __builtin_inf();
-  // norm = fr 2^ex, 1/2 <= fr < 1: X 2^12 = (G 2^(12 - ex)) / fr
+  // norm = fr 2^ex, 1/2 <= fr < 1: held is G 2^(12 - ex)
   const int ex = finite ? __builtin_amdgcn_frexp_exp(norm) : 0;
-  if (t == 0 && blockIdx.x == 0 && blockIdx.y == 0)
-    factor[batch] = finite ? (float)(1.0 / __builtin_amdgcn_frexp_mant(norm)) : __builtin_nanf("");
+  if (t == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
+    float* f = factor + (int64_t)batch * (2 * kMaxOrthoSteps);
+    if (finite) {
+      ortho_factors(steps, norm, ex, eps, f);
+    } else {
+      for (int k = 0; k < 2 * steps.steps; ++k) f[k] = __builtin_nanf("");
+    }
+  }
   // (buffers are padded to whole tiles of 64 along their rows; rows past the matrix are not there)
   // straight: rows of G; turned: its columns
   const int64_t of_x = (int64_t)batch * b.m * b.np, of_xt = (int64_t)batch * b.n * b.mp;
@@ -197,7 +229,7 @@ __global__ __launch_bounds__(256) void ortho_begin_kernel(const TIn* __restrict_
 enum OrthoStep : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2, kOrthoLast = 3, kOrthoLastWide = 4 };
 struct OrthoEnd {
   float a, b, c;          // the step's coefficients
-  const float* factor;    // of the first step's X (null: 1)
+  const float* factor;    // Gram, update: the step's factor of the first matrix
   const uint16_t *old, *old_low;  // polynomial: A; update: X^T as it was (second halves null: zeros)
   uint16_t *to, *to_low;          // Gram, polynomial: [batch][m][mp]; update: X^T
   uint16_t *x, *x_low;            // update: X
@@ -296,7 +328,7 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = v[8 * q + i];
     if constexpr (STEP == kOrthoGram) {
-      const float s = f * f * (kScaleA / (kScaleX * kScaleX));
+      const float s = f * (kScaleA / (kScaleX * kScaleX));
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] *= s;
     } else if constexpr (STEP == kOrthoPoly) {
@@ -361,7 +393,7 @@ __device__ __forceinline__ void ortho_patch(const OrthoEnd& e, const v16f& v, co
 template <int STEP, int MI, int NI>
 __device__ __forceinline__ void ortho_patches(const OrthoEnd& e, const v16f (&v)[MI][NI], const RowPlace& p) {
   constexpr int P = MI * NI, kAhead = 2;
-  const float f = e.factor ? e.factor[p.batch] : 1.0f;
+  const float f = STEP == kOrthoPoly ? 1.0f : e.factor[p.batch * (2 * kMaxOrthoSteps)];
   OrthoOld old[kAhead + 1];
 #pragma unroll
   for (int u = 0; u < (P < kAhead ? P : kAhead); ++u) ortho_load<STEP>(e, p, p.m + 32 * (u / NI), p.n + 32 * (u % NI), old[u]);
@@ -519,17 +551,24 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
 
   const dim3 ngrid((unsigned)p.norm_blocks, (unsigned)B);
   const dim3 bgrid((unsigned)((p.C + 63) / 64), (unsigned)((p.R + 63) / 64), (unsigned)B);
+  OrthoSteps how{};
+  how.steps = steps;
+  for (int k = 0; k < steps; ++k) {
+    how.a[k] = (float)std::fabs(coef[3 * k]);
+    how.b[k] = (float)std::fabs(coef[3 * k + 1]);
+    how.c[k] = (float)std::fabs(coef[3 * k + 2]);
+  }
   const OrthoBuffers b{x, x_low, xt[0], xt[0] + to_low_xt, p.m, p.n, p.mp, p.np};
   if (gt == 0) {
     hipLaunchKernelGGL(ortho_norm_kernel<uint16_t>, ngrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, wide, norms);
     FP8BQ_TRY(hipGetLastError());
     hipLaunchKernelGGL(ortho_begin_kernel<uint16_t>, bgrid, dim3(256), 0, st, (const uint16_t*)g, p.R, p.C, ldg, gbatch, norms,
-                       p.norm_blocks, eps, b, (int)tall, wide, factor);
+                       p.norm_blocks, eps, b, (int)tall, wide, how, factor);
   } else {
     hipLaunchKernelGGL(ortho_norm_kernel<float>, ngrid, dim3(256), 0, st, (const float*)g, p.R, p.C, ldg, gbatch, wide, norms);
     FP8BQ_TRY(hipGetLastError());
     hipLaunchKernelGGL(ortho_begin_kernel<float>, bgrid, dim3(256), 0, st, (const float*)g, p.R, p.C, ldg, gbatch, norms,
-                       p.norm_blocks, eps, b, (int)tall, wide, factor);
+                       p.norm_blocks, eps, b, (int)tall, wide, how, factor);
   }
   FP8BQ_TRY(hipGetLastError());
 
@@ -539,7 +578,7 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     e.a = (float)coef[3 * k];
     e.b = (float)coef[3 * k + 1];
     e.c = (float)coef[3 * k + 2];
-    e.factor = first ? factor : nullptr;
+    e.factor = factor + 2 * k;
     const bool low = !(first && gt == 0);  // X has second halves
     e.x = x;
     e.x_low = x_low;
@@ -562,7 +601,6 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     e.to = gram;
     e.to_low = gram + to_low_sym;
     FP8BQ_TRY(launch_product<kOrthoGram>(d, e, p.gram, B, parts, st));
-    e.factor = nullptr;
     d.a = d.b = (const uint8_t*)gram;  // P
     d.lda = d.ldb = 2 * p.mp;
     d.K = 2 * p.mp;
@@ -574,7 +612,7 @@ hipError_t launch_ortho(const void* g, int gt, int64_t ldg, int64_t gbatch, cons
     e.to = poly;
     e.to_low = poly + to_low_sym;
     FP8BQ_TRY(launch_product<kOrthoPoly>(d, e, p.poly, B, parts, st));
-    e.factor = first ? factor : nullptr;
+    e.factor = factor + 2 * k + 1;
     d.a = (const uint8_t*)xt[k & 1];  // X^T P
     d.lda = 2 * p.mp;
     d.b = (const uint8_t*)poly;

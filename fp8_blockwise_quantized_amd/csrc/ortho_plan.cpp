@@ -75,7 +75,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t R, int64_t C, int cu_count, bool* fi
   };
   const double b = (double)batch, m = (double)p.m, n = (double)p.n, mp = (double)p.mp, np = (double)p.np;
   p.at_norms = take(b * p.norm_blocks * 8.0);
-  p.at_factor = take(b * 4.0);
+  p.at_factor = take(b * kMaxOrthoSteps * 8.0);
   p.at_x = take(b * m * np * 2.0);
   p.at_xt[0] = take(b * n * mp * 4.0);
   p.at_xt[1] = take(b * n * mp * 4.0);

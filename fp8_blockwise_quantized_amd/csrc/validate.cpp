@@ -768,7 +768,7 @@ int validate_ortho(const OrthoCheck& c, bool* empty) {
   *empty = false;
   if (in_esize(c.gt) == 0) return kErrDtype;
   if (c.B < 0 || c.R < 0 || c.C < 0 || c.B > kMaxOrthoBatch || c.R > kMaxOrthoSide || c.C > kMaxOrthoSide) return kErrShape;
-  if (c.steps < 1 || c.steps > 64 || !(c.eps > 0.0) || !(c.eps - c.eps == 0.0)) return kErrValue;
+  if (c.steps < 1 || c.steps > kMaxOrthoSteps || !(c.eps > 0.0) || !(c.eps - c.eps == 0.0)) return kErrValue;
   if (c.coef == nullptr) return kErrNull;
   for (int i = 0; i < 3 * c.steps; ++i)
     if (!(c.coef[i] - c.coef[i] == 0.0)) return kErrValue;

@@ -8,7 +8,7 @@
  *
  * Accuracy.  X, A and the polynomial are held in 22 bits, and their products taken of these, sums in FP32: the result is off
  * by 2^-14 of its norm or less besides its own rounding to BF16, for matrices of full and of low rank, of equal singular
- * values and of a few rows alike (up to ten steps of 3.4445, -4.7750, 2.0315).
+ * values and of a few rows alike, and however far |G| is below eps (up to twelve steps of 3.4445, -4.7750, 2.0315).
  * Until the last step singular values have to stay below 15.9, and in every step those of the polynomial b A + c A^2 below
  * 255 (16-bit floats hold no more); past that the result is not finite.  A matrix of zeros gives zeros; one with a NaN or
  * an infinity gives NaN in all of its places and leaves the others of the batch alone.

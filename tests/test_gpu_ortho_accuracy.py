@@ -108,3 +108,37 @@ def test_up_to_the_stated_limits(shape, coefficients):
     g = torch.zeros(1, *shape, device="cuda")
     g[0, shape[0] // 2, shape[1] // 3] = 3.0
     hold(fq.orthogonalize(g, steps=len(coefficients), coefficients=list(coefficients)), g, coefficients)
+
+
+@pytest.mark.parametrize("steps", [1, 5, 12])
+@pytest.mark.parametrize("size", [1e-9, 1e-12, 1e-17, 1e-18, 1e-20, 1e-30])
+def test_norms_far_below_eps(size, steps):
+    """X = G / (|G| + eps) is then tiny, and the steps take it up again by about 3.44 each, to one after enough of them."""
+    say("ortho small", size, steps)
+    for dtype in (F32, BF16):
+        g = (normal(4, 128, 256, seed=9) * size).to(dtype)
+        g[1] *= 1e-6
+        g[2] = 0.0
+        g[3] = normal(128, 256, seed=10)
+        y = fq.orthogonalize(g, steps=steps)
+        assert not y[2].any() and bool((y[[0, 1, 3]] != 0).any(2).all())
+        near_all = g[[0, 1, 3]]
+        hold(y[[0, 1, 3]], near_all, (MUON,) * steps)
+        wide = (normal(1, 1000, 700, seed=11) * size).to(dtype)
+        hold(fq.orthogonalize(wide, steps=steps), wide, (MUON,) * steps)
+
+
+@pytest.mark.parametrize("eps", [1e-3, 1.0, 1e4, 1e30])
+def test_large_eps(eps):
+    say("ortho eps", eps)
+    each = [(3.0, -3.2, 1.2), (0.01, 0.0, 0.0), (20.0, -5.0, 7.0), (3.4445, -4.7750, 2.0315)]
+    g = normal(1, 90, 333, seed=12)
+    hold(fq.orthogonalize(g, steps=4, coefficients=each, eps=eps), g, each, eps)
+
+
+def test_steps_that_leave_nothing():
+    say("ortho nothing")
+    g = normal(2, 70, 80, seed=13)
+    for first in ((0.0, 0.0, 0.0), (1e-300, 0.0, 0.0)):
+        y = fq.orthogonalize(g, steps=3, coefficients=[first, MUON, MUON])
+        assert not y.any()
