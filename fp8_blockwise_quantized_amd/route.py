@@ -247,6 +247,7 @@ def combine_rows_backward(dout, y, rows, weights, slots):
     dev = dout.get_device()
     args = _combine_backward(dout, y, rows, weights, slots, dev)
     at = stream(dev)
-    dy, dweights = y.new_empty(y.shape), weights.new_empty(weights.shape)
+    # (the call writes nothing where the rows have no elements)
+    dy, dweights = y.new_empty(y.shape), weights.new_empty(weights.shape) if y.shape[1] else weights.new_zeros(weights.shape)
     _call("fp8bq_combine_rows_backward", *args, dy.data_ptr(), y.shape[1], dweights.data_ptr(), at)
     return dy, dweights

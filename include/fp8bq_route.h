@@ -12,7 +12,8 @@
  * Conventions, errors and stream order as in fp8bq.h.  experts, rows, slots, weights, bias and offsets are contiguous;
  * their addresses are multiples of their element's size.  Logits may have any leading dimension and their element's
  * alignment.  Inputs need not be finite here.  1 <= E <= FP8BQ_MAX_EXPERTS, 1 <= k <= FP8BQ_MAX_CHOICES and T k < 2^31.
- * T == 0 (or H == 0) is a successful no-op, except that fp8bq_expert_rows then writes offsets of zero.
+ * T == 0 (or H == 0) is a successful no-op, except that fp8bq_expert_rows then writes offsets of zero.  (So dweights of
+ * rows without elements, whose sums are zero, are the caller's to clear.)
  * Everything is deterministic: sums run in a fixed order, ties go to the lowest index.
  */
 #ifndef FP8BQ_ROUTE_H_
