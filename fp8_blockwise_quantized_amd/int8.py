@@ -166,9 +166,14 @@ def fp8bq_grouped_linear_int8(x, offsets, qw, sw, y, ws=None):
     return E, T, N, K, op, xp, _in(x), ldx, qwp, ldqw, swp, yp, _out(y), ldy, wsp, wsb, stream(dev)
 
 
+def _scales(x, n, elements):
+    """n scales to be written; the calls write none over no elements, where the rule's is the smallest one."""
+    return x.new_empty(n, dtype=torch.float32) if elements else x.new_full((n,), 1e-12, dtype=torch.float32)
+
+
 def quantize_int8(x):
     R, C = x.shape
-    q, s = x.new_empty((R, C), dtype=torch.int8), x.new_empty(R, dtype=torch.float32)
+    q, s = x.new_empty((R, C), dtype=torch.int8), _scales(x, R, C)
     fp8bq_quantize_int8(x, q, s)
     return q, s
 
@@ -176,7 +181,7 @@ def quantize_int8(x):
 @on_its_device
 def quantize_int8_t(x):
     R, C = x.shape
-    qt, st = x.new_empty((C, _padded(R)), dtype=torch.int8), x.new_empty(C, dtype=torch.float32)
+    qt, st = x.new_empty((C, _padded(R)), dtype=torch.int8), _scales(x, C, R)
     fp8bq_quantize_int8_t.__wrapped__(x, qt, st, _space("fp8bq_quantize_int8_t_workspace_size", x, R, C))
     return qt, st
 

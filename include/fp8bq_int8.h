@@ -14,7 +14,8 @@
  * Layouts.  Codes [R, K] bytes, row stride a multiple of 16; K % 16 == 0.  Scales [R] FP32, contiguous.  Output
  * matrices may have any leading dimension >= N.  Conventions, alignment, errors and stream order as in fp8bq.h (inputs
  * need not be finite here); R and C of the quantizers, M and N are below 2^30, and 255 times the leading dimension of
- * codes plus K is below 2^31.
+ * codes plus K is below 2^31.  The quantizers are no-ops without rows or without columns: scales over no elements, by the
+ * rule 1e-12, are the caller's to set.
  */
 #ifndef FP8BQ_INT8_H_
 #define FP8BQ_INT8_H_
