@@ -129,14 +129,16 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 
 
 def on_its_device(fn):
-    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that."""
+    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that.  Where all
+    arguments are named any tensor of them tells the device (tensors of two devices are refused)."""
 
     @functools.wraps(fn)
-    def call(first, *args, **kwargs):
+    def call(*args, **kwargs):
+        first = args[0] if args else next((v for v in kwargs.values() if isinstance(v, torch.Tensor)), None)
         if not isinstance(first, torch.Tensor) or not first.is_cuda or first.get_device() == _current_device():
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
         with torch.cuda.device(first.get_device()):
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
 
     return call
 
