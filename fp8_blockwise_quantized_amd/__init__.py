@@ -279,7 +279,7 @@ def prepare(fn, *args, **kwargs):
         if st != 0:
             raise Fp8bqError(st, name)
 
-    return launch
+    return fn.prepared(launch, args, kwargs) if hasattr(fn, "prepared") else launch
 
 
 @_entry

@@ -128,18 +128,31 @@ def batch(t, name, shape, dtypes, device):
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+def _device_of(args, kwargs):
+    """Index of the device of a call's first tensor, or of any where all arguments are named (tensors of two devices are
+    refused); None without one."""
+    first = args[0] if args else next((v for v in kwargs.values() if isinstance(v, torch.Tensor)), None)
+    return first.get_device() if isinstance(first, torch.Tensor) and first.is_cuda else None
+
+
 def on_its_device(fn):
-    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that.  Where all
-    arguments are named any tensor of them tells the device (tensors of two devices are refused)."""
+    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that."""
+
+    def on(device, fn, args, kwargs):
+        if device is None or device == _current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(device):
+            return fn(*args, **kwargs)
 
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        first = args[0] if args else next((v for v in kwargs.values() if isinstance(v, torch.Tensor)), None)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda or first.get_device() == _current_device():
-            return fn(*args, **kwargs)
-        with torch.cuda.device(first.get_device()):
-            return fn(*args, **kwargs)
+        return on(_device_of(args, kwargs), fn, args, kwargs)
 
+    def prepared(launch, args, kwargs):
+        device = _device_of(args, kwargs)
+        return lambda: on(device, launch, (), {})
+
+    call.prepared = prepared  # (what prepare() makes of a launch of this call)
     return call
 
 
