@@ -138,19 +138,25 @@ def _device_of(args, kwargs):
 def on_its_device(fn):
     """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that."""
 
-    def on(device, fn, args, kwargs):
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        device = _device_of(args, kwargs)
         if device is None or device == _current_device():
             return fn(*args, **kwargs)
         with torch.cuda.device(device):
             return fn(*args, **kwargs)
 
-    @functools.wraps(fn)
-    def call(*args, **kwargs):
-        return on(_device_of(args, kwargs), fn, args, kwargs)
-
     def prepared(launch, args, kwargs):
         device = _device_of(args, kwargs)
-        return lambda: on(device, launch, (), {})
+
+        def there():
+            if device == _current_device():
+                launch()
+            else:
+                with torch.cuda.device(device):
+                    launch()
+
+        return there
 
     call.prepared = prepared  # (what prepare() makes of a launch of this call)
     return call
