@@ -680,7 +680,7 @@ static int check_route(const RouteCheck& g, bool* empty) {
   if (g.score != 0 && g.score != 1) return kErrValue;
   if (!(g.scale - g.scale == 0.0)) return kErrValue;  // (NaN, infinities)
   if (g.T < 0 || g.E < 1 || g.E > kMaxGroupExperts || g.k < 1 || g.k > kMaxChoices || g.k > g.E) return kErrShape;
-  if (g.T >= ((int64_t)1 << 31) / g.k) return kErrShape;
+  if (g.T > (((int64_t)1 << 31) - 1) / g.k) return kErrShape;
   if (g.groups < 1 || g.groups > kMaxExpertGroups || g.E % g.groups != 0) return kErrShape;
   const int64_t per = g.E / g.groups;
   if (g.top_groups < 1 || g.top_groups > g.groups || g.k > g.top_groups * per) return kErrShape;
@@ -731,7 +731,8 @@ int validate_rows(const RowsCheck& g, int inputs, int vectors, bool* empty) {
   if (in_esize(g.out_type) == 0) return kErrDtype;
   for (int i = 0; i < inputs; ++i)
     if (in_esize(g.type[i]) == 0) return kErrDtype;
-  if (g.T < 0 || g.H < 0 || g.H % 8 != 0 || g.k < 1 || g.k > kMaxChoices || g.T >= ((int64_t)1 << 31) / g.k) return kErrShape;
+  if (g.T < 0 || g.H < 0 || g.H % 8 != 0 || g.k < 1 || g.k > kMaxChoices || g.T > (((int64_t)1 << 31) - 1) / g.k)
+    return kErrShape;
   if (g.T == 0 || g.H == 0) {
     *empty = true;
     return kOk;
