@@ -128,26 +128,24 @@ def batch(t, name, shape, dtypes, device):
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _device_of(args, kwargs):
-    """Index of the device of a call's first tensor, or of any where all arguments are named (tensors of two devices are
-    refused); None without one."""
-    first = args[0] if args else next((v for v in kwargs.values() if isinstance(v, torch.Tensor)), None)
-    return first.get_device() if isinstance(first, torch.Tensor) and first.is_cuda else None
+def _any_tensor(kwargs):
+    return next((v for v in kwargs.values() if isinstance(v, torch.Tensor)), None)
 
 
 def on_its_device(fn):
-    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that."""
+    """fn(tensor, ...) with the tensor's device as the current one: plans, workspace sizes and launches go by that.  Where all
+    arguments are named any tensor of them tells the device (tensors of two devices are refused)."""
 
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        device = _device_of(args, kwargs)
-        if device is None or device == _current_device():
+        first = args[0] if args else _any_tensor(kwargs)
+        if not isinstance(first, torch.Tensor) or not first.is_cuda or first.get_device() == _current_device():
             return fn(*args, **kwargs)
-        with torch.cuda.device(device):
+        with torch.cuda.device(first.get_device()):
             return fn(*args, **kwargs)
 
     def prepared(launch, args, kwargs):
-        device = _device_of(args, kwargs)
+        device = (args[0] if args else _any_tensor(kwargs)).get_device()
 
         def there():
             if device == _current_device():
