@@ -14,7 +14,8 @@
  * an infinity gives NaN in all of its places and leaves the others of the batch alone.
  *
  * Conventions, errors and stream order as in fp8bq.h, except that g and out need their element's alignment only and may
- * have any leading dimension >= C and any batch stride that keeps the matrices apart.  Deterministic.
+ * have any leading dimension >= C and any batch stride from (R - 1) ld + C on: one matrix behind the other, not between its
+ * rows.  Deterministic.
  */
 #ifndef FP8BQ_ORTHO_H_
 #define FP8BQ_ORTHO_H_
